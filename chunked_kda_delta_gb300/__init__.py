@@ -16,10 +16,21 @@ from .kda import (  # noqa: F401
     kda_plan,
     kda_plan_varlen,
     kda_decode,
+    kda_decode_paged,
     STATE_F32,
     STATE_BF16,
     load_library,
     MODE_SERIAL,
     MODE_SEGMENT,
     MODE_AUTO,
+)
+from .serving import (  # noqa: F401
+    kda_pages_alloc,
+    kda_pages_free,
+    kda_pages_fork,
+    kda_pages_compact,
+    kda_pages_copy,
+    kda_kvcache_append,
+    kda_kvcache_attention,
+    kda_beam_select,
 )

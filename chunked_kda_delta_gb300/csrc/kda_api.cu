@@ -20,11 +20,19 @@
 #include <vector>
 
 #include "../../include/kda.h"
+#include "kda_host.cuh"
 #include "kda_internal.cuh"
 
-namespace {
+using namespace kda::host;
 
+namespace {
 thread_local char t_last_error[512] = "";
+}  // namespace
+
+namespace kda {
+namespace host {
+
+void clear_error() { t_last_error[0] = '\0'; }
 
 kda_status fail(kda_status st, const char* fmt, ...) {
     va_list ap;
@@ -38,22 +46,26 @@ kda_status cuda_fail(cudaError_t e, const char* what) {
     return fail(KDA_ERR_CUDA, "%s failed: %s", what, cudaGetErrorString(e));
 }
 
+}  // namespace host
+}  // namespace kda
+
+namespace {
+
 __device__ int32_t g_status_word = 0;
 
 constexpr int kMaxDevices = 64;
 constexpr int64_t kDefaultWaitLimit = 1ll << 22;
 constexpr size_t kMaxWorkspaces = 8;
+constexpr size_t kMaxServingWorkspaces = 32;  // streams with their own serving scratch
 constexpr int kMaxHostPieces = 64;  // pieces kda_prefill_host may stream a call in
-
-struct DeviceInfo {
-    bool ready = false;
-    int cc_major = 0, cc_minor = 0, sm_count = 0;
-    int resident_clusters = 0;  // co-resident 2-CTA clusters of the fused kernel
-    int32_t* status = nullptr;
-};
 
 std::mutex g_mutex;
 DeviceInfo g_devices[kMaxDevices];
+
+}  // namespace
+
+namespace kda {
+namespace host {
 
 kda_status device_info(int dev, DeviceInfo** out) {
     if (dev < 0 || dev >= kMaxDevices) return fail(KDA_ERR_UNSUPPORTED_DEVICE, "device %d", dev);
@@ -106,11 +118,21 @@ kda_status device_info(int dev, DeviceInfo** out) {
     return KDA_OK;
 }
 
+kda_status current_device(int* dev, DeviceInfo** out) {
+    const cudaError_t e = cudaGetDevice(dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    return device_info(*dev, out);
+}
+
+}  // namespace host
+}  // namespace kda
+
+namespace {
+
 // ---------------------------------------------------------------------------
 // Workspaces: one device buffer per (device, stream), grown on demand, at most
-// kMaxWorkspaces alive (least recently used evicted).
-enum WorkspaceKind { kWsSegment = 0, kWsHostArena = 1 };
-
+// kMaxWorkspaces alive (least recently used evicted).  Serving scratch counts by itself, up
+// to kMaxServingWorkspaces.
 struct Workspace {
     int device;
     void* stream;
@@ -120,7 +142,13 @@ struct Workspace {
     unsigned long long last_use;
 };
 std::vector<Workspace> g_workspaces;
+std::vector<Workspace> g_retired;  // outgrown serving scratch: captured graphs may still use it
 unsigned long long g_use_clock = 0;
+
+}  // namespace
+
+namespace kda {
+namespace host {
 
 kda_status get_workspace(int dev, cudaStream_t stream, int kind, size_t bytes, void** out) {
     *out = nullptr;
@@ -141,15 +169,27 @@ kda_status get_workspace(int dev, cudaStream_t stream, int kind, size_t bytes, v
     for (size_t i = 0; i < g_workspaces.size(); ++i)
         if (g_workspaces[i].device == dev && g_workspaces[i].stream == (void*)stream &&
             g_workspaces[i].kind == kind) {
-            cudaStreamSynchronize(stream);
-            cudaFree(g_workspaces[i].ptr);
+            if (kind == kWsServing) {
+                g_retired.push_back(g_workspaces[i]);
+            } else {
+                cudaStreamSynchronize(stream);
+                cudaFree(g_workspaces[i].ptr);
+            }
             g_workspaces.erase(g_workspaces.begin() + i);
             break;
         }
-    if (g_workspaces.size() >= kMaxWorkspaces) {
-        size_t lru = 0;
-        for (size_t i = 1; i < g_workspaces.size(); ++i)
-            if (g_workspaces[i].last_use < g_workspaces[lru].last_use) lru = i;
+    const bool serving = kind == kWsServing;
+    size_t alive = 0, lru = 0;
+    unsigned long long oldest = ~0ull;
+    for (size_t i = 0; i < g_workspaces.size(); ++i)
+        if ((g_workspaces[i].kind == kWsServing) == serving) {
+            ++alive;
+            if (g_workspaces[i].last_use < oldest) {
+                oldest = g_workspaces[i].last_use;
+                lru = i;
+            }
+        }
+    if (alive >= (serving ? kMaxServingWorkspaces : kMaxWorkspaces)) {
         int cur;
         cudaGetDevice(&cur);
         cudaSetDevice(g_workspaces[lru].device);
@@ -169,6 +209,11 @@ kda_status get_workspace(int dev, cudaStream_t stream, int kind, size_t bytes, v
     *out = p;
     return KDA_OK;
 }
+
+}  // namespace host
+}  // namespace kda
+
+namespace {
 
 // ---------------------------------------------------------------------------
 // TMA descriptors.  cuTensorMapEncodeTiled is reached through the runtime's
@@ -211,19 +256,6 @@ kda_status encode_chunk_map(CUtensorMap* m, const void* base, CUtensorMapDataTyp
 }
 
 // ---------------------------------------------------------------------------
-struct Range {
-    const void* p;
-    size_t bytes;
-};
-
-bool overlaps(Range a, Range b) {
-    if (!a.p || !b.p || a.bytes == 0 || b.bytes == 0) return false;
-    const uintptr_t a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p;
-    return a0 < b0 + b.bytes && b0 < a0 + a.bytes;
-}
-
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
-
 struct Problem {
     int64_t T_total, dense_len;
     int32_t N, H;        // H: heads of v, g, beta and the states
@@ -1108,6 +1140,71 @@ kda_status kda_decode(const kda_shape* shape, const uint16_t* q, const uint16_t*
     return KDA_OK;
 }
 
+kda_status kda_decode_paged(const kda_shape* shape, const uint16_t* q, const uint16_t* k,
+                            const uint16_t* v, const float* g, const uint16_t* beta, float scale,
+                            void* states, int32_t pages, int64_t page_stride,
+                            const int32_t* state_pages, int32_t state_dtype, uint16_t* out,
+                            void* stream) {
+    t_last_error[0] = '\0';
+    Problem pr{};
+    kda_status st = validate_shape(shape, false, &pr);
+    if (st != KDA_OK) return st;
+    if (state_dtype != KDA_STATE_F32 && state_dtype != KDA_STATE_BF16)
+        return fail(KDA_ERR_INVALID_ARGUMENT, "unknown state_dtype %d", state_dtype);
+    const size_t elem = state_dtype == KDA_STATE_BF16 ? 2 : 4;
+    if ((st = validate_pointers(pr, q, k, v, g, beta, scale, nullptr, nullptr, out, nullptr, elem)) !=
+        KDA_OK)
+        return st;
+    // The query heads of a group each run their state head's chain, so one of them would
+    // overwrite the state that another still has to read.
+    if (pr.Hq > pr.H)
+        return fail(KDA_ERR_INVALID_ARGUMENT, "num_q_heads (%d) above num_heads (%d) is not supported in place", pr.Hq, pr.H);
+    const int64_t page_elems = (int64_t)pr.H * kda::kD * kda::kD;
+    if (!state_pages || !aligned(state_pages, 4))
+        return fail(KDA_ERR_INVALID_ARGUMENT, "state_pages must be a 4-byte aligned pointer");
+    if (pages < 0 || (pages > 0 && (!states || !aligned(states, 16))))
+        return fail(KDA_ERR_INVALID_ARGUMENT, "states must be a 16-byte aligned pool of pages >= 0");
+    if (page_stride < page_elems || page_stride % 8 != 0 || page_stride > (int64_t)1 << 40)
+        return fail(KDA_ERR_INVALID_ARGUMENT,
+                    "page_stride must be a multiple of 8, at least num_heads * 128 * 128 (got %lld)",
+                    (long long)page_stride);
+    const size_t pool = pages > 0 ? ((size_t)(pages - 1) * page_stride + page_elems) * elem : 0;
+    const Sizes sz = sizes_of(pr, elem);
+    const Range others[] = {{q, sz.q}, {k, sz.k}, {v, sz.v}, {g, sz.g}, {beta, sz.beta}, {out, sz.out},
+                            {state_pages, (size_t)pr.N * 4}};
+    for (const Range& r : others)
+        if (overlaps({states, pool}, r))
+            return fail(KDA_ERR_ALIASING, "states overlaps another argument");
+    if (overlaps({out, sz.out}, {state_pages, (size_t)pr.N * 4}))
+        return fail(KDA_ERR_ALIASING, "out overlaps state_pages");
+    int dev = 0;
+    DeviceInfo* di = nullptr;
+    if ((st = current_device(&dev, &di)) != KDA_OK) return st;
+    if (pr.T_total == 0) return KDA_OK;
+    kda::DecodeParams p{};
+    p.q = reinterpret_cast<const __nv_bfloat16*>(q);
+    p.k = reinterpret_cast<const __nv_bfloat16*>(k);
+    p.v = reinterpret_cast<const __nv_bfloat16*>(v);
+    p.g = g;
+    p.beta = reinterpret_cast<const __nv_bfloat16*>(beta);
+    p.s0 = states;
+    p.sfin = states;
+    p.out = reinterpret_cast<__nv_bfloat16*>(out);
+    p.T = pr.dense_len;
+    p.N = pr.N;
+    p.H = pr.H;
+    p.Hq = pr.Hq;
+    p.scale = scale;
+    p.state_bf16 = state_dtype == KDA_STATE_BF16;
+    p.state_pages = state_pages;
+    p.num_pages = pages;
+    p.page_stride = page_stride;
+    p.status = di->status;
+    const cudaError_t e = kda::launch_decode(p, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "paged decode kernel launch");
+    return KDA_OK;
+}
+
 kda_status kda_get_device_status(void* stream, int32_t* code) {
     t_last_error[0] = '\0';
     if (!code) return fail(KDA_ERR_INVALID_ARGUMENT, "code is NULL");
@@ -1143,6 +1240,16 @@ kda_status kda_release_workspaces(int32_t device) {
             ++i;
         }
     }
+    for (size_t i = 0; i < g_retired.size();) {
+        if (device < 0 || g_retired[i].device == device) {
+            cudaSetDevice(g_retired[i].device);
+            cudaDeviceSynchronize();
+            cudaFree(g_retired[i].ptr);
+            g_retired.erase(g_retired.begin() + i);
+        } else {
+            ++i;
+        }
+    }
     for (size_t i = 0; i < g_pipes.size();) {
         if (device < 0 || g_pipes[i]->device == device) {
             destroy_pipe(*g_pipes[i]);
@@ -1165,6 +1272,8 @@ const char* kda_status_string(kda_status s) {
         case KDA_ERR_CUDA: return "KDA_ERR_CUDA";
         case KDA_ERR_CAPTURE_NEEDS_WARMUP: return "KDA_ERR_CAPTURE_NEEDS_WARMUP";
         case KDA_ERR_DEVICE_TIMEOUT: return "KDA_ERR_DEVICE_TIMEOUT";
+        case KDA_ERR_NO_FREE_PAGE: return "KDA_ERR_NO_FREE_PAGE";
+        case KDA_ERR_NONFINITE: return "KDA_ERR_NONFINITE";
     }
     return "KDA_ERR_UNKNOWN";
 }

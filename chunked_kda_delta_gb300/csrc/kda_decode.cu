@@ -17,6 +17,7 @@
 // CTAs per SM keep 128 KiB of loads in flight.  The reductions over key rows finish in
 // shared memory across the warps.  bf16 state: its own kernel below.
 #include "kda_internal.cuh"
+#include "kda_serving.cuh"
 
 namespace kda {
 namespace {
@@ -31,9 +32,26 @@ __device__ __forceinline__ void state_load(const float* p, float (&x)[4]) {
 __device__ __forceinline__ void state_store(float* p, const float (&x)[4]) {
     __stcs(reinterpret_cast<float4*>(p), make_float4(x[0], x[1], x[2], x[3]));
 }
-// kGrouped: unequal head counts (HeadMap); the equal-count instance keeps plain head
+// Element offset of head hs of sequence n's states in a pool; false for an idle sequence,
+// whose output rows become zero.
+__device__ __forceinline__ bool paged_state(const DecodeParams& p, int64_t n, int hs, size_t& off) {
+    const int32_t page = p.state_pages[n];
+    if (page >= 0 && page < p.num_pages) {
+        off = (size_t)page * p.page_stride + (size_t)hs * kD * kD;
+        return true;
+    }
+    if (page >= 0 && threadIdx.x == 0) report(p.status, kStatusBadIndex);
+    return false;
+}
+__device__ __forceinline__ void idle_output(const DecodeParams& p, int64_t n, int ho, int Ho) {
+    if (threadIdx.x >= kD) return;
+    for (int64_t t = 0; t < p.T; ++t)
+        p.out[(((size_t)n * p.T + t) * Ho + ho) * kD + threadIdx.x] = __float2bfloat16_rn(0.f);
+}
+
+// kPaged: states in a pool, updated in place.  kGrouped: unequal head counts (HeadMap); the equal-count instance keeps plain head
 // indexing (the map's arithmetic costs the bf16 kernel spills at its register cap).
-template <bool kGrouped>
+template <bool kGrouped, bool kPaged>
 __global__ void __launch_bounds__(kDecThreads, 2) kda_decode_kernel(const DecodeParams p) {
     __shared__ float s_k[kD], s_q[kD], s_e[kD], s_v[kD], s_d[kD];
     __shared__ __align__(16) float s_red[2][kDecThreads / 32][kD];
@@ -46,7 +64,9 @@ __global__ void __launch_bounds__(kDecThreads, 2) kda_decode_kernel(const Decode
     const int ho = (int)(blockIdx.x % Ho);
     const HeadMap hm = kGrouped ? head_map(ho, p.H, Hq) : HeadMap{ho, ho, ho, true};
     const int r0 = warp * kDecRows, c0 = lane * 4;
-    const size_t soff = ((size_t)n * p.H + hm.hs) * kD * kD + (size_t)r0 * kD + c0;
+    size_t soff = ((size_t)n * p.H + hm.hs) * kD * kD;
+    if (kPaged && !paged_state(p, n, hm.hs, soff)) return idle_output(p, n, ho, Ho);
+    soff += (size_t)r0 * kD + c0;
 
     float s[kDecRows][4];
     if (p.s0) {
@@ -154,7 +174,7 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <bool kGrouped>
+template <bool kGrouped, bool kPaged>
 __global__ void __launch_bounds__(kDecB16Threads, 3) kda_decode_bf16_kernel(const DecodeParams p) {
     __shared__ float s_k[kD], s_q[kD], s_e[kD], s_v[kD];
     __shared__ __align__(16) float s_d[kD];
@@ -169,7 +189,9 @@ __global__ void __launch_bounds__(kDecB16Threads, 3) kda_decode_bf16_kernel(cons
     const int ho = (int)(blockIdx.x % Ho);
     const HeadMap hm = kGrouped ? head_map(ho, p.H, Hq) : HeadMap{ho, ho, ho, true};
     const int rbase = warp * 32 + hw;  // this thread's rows: rbase + 2 i
-    const size_t soff = ((size_t)n * p.H + hm.hs) * kD * kD + (size_t)rbase * kD + c0;
+    size_t soff = ((size_t)n * p.H + hm.hs) * kD * kD;
+    if (kPaged && !paged_state(p, n, hm.hs, soff)) return idle_output(p, n, ho, Ho);
+    soff += (size_t)rbase * kD + c0;
 
     uint4 s[kDecB16Rows];
     if (p.s0) {
@@ -276,21 +298,29 @@ __global__ void __launch_bounds__(kDecB16Threads, 3) kda_decode_bf16_kernel(cons
 
 }  // namespace
 
+namespace {
+
+template <bool kGrouped, bool kPaged>
+void launch_decode_one(const DecodeParams& p, dim3 grid, cudaStream_t stream) {
+    if (p.state_bf16)
+        kda_decode_bf16_kernel<kGrouped, kPaged><<<grid, dim3(kDecB16Threads), 0, stream>>>(p);
+    else
+        kda_decode_kernel<kGrouped, kPaged><<<grid, dim3(kDecThreads), 0, stream>>>(p);
+}
+
+}  // namespace
+
 cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream) {
     const int64_t rows = (int64_t)p.N * (p.Hq > p.H ? p.Hq : p.H);
     if (rows == 0) return cudaSuccess;
     const dim3 grid((unsigned)rows);
     const bool grouped = p.Hq != p.H;
-    if (p.state_bf16) {
-        if (grouped)
-            kda_decode_bf16_kernel<true><<<grid, dim3(kDecB16Threads), 0, stream>>>(p);
-        else
-            kda_decode_bf16_kernel<false><<<grid, dim3(kDecB16Threads), 0, stream>>>(p);
+    if (p.state_pages) {
+        if (grouped) launch_decode_one<true, true>(p, grid, stream);
+        else launch_decode_one<false, true>(p, grid, stream);
     } else {
-        if (grouped)
-            kda_decode_kernel<true><<<grid, dim3(kDecThreads), 0, stream>>>(p);
-        else
-            kda_decode_kernel<false><<<grid, dim3(kDecThreads), 0, stream>>>(p);
+        if (grouped) launch_decode_one<true, false>(p, grid, stream);
+        else launch_decode_one<false, false>(p, grid, stream);
     }
     return cudaGetLastError();
 }

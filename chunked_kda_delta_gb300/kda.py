@@ -26,13 +26,16 @@ _STATUS = {
     0: "KDA_OK", 1: "KDA_ERR_INVALID_ARGUMENT", 2: "KDA_ERR_ALIASING",
     3: "KDA_ERR_UNSUPPORTED_DEVICE", 4: "KDA_ERR_OUT_OF_MEMORY", 5: "KDA_ERR_CUDA",
     6: "KDA_ERR_CAPTURE_NEEDS_WARMUP", 7: "KDA_ERR_DEVICE_TIMEOUT",
+    8: "KDA_ERR_NO_FREE_PAGE", 9: "KDA_ERR_NONFINITE",
 }
 
 EXPORTED_SYMBOLS = (
     "kda_prefill", "kda_prefill_ex", "kda_prefill_host", "kda_workspace_bytes",
     "kda_get_device_status", "kda_release_workspaces", "kda_status_string",
     "kda_last_error_message", "kda_version", "kda_prefill_segment_noalloc", "kda_plan",
-    "kda_plan_varlen", "kda_decode",
+    "kda_plan_varlen", "kda_decode", "kda_decode_paged", "kda_pages_alloc", "kda_pages_free",
+    "kda_pages_fork", "kda_pages_compact", "kda_pages_copy", "kda_kvcache_append",
+    "kda_kvcache_attention", "kda_beam_select",
 )
 
 STATE_F32 = 0
@@ -58,6 +61,24 @@ class KdaOptions(ctypes.Structure):
     _fields_ = [("mode", ctypes.c_int32), ("segment_len", ctypes.c_int32),
                 ("wait_limit", ctypes.c_int64), ("debug_flags", ctypes.c_int32),
                 ("host_pieces", ctypes.c_int32), ("state_dtype", ctypes.c_int32)]
+
+
+class KdaPageShape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("width", ctypes.c_int32), ("pages", ctypes.c_int32)]
+
+
+class KdaPool(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("page_bytes", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("layer_stride", ctypes.c_int64),
+                ("layers", ctypes.c_int32)]
+
+
+class KdaKvCache(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("pages", ctypes.c_int32), ("page_tokens", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("tables", ctypes.c_void_p), ("rows", ctypes.c_int32), ("width", ctypes.c_int32)]
 
 
 _lib = None
@@ -96,6 +117,20 @@ def load_library(path: Optional[str] = None, build_if_missing: bool = False) -> 
                                  ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int32)]
         lib.kda_decode.argtypes = [ctypes.POINTER(KdaShape), u16p, u16p, u16p, f32p, u16p,
                                    ctypes.c_float, vp, vp, ctypes.c_int32, u16p, vp]
+        i32, i64, f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+        shape, pool, cache = (ctypes.POINTER(x) for x in (KdaPageShape, KdaPool, KdaKvCache))
+        lib.kda_decode_paged.argtypes = [ctypes.POINTER(KdaShape), u16p, u16p, u16p, f32p, u16p,
+                                         f32, vp, i32, i64, i32p, i32, u16p, vp]
+        lib.kda_pages_alloc.argtypes = [shape, vp, vp, vp, vp, vp, vp]
+        lib.kda_pages_free.argtypes = [shape, vp, vp, vp, vp, vp, vp]
+        lib.kda_pages_fork.argtypes = [shape, vp, vp, vp, vp, i32, pool, i32, vp, vp, vp]
+        lib.kda_pages_compact.argtypes = [shape, vp, vp, pool, i32, vp, vp, vp, vp, vp]
+        lib.kda_pages_copy.argtypes = [i32, i32, vp, vp, pool, i32, vp]
+        lib.kda_kvcache_append.argtypes = [cache, vp, vp, i32, i64, i64, i64, vp, vp, vp]
+        lib.kda_kvcache_attention.argtypes = [cache, vp, i32, i32, i64, i64, vp, vp, f32, vp, i64,
+                                              vp]
+        lib.kda_beam_select.argtypes = [i32, i32, i32, i32, vp, i32, i64, vp, vp, i32, vp, vp, vp,
+                                        vp, vp]
         lib.kda_get_device_status.argtypes = [vp, ctypes.POINTER(ctypes.c_int32)]
         lib.kda_release_workspaces.argtypes = [ctypes.c_int32]
         lib.kda_status_string.argtypes = [ctypes.c_int]
@@ -105,7 +140,10 @@ def load_library(path: Optional[str] = None, build_if_missing: bool = False) -> 
         for f in (lib.kda_prefill, lib.kda_prefill_ex, lib.kda_prefill_host,
                   lib.kda_prefill_segment_noalloc, lib.kda_decode,
                   lib.kda_workspace_bytes, lib.kda_get_device_status, lib.kda_plan,
-                  lib.kda_release_workspaces):
+                  lib.kda_release_workspaces, lib.kda_decode_paged, lib.kda_pages_alloc,
+                  lib.kda_pages_free, lib.kda_pages_fork, lib.kda_pages_compact,
+                  lib.kda_pages_copy, lib.kda_kvcache_append, lib.kda_kvcache_attention,
+                  lib.kda_beam_select):
             f.restype = ctypes.c_int
         if path is None:
             _lib = lib
@@ -461,3 +499,54 @@ def kda_decode(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tenso
                             _STATE_DTYPES[state_dtype], _ptr(out), ctypes.c_void_p(int(stream)))
     _check(lib, st)
     return (out.squeeze(1) if single else out), final_state
+
+
+def kda_decode_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
+                     beta: torch.Tensor, states: torch.Tensor, state_pages: torch.Tensor,
+                     scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                     stream=None):
+    """:func:`kda_decode` on a pool of states, in place; returns ``out``.
+
+    ``states``: ``[pages, H, 128, 128]`` in fp32 or bf16, its pages contiguous (a layer of a
+    ``[layers, pages, ...]`` pool, or a slice along the pages); ``state_pages``: int32 ``[B]``,
+    the page of each sequence.  Sequences with a negative page are idle: their output is zero.
+    q may have at most v's heads.
+    """
+    lib = load_library()
+    single = q.dim() == 3
+    if single:
+        q, k, v, g = (x.unsqueeze(1) for x in (q, k, v, g))
+        beta = beta.unsqueeze(1)
+    _check_tensors(q, k, v, g, beta, None, None, "cuda")
+    if q.dim() != 4:
+        raise ValueError("q must be [B, H, 128] or [B, T, H, 128]")
+    B, T, Hq, D = q.shape
+    H = v.shape[2]
+    if states.dtype not in _STATE_DTYPES or states.device != q.device:
+        raise ValueError("states must be an fp32 or bf16 tensor on q's device")
+    if states.dim() != 4 or tuple(states.shape[1:]) != (H, D, D):
+        raise ValueError(f"states must be [pages, {H}, {D}, {D}]")
+    if tuple(states.stride()[1:]) != (D * D, D, 1):
+        raise ValueError("the pages of states must be contiguous")
+    if state_pages.dtype != torch.int32 or tuple(state_pages.shape) != (B,) or \
+            not state_pages.is_contiguous() or state_pages.device != q.device:
+        raise ValueError(f"state_pages must be a contiguous int32 [{B}] tensor on q's device")
+    if scale is None:
+        scale = D ** -0.5
+    _check_result("out", out, _out_shape(q, v), torch.bfloat16, "cuda")
+    if out is None:
+        out = torch.empty(_out_shape(q, v), dtype=q.dtype, device=q.device)
+    if stream is None:
+        stream = torch.cuda.current_stream(q.device).cuda_stream
+    elif isinstance(stream, torch.cuda.Stream):
+        stream = stream.cuda_stream
+    shape = KdaShape(B, T, 0, H, D, Hq)
+    stride = states.stride(0) if states.shape[0] > 1 else H * D * D
+    with torch.cuda.device(q.device):
+        st = lib.kda_decode_paged(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
+                                  _ptr(beta), ctypes.c_float(scale), _ptr(states),
+                                  states.shape[0], stride, _ptr(state_pages),
+                                  _STATE_DTYPES[states.dtype], _ptr(out),
+                                  ctypes.c_void_p(int(stream)))
+    _check(lib, st)
+    return out.squeeze(1) if single else out

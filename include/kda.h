@@ -70,7 +70,9 @@ typedef enum kda_status {
     KDA_ERR_CAPTURE_NEEDS_WARMUP = 6, /* a workspace would be allocated during stream capture
                                          (flashinfer PR #4313, review of EncodeTmaPointers:
                                          warm the workspace before capture) */
-    KDA_ERR_DEVICE_TIMEOUT = 7        /* a device-side bounded wait ran out (status word) */
+    KDA_ERR_DEVICE_TIMEOUT = 7,       /* a device-side bounded wait ran out (status word) */
+    KDA_ERR_NO_FREE_PAGE = 8,         /* a page operation found too few free pages (status word) */
+    KDA_ERR_NONFINITE = 9             /* the cache append met an infinity or a NaN (status word) */
 } kda_status;
 
 /* Problem shape.  Dense: cu_seqlens == NULL, `batch` sequences of `seq_len`
@@ -246,6 +248,191 @@ kda_status kda_decode(const kda_shape* shape, const uint16_t* q, const uint16_t*
                       const void* initial_state, void* final_state, int32_t state_dtype,
                       uint16_t* out, void* stream);
 
+/* ---------------------------------------------------------------------------------------
+ * Pages.  A server keeps what its rows (sequences, beams) have accumulated in pools of
+ * pages: recurrent states (one page a row, holding a layer's [H][128][128] states) and the
+ * key/value cache of full-attention layers (a page holds page_tokens tokens).  One page
+ * number stands for the same page of every pool and layer.  The operations below work on
+ *   tables  int32 [rows][width]: the pages of each row in order, -1 where there is none
+ *   refs    int32 [pages]: references to each page, 0 where it is free.  Every table entry
+ *           is one reference; whoever else keeps a page (a prefix cache) adds its own
+ * and leave both as they are: they write new tables and new refs, which must not overlap
+ * any input.  All of them run on `stream` without a host synchronisation, take device
+ * pointers (4-byte aligned) and give the same result in every run.  Numbers out of range are
+ * treated as absent and recorded in the device status word as KDA_ERR_INVALID_ARGUMENT. */
+typedef struct kda_page_shape {
+    int32_t rows;   /* >= 0; rows * width <= 2^30 */
+    int32_t width;  /* >= 1 */
+    int32_t pages;  /* >= 0, <= 2^30 */
+} kda_page_shape;
+
+/* One pool: `layers` layers of `pages` pages of page_bytes contiguous bytes, page p of layer l
+ * at base + l * layer_stride + p * page_stride (strides in bytes, at least the size of what
+ * they step over). */
+typedef struct kda_pool {
+    void* base;
+    int64_t page_bytes;
+    int64_t page_stride;
+    int64_t layer_stride;
+    int32_t layers;
+} kda_pool;
+
+#define KDA_MAX_POOLS 64  /* pools of one call */
+
+/* kda_pages_alloc -- gives row r at least want[r] pages: every entry j < want[r] that holds
+ * none gets the next free page, lowest page first, entries in order (row by row).
+ *   want  device int32 [rows]; values above width are recorded and taken as width
+ * With too few free pages the remaining entries stay -1 and KDA_ERR_NO_FREE_PAGE goes to the
+ * status word.  Contents of the pages are not touched. */
+kda_status kda_pages_alloc(const kda_page_shape* shape, const int32_t* tables, const int32_t* refs,
+                           const int32_t* want, int32_t* new_tables, int32_t* new_refs, void* stream);
+
+/* kda_pages_free -- drops the rows whose drop[r] (device uint8 [rows]) is not zero: their
+ * entries become -1 and give up their references. */
+kda_status kda_pages_free(const kda_page_shape* shape, const int32_t* tables, const int32_t* refs,
+                          const uint8_t* drop, int32_t* new_tables, int32_t* new_refs, void* stream);
+
+/* kda_pages_fork -- row r continues row parents[r] (-1: row r ends).  The step that beam search
+ * needs after its selection, for all rows at once:
+ *   entries j < lens[parent] / page_tokens hold whole pages, which are shared (one more
+ *   reference); the entries from there on will be written to, so each row gets them to
+ *   itself: the first row (lowest r) takes the parent's page over where nobody else still
+ *   holds it, every other row gets the next free page (lowest first, entries in order)
+ *   and a copy of the contents in every pool.  Pages of rows that nobody continues are
+ *   free before any is taken, so rows of one private page each never need spare pages.
+ *   parents      device int32 [rows]
+ *   lens         device int32 [rows], tokens of the rows before the fork; may be NULL when
+ *                page_tokens is 0
+ *   page_tokens  tokens a page holds; 0: every page is private (recurrent states)
+ *   pools        host array of num_pools (0 .. KDA_MAX_POOLS) pools, read during the call
+ * With too few free pages the remaining entries become -1 and KDA_ERR_NO_FREE_PAGE goes to
+ * the status word. */
+kda_status kda_pages_fork(const kda_page_shape* shape, const int32_t* tables, const int32_t* refs,
+                          const int32_t* parents, const int32_t* lens, int32_t page_tokens,
+                          const kda_pool* pools, int32_t num_pools, int32_t* new_tables,
+                          int32_t* new_refs, void* stream);
+
+/* kda_pages_compact -- moves the pages in use to the front: with n pages in use, those
+ * numbered n and above move to the free ones below n, in order, in every pool.
+ *   page_map  device int32 [pages]: the new number of each page, -1 for free ones
+ *   num_live  device int32 [1]: n */
+kda_status kda_pages_compact(const kda_page_shape* shape, const int32_t* tables, const int32_t* refs,
+                             const kda_pool* pools, int32_t num_pools, int32_t* new_tables,
+                             int32_t* new_refs, int32_t* page_map, int32_t* num_live, void* stream);
+
+/* kda_pages_copy -- copies page src[i] to page dst[i] in every pool, i < count; pairs with a
+ * negative number are skipped.  No page may be the destination of two pairs, nor the
+ * destination of one and the source of another: their contents would be undefined. */
+kda_status kda_pages_copy(int32_t pages, int32_t count, const int32_t* src, const int32_t* dst,
+                          const kda_pool* pools, int32_t num_pools, void* stream);
+
+/* kda_decode_paged -- kda_decode on a pool of states: sequence n reads and updates, in place,
+ * the states at page state_pages[n] (device int32 [N]).
+ *   states       device, `pages` pages of [H][128][128] of state_dtype, page p at element
+ *                p * page_stride (page_stride >= H * 128 * 128, a multiple of 8)
+ * Sequences with a negative page are idle: their output rows are zero.  A page number >= pages
+ * is treated the same and recorded as KDA_ERR_INVALID_ARGUMENT in the status word.  No
+ * page may be given to two sequences.  num_q_heads <= num_heads: with grouped query heads
+ * several blocks read the state that one of them updates.  Everything else as kda_decode. */
+kda_status kda_decode_paged(const kda_shape* shape, const uint16_t* q, const uint16_t* k,
+                            const uint16_t* v, const float* g, const uint16_t* beta, float scale,
+                            void* states, int32_t pages, int64_t page_stride,
+                            const int32_t* state_pages, int32_t state_dtype, uint16_t* out,
+                            void* stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Key/value cache in 8 bits for the full-attention layers of a model that mixes them with KDA
+ * layers.  Codes are e4m3 (4 exponent and 3 mantissa bits, largest value 448) and share one
+ * fp32 scale per block of tokens (a page) and head: value = scale * code.
+ *   k_codes, v_codes  uint8 [pages][num_kv_heads][page_tokens][head_dim], 16-byte aligned
+ *   k_scale, v_scale  fp32 [pages][num_kv_heads]
+ *   tables            int32 [rows][width]: token j of row r is in page tables[r][j / page_tokens]
+ * Activations are bf16 or fp16 (KDA_ACT_*). */
+#define KDA_ACT_BF16 0
+#define KDA_ACT_F16 1
+
+typedef struct kda_kvcache {
+    void* k_codes;
+    void* v_codes;
+    float* k_scale;
+    float* v_scale;
+    int32_t pages;
+    int32_t page_tokens;   /* 16, 32, 64 or 128 */
+    int32_t num_kv_heads;  /* >= 1 */
+    int32_t head_dim;      /* 64 or 128 */
+    const int32_t* tables; /* [rows][width] */
+    int32_t rows;
+    int32_t width;
+} kda_kvcache;
+
+/* kda_kvcache_append -- quantises new tokens into the cache.  Row r appends tokens
+ * cu_tokens[r] .. cu_tokens[r + 1] - 1 of k and v at positions lens[r], lens[r] + 1, ...
+ * Per touched page and head, with a the largest finite magnitude among its new values: a page
+ * whose first token is among them gets scale a / 448 (whatever it held before); an open
+ * page keeps its scale s where a <= 448 s, and otherwise takes a / 448, its older codes
+ * rounded again for it.  Quotients are IEEE fp32, codes rounded to nearest even.
+ * Infinities are stored as +-448, NaN as 0; both record KDA_ERR_NONFINITE.
+ *   k, v          device [num_tokens][num_kv_heads][head_dim], token stride in elements (a
+ *                 multiple of 8, at least num_kv_heads * head_dim), 16-byte aligned
+ *   lens          device int32 [rows]: tokens each row holds before the call (not updated)
+ *   cu_tokens     device int32 [rows + 1] (cu_seqlens rules) or NULL: one token for each
+ *                 row, num_tokens = rows
+ * The pages must be there (kda_pages_alloc) and private to their row (kda_pages_fork).
+ * Tokens without a page are dropped and recorded as KDA_ERR_INVALID_ARGUMENT. */
+kda_status kda_kvcache_append(const kda_kvcache* cache, const void* k, const void* v,
+                              int32_t act_dtype, int64_t k_stride, int64_t v_stride,
+                              int64_t num_tokens, const int32_t* lens, const int32_t* cu_tokens,
+                              void* stream);
+
+/* kda_kvcache_attention -- causal attention of new tokens over the cache.  Row r has lens[r]
+ * tokens in the cache, its query tokens cu_tokens[r] .. cu_tokens[r + 1] - 1 among them as the
+ * last ones: token i of n sits at position p = lens[r] - n + i and sees keys 0 .. p,
+ *     o = sum_j softmax_j(scale * q . k_j) v_j,
+ * zero where it sees none.  Query head h reads key/value head h / (num_q_heads /
+ * num_kv_heads).  Sums are fp32; the softmax weights are rounded to fp16 for the product with
+ * the codes.
+ *   q, out        device [num_tokens][num_q_heads][head_dim] of act_dtype, token strides in
+ *                 elements (multiples of 8), 16-byte aligned; out must not overlap any input
+ *   lens          device int32 [rows]
+ *   cu_tokens     device int32 [rows + 1] or NULL: one token for each row, num_tokens = rows
+ *   scale         finite
+ * Codes at positions below lens[r] must be finite (the append writes no others); what a page
+ * holds past them is never used.  Positions whose page is missing are skipped and
+ * recorded as KDA_ERR_INVALID_ARGUMENT. */
+kda_status kda_kvcache_attention(const kda_kvcache* cache, const void* q, int32_t num_q_heads,
+                                 int32_t act_dtype, int64_t q_stride, int64_t num_tokens,
+                                 const int32_t* lens, const int32_t* cu_tokens, float scale,
+                                 void* out, int64_t out_stride, void* stream);
+
+/* ---------------------------------------------------------------------------------------
+ * kda_beam_select -- one step of beam search: the num_out best continuations of each request.
+ * Beam w of request b scored scores[b][w]; its token t continues it with
+ *     total = scores[b][w] + (logit - lse),  lse = log sum exp over the beam's logits,
+ * and the request's num_out largest totals over all beams and tokens are its new beams,
+ * best first, equal totals in the order of w * vocab + t.  Logits that are not finite are no
+ * candidates and do not enter lse; nor is a candidate whose total is not above -inf.  A
+ * finished beam (done) continues only with eos, at its unchanged score.
+ *   logits      device [batch * beams] rows of vocab values, logits_dtype KDA_LOGITS_*, row
+ *               stride in elements (>= vocab), aligned to its element size
+ *   scores      device fp32 [batch][beams]
+ *   done        device uint8 [batch][beams], or NULL (no beam is finished)
+ *   eos         a token in [0, vocab), or -1 (none; needs done == NULL)
+ *   new_scores  fp32 [batch][num_out];  tokens, parents  int32 [batch][num_out]: the token and
+ *               the row b * beams + w it continues (what kda_pages_fork takes as parents
+ *               when num_out == beams).  Places that no candidate is left for get
+ *               -inf, -1, -1
+ *   new_done    uint8 [batch][num_out] or NULL: 1 where the token is eos, the parent was
+ *               finished, or the place is empty
+ * 1 <= beams, num_out <= 64; beams * vocab <= 2^31 - 1; outputs must not overlap inputs. */
+#define KDA_LOGITS_F32 0
+#define KDA_LOGITS_BF16 1
+#define KDA_LOGITS_F16 2
+kda_status kda_beam_select(int32_t batch, int32_t beams, int32_t vocab, int32_t num_out,
+                           const void* logits, int32_t logits_dtype, int64_t logits_stride,
+                           const float* scores, const uint8_t* done, int32_t eos,
+                           float* new_scores, int32_t* tokens, int32_t* parents,
+                           uint8_t* new_done, void* stream);
+
 /* Bytes of device workspace a call with this shape and these options uses
  * (0 for serial mode).  The segment pipeline's scratch (per-segment summaries,
  * transitions and carries: cuLA PR #103, review of the CP driver's _get_scratch, which
@@ -288,7 +475,8 @@ kda_status kda_plan_varlen(const kda_shape* shape, const int32_t* host_cu_seqlen
 
 /* Reads and clears the device status word of the current device after
  * synchronising `stream`.  *code receives KDA_OK, KDA_ERR_INVALID_ARGUMENT
- * (malformed cu_seqlens contents seen by a kernel) or KDA_ERR_DEVICE_TIMEOUT.
+ * (malformed cu_seqlens or page numbers seen by a kernel), KDA_ERR_DEVICE_TIMEOUT,
+ * KDA_ERR_NO_FREE_PAGE or KDA_ERR_NONFINITE (the first condition since the last read).
  * The pages validate on the host and abort the call with a message (flashinfer PR
  * #4313, review of flashkda_binding_common.cuh: the TVM_FFI_ICHECK target, shape and
  * capacity checks) and record a device-side hazard only in review (flashinfer PR #4351,
@@ -303,7 +491,9 @@ kda_status kda_get_device_status(void* stream, int32_t* code);
  * pages' scratch cache raced across streams because its key lacked the stream (cuLA PR
  * #103, review of _get_scratch) and their per-stream workspace maps grew without bound
  * (flashinfer PR #4313, review of kda_prefill.py, which asks for a bound or an eviction
- * path); this call is the explicit release. */
+ * path); this call is the explicit release.  The scratch of the cache, page and beam calls
+ * is one more buffer per (device, stream), for at most 32 of them; where a larger call grows
+ * it, the smaller buffer lives on until this call, so graphs captured on it stay valid. */
 kda_status kda_release_workspaces(int32_t device);
 
 /* Static description of a status code.  The pages' bindings fail with a message per

@@ -1,0 +1,287 @@
+"""The 8-bit paged cache: append bit for bit, attention against 64 bits.
+
+Attention's bound, from its roundings: the softmax weights are fp16 (relative 2^-11, and
+2^-25 of the largest weight where they leave fp16's normal range) on the weighted sum of |v|,
+scores carry fp32 errors of a few 2^-23 of their size (below 64 here: 2^-15 of the weights),
+the output is rounded once (2^-9 for bf16, 2^-12 for fp16, of its own size).  Allowed: twice
+the output's rounding plus 2^-10 sum_j p_j |v_j| plus 1e-6."""
+import numpy as np
+import pytest
+import torch
+
+import chunked_kda_delta_gb300 as K
+import serving_testutil as ref
+
+pytestmark = pytest.mark.gpu
+F8 = torch.float8_e4m3fn
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
+
+
+def make_cache(rng, rows, hkv, page, d, lens, spare=2):
+    """Random codes everywhere (NaN codes included past the rows' tokens), tables in random order."""
+    need = [-(-int(n) // page) for n in lens]
+    pages = sum(need) + spare
+    order = rng.permutation(pages)
+    tables = np.full((rows, max(1, max(need, default=1))), -1)
+    at = 0
+    kc, vc = (rng.integers(0, 256, (pages, hkv, page, d), dtype=np.uint8) for _ in range(2))
+    for r in range(rows):
+        tables[r, : need[r]] = order[at: at + need[r]]
+        at += need[r]
+        for i in range(need[r]):
+            m = min(page, int(lens[r]) - i * page)
+            for c in (kc, vc):
+                x = c[tables[r, i], :, :m]
+                x[(x & 0x7F) == 0x7F] = 0x11
+                c[tables[r, i], :, m:] |= 0x7F  # NaN where no token is
+    ks, vs = (rng.uniform(0.2, 2.0, (pages, hkv)).astype(np.float32) / 448 for _ in range(2))
+    return kc, vc, ks, vs, tables
+
+
+def gpu_cache(kc, vc, ks, vs, tables):
+    return (torch.as_tensor(kc).cuda().view(F8), torch.as_tensor(vc).cuda().view(F8), torch.as_tensor(ks).cuda(),
+            torch.as_tensor(vs).cuda(), torch.as_tensor(tables).to(torch.int32).cuda())
+
+
+def cu_of(counts):
+    return torch.tensor([0] + list(np.cumsum(counts)), dtype=torch.int32, device="cuda")
+
+
+def check_attention(rng, rows, hq, hkv, d, page, lens, counts, dtype, cu=True, q_scale=1.0, scale=None, q=None, tables=None):
+    kc, vc, ks, vs, tab = make_cache(rng, rows, hkv, page, d, lens)
+    if tables is not None:
+        tab = tables(tab)
+    if q is None:
+        q = torch.as_tensor(rng.standard_normal((sum(counts), hq, d)) * q_scale).to(DT[dtype])
+    scale = d ** -0.5 if scale is None else scale
+    want, weight = ref.attention(q.double().numpy(), kc, vc, ks, vs, tab, lens, counts, page, scale)
+    got = K.kda_kvcache_attention(q.cuda(), *gpu_cache(kc, vc, ks, vs, tab), torch.as_tensor(lens).to(torch.int32).cuda(),
+                                  cu_tokens=cu_of(counts) if cu else None, scale=scale)
+    assert got.dtype == q.dtype
+    got = got.double().cpu().numpy()
+    eps = 2.0 ** (-8 if dtype == "bf16" else -11)
+    allowed = eps * np.abs(want) + 2.0 ** -10 * weight + 1e-6
+    assert np.isfinite(got).all()
+    assert (np.abs(got - want) <= allowed).all(), np.max(np.abs(got - want) / allowed)
+
+
+@pytest.mark.parametrize("hq,hkv,d,page", [(1, 1, 128, 16), (8, 1, 64, 32), (12, 3, 128, 64), (7, 1, 128, 128), (32, 2, 64, 16), (40, 1, 128, 64)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_one_token(hq, hkv, d, page, dtype):
+    rng = np.random.default_rng(hq * 1000 + d + page)
+    lens = [0, 1, 15, 16, 17, 127, 128, 129, 300, 1000]
+    check_attention(rng, len(lens), hq, hkv, d, page, lens, [1] * len(lens), dtype, cu=False)
+
+
+@pytest.mark.parametrize("hq,hkv,d,page", [(4, 4, 128, 16), (6, 2, 64, 64), (16, 1, 128, 32), (5, 1, 64, 128)])
+def test_several_tokens(hq, hkv, d, page):
+    rng = np.random.default_rng(hq + d + page)
+    counts = [0, 3, 1, 40, 70, 5, 0]
+    lens = [9, 3, 500, 40, 333, 2, 0]  # all new, mostly old, more new tokens than cached ones
+    check_attention(rng, len(lens), hq, hkv, d, page, lens, counts, "bf16")
+
+
+def test_one_long_row_is_split():
+    rng = np.random.default_rng(3)
+    check_attention(rng, 2, 8, 1, 128, 64, [20000, 1], [1, 1], "fp16", cu=False)
+
+
+def test_large_scores_and_extreme_queries():
+    rng = np.random.default_rng(4)
+    q = torch.as_tensor(rng.standard_normal((3, 4, 64)))
+    q[0] *= 1e30  # beyond fp16
+    q[1] *= 1e-30
+    q[2] = 0
+    q = q.to(torch.bfloat16)
+    kc, vc, ks, vs, tab = make_cache(rng, 3, 2, 16, 64, [40, 40, 40])
+    for r, s in ((0, 1e-30), (1, 1e30), (2, 1.0)):
+        one = slice(r, r + 1)
+        want, weight = ref.attention(q[one].double().numpy(), kc, vc, ks, vs, tab[one], [40], [1], 16, s)
+        got = K.kda_kvcache_attention(q[one].cuda(), *gpu_cache(kc, vc, ks, vs, tab[one]), torch.tensor([40], dtype=torch.int32).cuda(), scale=s)
+        got = got.double().cpu().numpy()
+        assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -10 * weight + 1e-6).all()
+
+
+def test_scales_that_differ_by_orders_of_magnitude():
+    rng = np.random.default_rng(6)
+    lens = [200]
+    kc, vc, ks, vs, tab = make_cache(rng, 1, 1, 16, 64, lens)
+    vs *= (10.0 ** rng.integers(-6, 6, vs.shape)).astype(np.float32)
+    vs[tab[0, 0]] = 0
+    q = torch.as_tensor(rng.standard_normal((1, 4, 64))).to(torch.bfloat16)
+    want, weight = ref.attention(q.double().numpy(), kc, vc, ks, vs, tab, lens, [1], 16, 0.125)
+    got = K.kda_kvcache_attention(q.cuda(), *gpu_cache(kc, vc, ks, vs, tab), torch.tensor(lens, dtype=torch.int32).cuda()).double().cpu().numpy()
+    assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -10 * weight + 1e-6).all()
+
+
+def test_missing_pages_are_skipped_and_recorded():
+    rng = np.random.default_rng(7)
+    K.kda_get_device_status()
+
+    def broken(t):
+        t = t.copy()
+        t[0, 1], t[1, 0] = -1, 10 ** 6
+        return t
+
+    check_attention(rng, 2, 4, 2, 128, 16, [100, 16], [1, 1], "bf16", cu=False, tables=broken)
+    assert K.kda_get_device_status() == 1
+
+
+def test_lengths_past_the_table_are_recorded():
+    rng = np.random.default_rng(8)
+    kc, vc, ks, vs, tab = make_cache(rng, 2, 1, 16, 64, [32, 32])
+    q = torch.randn(2, 1, 64, device="cuda", dtype=torch.bfloat16)
+    cache = gpu_cache(kc, vc, ks, vs, tab)
+    K.kda_get_device_status()
+    a = K.kda_kvcache_attention(q, *cache, torch.tensor([33, -5], dtype=torch.int32, device="cuda"))
+    assert K.kda_get_device_status() == 1
+    b = K.kda_kvcache_attention(q, *cache, torch.tensor([32, 0], dtype=torch.int32, device="cuda"))
+    assert torch.equal(a, b) and (b[1] == 0).all() and K.kda_get_device_status() == 0
+
+
+def test_strided_queries_and_outputs_and_reruns():
+    rng = np.random.default_rng(9)
+    lens = [77, 3000, 12]
+    cache = gpu_cache(*make_cache(rng, 3, 2, 32, 128, lens))
+    ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    wide = torch.randn(3, 3, 8, 128, device="cuda", dtype=torch.bfloat16)  # [tokens, qkv, heads, dim]
+    q = wide[:, 1]
+    plain = K.kda_kvcache_attention(q.contiguous(), *cache, ln)
+    out = torch.zeros(3, 2, 8, 128, device="cuda", dtype=torch.bfloat16)
+    K.kda_kvcache_attention(q, *cache, ln, out=out[:, 0])
+    assert torch.equal(out[:, 0], plain) and (out[:, 1] == 0).all()
+    for _ in range(3):
+        assert torch.equal(K.kda_kvcache_attention(q, *cache, ln), plain)
+
+
+def test_malformed_offsets_are_recorded():
+    rng = np.random.default_rng(10)
+    cache = gpu_cache(*make_cache(rng, 2, 1, 16, 64, [40, 40]))
+    ln = torch.tensor([40, 40], dtype=torch.int32, device="cuda")
+    q = torch.randn(4, 1, 64, device="cuda", dtype=torch.bfloat16)
+    K.kda_get_device_status()
+    for bad in ([0, 5, 4], [1, 2, 4], [0, 2, 3], [0, -3, 4]):
+        K.kda_kvcache_attention(q, *cache, ln, cu_tokens=torch.tensor(bad, dtype=torch.int32, device="cuda"))
+        assert K.kda_get_device_status() == 1, bad
+        K.kda_kvcache_append(q, q, *cache, ln - 8, cu_tokens=torch.tensor(bad, dtype=torch.int32, device="cuda"))
+        assert K.kda_get_device_status() == 1, bad
+
+
+def test_offsets_past_32_bits():
+    # 2^25 key blocks of 128 bytes and more: the last pages lie past 2^32 bytes of codes
+    pages, d, page = 40000, 128, 128
+    codes = torch.zeros(pages, 8, page, d, dtype=torch.uint8, device="cuda")  # 5.2 GB
+    scale = torch.ones(pages, 8, device="cuda")
+    rng = np.random.default_rng(11)
+    kc, vc, ks, vs, _ = make_cache(rng, 1, 8, page, d, [page], spare=0)
+    codes[-1] = torch.as_tensor(vc[0]).cuda()
+    q = torch.as_tensor(rng.standard_normal((1, 8, d))).to(torch.bfloat16)
+    tab = torch.tensor([[pages - 1]], dtype=torch.int32, device="cuda")
+    ln = torch.tensor([page], dtype=torch.int32, device="cuda")
+    got = K.kda_kvcache_attention(q.cuda(), codes.view(F8), codes.view(F8), scale, scale, tab, ln)
+    one = codes[-1:].contiguous()
+    near = K.kda_kvcache_attention(q.cuda(), one.view(F8), one.view(F8), scale[:1].contiguous(), scale[:1].contiguous(), torch.zeros_like(tab), ln)
+    assert torch.equal(got, near) and got.abs().max() > 0
+    k = torch.randn(1, 8, d, device="cuda").to(torch.bfloat16)
+    K.kda_kvcache_append(k, k, codes.view(F8), codes.view(F8).clone(), scale, scale.clone(), tab, ln - 1)
+    K.kda_kvcache_append(k, k, one.view(F8), one.view(F8).clone(), torch.ones_like(scale[:1]), torch.ones_like(scale[:1]), torch.zeros_like(tab), ln - 1)
+    assert torch.equal(codes[-1], one[0])
+
+
+def check_append(rng, hkv, d, page, lens, counts, dtype, cu=True, spoil=None, strided=False):
+    total = [a + b for a, b in zip(lens, counts)]
+    kc, vc, ks, vs, tab = make_cache(rng, len(lens), hkv, page, d, total)
+    for c in (kc, vc):
+        c[(c & 0x7F) == 0x7F] = 0x11  # older tokens are finite
+    xs = [torch.as_tensor(rng.standard_normal((sum(counts), hkv, d)) * s).to(DT[dtype]) for s in (1.0, 3.0)]
+    if spoil:
+        spoil(xs)
+    dc = gpu_cache(kc, vc, ks, vs, tab)
+    cu_t = cu_of(counts) if cu else None
+    ln = torch.as_tensor(lens).to(torch.int32).cuda()
+    if strided:
+        wide = torch.zeros(sum(counts), 3, hkv, d, dtype=DT[dtype], device="cuda")
+        wide[:, 0], wide[:, 2] = xs[0].cuda(), xs[1].cuda()
+        K.kda_kvcache_append(wide[:, 0], wide[:, 2], *dc, ln, cu_tokens=cu_t)
+    else:
+        K.kda_kvcache_append(xs[0].cuda(), xs[1].cuda(), *dc, ln, cu_tokens=cu_t)
+    for x, c, s, gc, gs in ((xs[0], kc, ks, dc[0], dc[2]), (xs[1], vc, vs, dc[1], dc[3])):
+        ref.append(x.float().numpy(), c, s, tab, lens, counts, page)
+        assert np.array_equal(gs.cpu().numpy(), s)
+        assert np.array_equal(gc.view(torch.uint8).cpu().numpy(), c)
+
+
+@pytest.mark.parametrize("hkv,d,page,dtype", [(1, 128, 16, "bf16"), (3, 64, 32, "fp16"), (8, 128, 64, "bf16"), (2, 64, 128, "bf16"), (5, 128, 128, "fp16")])
+def test_append(hkv, d, page, dtype):
+    rng = np.random.default_rng(hkv * page)
+    K.kda_get_device_status()
+    check_append(rng, hkv, d, page, [0, 1, page - 1, page, 5 * page + 3, 40, 7], [1] * 7, dtype, cu=False)
+    check_append(rng, hkv, d, page, [0, 1, page - 1, page, 5 * page + 3, 40, 7], [0, 1, 2, page, 3 * page + 1, 2 * page - 1, 0], dtype)
+    check_append(rng, hkv, d, page, [3, 0], [300, 1], dtype, strided=True)
+    assert K.kda_get_device_status() == 0
+
+
+def test_append_many_rows():
+    rng = np.random.default_rng(12)
+    rows = 300
+    check_append(rng, 1, 64, 16, rng.integers(0, 40, rows).tolist(), rng.integers(0, 40, rows).tolist(), "bf16")
+
+
+@pytest.mark.parametrize("cu", [False, True])
+def test_append_of_values_that_are_not_finite(cu):
+    def spoil(xs):
+        xs[0][0, 0, 3], xs[0][1, 1, 5], xs[1][2, 0, 0] = float("nan"), float("inf"), float("-inf")
+        xs[1][1] = float("nan")
+        xs[0][3] = 0
+
+    rng = np.random.default_rng(13)
+    K.kda_get_device_status()
+    check_append(rng, 2, 64, 16, [4, 0, 16, 0], [1] * 4, "bf16", cu=cu, spoil=spoil)
+    assert K.kda_get_device_status() == 9
+
+
+def test_append_without_a_page_is_recorded():
+    rng = np.random.default_rng(14)
+    kc, vc, ks, vs, tab = make_cache(rng, 2, 1, 16, 64, [16, 16], spare=0)
+    tab[0, 0] = -1
+    cache = gpu_cache(kc, vc, ks, vs, tab)
+    before = cache[0].view(torch.uint8).clone()
+    x = torch.randn(2, 1, 64, device="cuda", dtype=torch.bfloat16)
+    K.kda_get_device_status()
+    for lens in ([3, 16], [3, -1]):  # no page; past the table; a negative length
+        ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        K.kda_kvcache_append(x, x, *cache, ln)
+        assert K.kda_get_device_status() == 1
+        K.kda_kvcache_append(x, x, *cache, ln, cu_tokens=cu_of([1, 1]))
+        assert K.kda_get_device_status() == 1
+    assert torch.equal(cache[0].view(torch.uint8), before)
+
+
+def test_append_then_attend_in_a_graph():
+    rng = np.random.default_rng(15)
+    lens = [30, 63, 0]
+    kc, vc, ks, vs, tab = make_cache(rng, 3, 2, 32, 64, [n + 2 for n in lens])
+    cache = gpu_cache(kc, vc, ks, vs, tab)
+    k, v, q = (torch.randn(3, h, 64, device="cuda", dtype=torch.bfloat16) for h in (2, 2, 4))
+    ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    out = torch.empty_like(q)
+
+    def step():
+        K.kda_kvcache_append(k, v, *cache, ln)
+        K.kda_kvcache_attention(q, *cache, ln + 1, out=out)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            step()
+    torch.cuda.current_stream().wait_stream(s)
+    for x in (k, v, q):
+        x.copy_(torch.randn_like(x))
+    g.replay()
+    torch.cuda.synchronize()
+    first = out.clone()
+    step()
+    assert torch.equal(out, first)
