@@ -118,10 +118,10 @@ struct BeamParams {
     uint8_t* new_done;
     // scratch
     uint64_t* cand;           // [batch * beams][segs][k + 1]
-    float2* part;             // [batch * beams][segs]: segment maximum, sum of exp
+    float4* part;             // [batch * beams][segs]: sums of exponentials (kda_beam.cu)
     int32_t segs, seg_len;
 };
-int beam_seg_len(int64_t rows, int32_t vocab, int sm_count);
+int beam_seg_len(int64_t rows, int32_t vocab, int elem, int sm_count);
 cudaError_t launch_beam(const BeamParams& p, cudaStream_t stream);
 
 }  // namespace kda

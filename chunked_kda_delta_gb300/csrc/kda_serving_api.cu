@@ -475,16 +475,17 @@ kda_status kda_beam_select(int32_t batch, int32_t beams, int32_t vocab, int32_t 
         p.tokens = tokens;
         p.parents = parents;
         p.new_done = new_done;
-        p.seg_len = kda::beam_seg_len(rows, vocab, di->sm_count);
+        p.seg_len = kda::beam_seg_len(rows, vocab, (int)elem, di->sm_count);
         // Rows that do not all start on 16 bytes are cut at 16-byte boundaries: up to one
         // load's elements more.
         const bool even = aligned(logits, 16) && (size_t)logits_stride * elem % 16 == 0;
         p.segs = (int32_t)(((int64_t)vocab + (even ? 0 : 16 / elem - 1) + p.seg_len - 1) / p.seg_len);
-        const size_t cb = (size_t)rows * p.segs * (num_out + 1) * 8, pb = (size_t)rows * p.segs * 8;
+        if (rows * p.segs > 0x7fffffffll) return fail(KDA_ERR_INVALID_ARGUMENT, "batch * beams * vocab is too large");
+        const size_t pb = (size_t)rows * p.segs * 16, cb = (size_t)rows * p.segs * (num_out + 1) * 8;
         char* ws = nullptr;
         if ((st = scratch(dev, stream, cb + pb, &ws)) != KDA_OK) return st;
-        p.cand = reinterpret_cast<uint64_t*>(ws);
-        p.part = reinterpret_cast<float2*>(ws + cb);
+        p.part = reinterpret_cast<float4*>(ws);
+        p.cand = reinterpret_cast<uint64_t*>(ws + pb);
         const cudaError_t e = kda::launch_beam(p, (cudaStream_t)stream);
         return e == cudaSuccess ? KDA_OK : cuda_fail(e, "beam selection launch");
     });
