@@ -1,15 +1,17 @@
 // kda_beam.cu -- one step of beam search: log-softmax over the vocabulary, the largest
 // totals over beams and tokens, in two launches.
 //
-// Bound by reading the logits once.  beam_scan gives every warp a segment of a row (request,
-// beam), which it reads in steps of four 16-byte loads a lane, the next step's loads under way
-// while it works on this one.  Warps share nothing, so no barrier holds up the loads.  A lane
-// keeps its own running sum of exponentials; the warp keeps the segment's k + 1 largest
-// logits as a sorted list spread over its lanes, and only values not below the list's last
-// take the path that inserts them (about (k + 1) ln(n) of n values in no particular order).
-// The first step's list starts from a bound: the (k + 1)-th largest of the lanes' (or of the
-// loads') own maxima is not above the (k + 1)-th largest value.  beam_join, one CTA a request,
-// puts the sums together and ranks the candidates.
+// Bound by reading the logits once.  beam_scan gives every CTA a segment of a row (request,
+// beam).  Its warps stream it in steps of four 16-byte loads a lane, the next step's loads
+// under way while they work on this one; a lane keeps a running sum of exponentials and
+// notes the largest value of each of its steps, nothing else.  Selection comes after the stream:
+// the lanes form 32 groups (128 where k + 1 does not fit), and the (k + 1)-th largest of the
+// groups' maxima is not above the segment's (k + 1)-th largest value.  Only the steps of lanes
+// whose noted maximum reaches that bound are read again, a few dozen bytes each and little
+// more than k + 1 of them, and their values that reach it are the candidates.  (Keeping sorted
+// lists while streaming, with a bound that rises, took 12 us more on 256 rows of 131072: some
+// warp always has a value to insert.)  beam_join, one CTA a request, puts the sums together and
+// ranks the candidates.
 //
 // Candidates are 64-bit keys (value, complement of the index), all different: ranking them
 // by counting larger keys needs no sort and ties go to the lowest index.
@@ -32,13 +34,22 @@
 namespace kda {
 namespace {
 
-constexpr int kScanWarps = 4;
+constexpr int kScanWarps = 8, kScanThreads = kScanWarps * 32;
 constexpr int kJoinThreads = 512, kGroups = 128;
 constexpr int kBuffer = 512;  // candidate keys of one selection
 constexpr int kLoads = 4;     // 16-byte loads of a lane and step
+constexpr int kMaxSteps = 16; // of a warp
 constexpr float kNegInf = -INFINITY;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kHuge = 1e30f;
+
+// 2^x by the hardware's instruction (results below 2^-126 are 0, which sums of a largest
+// term near 1 do not notice).
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 // Whole number in the order of the float (-0 counts as +0).
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -59,32 +70,47 @@ __device__ __forceinline__ float usable(float x) { return fabsf(x) < INFINITY ? 
 
 template <typename T> struct Logit;
 template <> struct Logit<float> {
+    static constexpr int kPer = 1;  // values of a 32-bit word
     static __device__ __forceinline__ void unpack(uint32_t w, float* v) { v[0] = __uint_as_float(w); }
     static __device__ __forceinline__ float get(float x) { return x; }
+    // Largest of two words, by values; NaN loses.
+    static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+        return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    }
     static constexpr uint32_t kNone = 0xff800000u;  // -inf
     static __device__ __forceinline__ uint32_t bits(float x) { return __float_as_uint(x); }
     static __device__ __forceinline__ float from(uint32_t b) { return __uint_as_float(b); }
     static constexpr uint32_t kSign = 0x80000000u;
 };
 template <> struct Logit<__nv_bfloat16> {
+    static constexpr int kPer = 2;
     static __device__ __forceinline__ void unpack(uint32_t w, float* v) {
         v[0] = __uint_as_float(w << 16);
         v[1] = __uint_as_float(w & 0xffff0000u);
     }
-    static constexpr uint32_t kNone = 0xff80u;
     static __device__ __forceinline__ float get(__nv_bfloat16 x) { return __bfloat162float(x); }
+    static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+        const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+        return *reinterpret_cast<const uint32_t*>(&m);
+    }
+    static constexpr uint32_t kNone = 0xff80u;
     static __device__ __forceinline__ uint32_t bits(float x) { return __bfloat16_as_ushort(__float2bfloat16(x)); }
     static __device__ __forceinline__ float from(uint32_t b) { return __bfloat162float(__ushort_as_bfloat16((unsigned short)b)); }
     static constexpr uint32_t kSign = 0x8000u;
 };
 template <> struct Logit<__half> {
+    static constexpr int kPer = 2;
     static __device__ __forceinline__ void unpack(uint32_t w, float* v) {
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
         v[0] = f.x;
         v[1] = f.y;
     }
-    static constexpr uint32_t kNone = 0xfc00u;
     static __device__ __forceinline__ float get(__half x) { return __half2float(x); }
+    static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+        const __half2 m = __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+        return *reinterpret_cast<const uint32_t*>(&m);
+    }
+    static constexpr uint32_t kNone = 0xfc00u;
     static __device__ __forceinline__ uint32_t bits(float x) { return __half_as_ushort(__float2half(x)); }
     static __device__ __forceinline__ float from(uint32_t b) { return __half2float(__ushort_as_half((unsigned short)b)); }
     static constexpr uint32_t kSign = 0x8000u;
@@ -127,199 +153,230 @@ __device__ __forceinline__ uint4 load16(const T* x, int at, int vocab) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The largest keys of a warp, in order: number r of them in lane r % 32, register r / 32.
-template <int kRegs>
-struct TopList {
-    uint64_t key[kRegs];
-    __device__ __forceinline__ void clear() {
+// A step's values that are not finite, or huge: sums of the others and of the huge ones.
+struct Sums {
+    float c, sum;      // sum of 2^(x log2 e - c)
+    float huge, huge_sum;  // sum of exp(x - huge) over |x| >= kHuge
+};
+template <typename T>
+__device__ __noinline__ float slow_sums(const T* x, int at, int vocab, Sums& s) {
+    uint32_t words[kLoads * 4];
 #pragma unroll
-        for (int i = 0; i < kRegs; ++i) key[i] = 0;
+    for (int i = 0; i < kLoads; ++i) {
+        const uint4 w = load16(x, at + i * 32 * (int)(16 / sizeof(T)), vocab);
+        words[4 * i] = w.x; words[4 * i + 1] = w.y; words[4 * i + 2] = w.z; words[4 * i + 3] = w.w;
     }
-    // The r-th key, for all lanes.
-    __device__ __forceinline__ uint64_t at(int r) const {
-        uint64_t k = key[0];
+    float rest = kNegInf, high = kNegInf;
+    constexpr int kPer = Logit<T>::kPer;
 #pragma unroll
-        for (int i = 1; i < kRegs; ++i) k = (r >> 5) == i ? key[i] : k;
-        return __shfl_sync(0xffffffffu, k, r & 31);
-    }
-    // Puts k (the same in all lanes) in its place.
-    __device__ __forceinline__ void insert(uint64_t k, int lane) {
-        uint64_t carry = k;  // what enters register i at its first lane from its place on
-        int before = 0;
+    for (int i = 0; i < kLoads * 4; ++i) {
+        float v[kPer];
+        Logit<T>::unpack(words[i], v);
 #pragma unroll
-        for (int i = 0; i < kRegs; ++i) before += __popc(__ballot_sync(0xffffffffu, key[i] > k));
-#pragma unroll
-        for (int i = 0; i < kRegs; ++i) {
-            const uint64_t up = __shfl_up_sync(0xffffffffu, key[i], 1), last = __shfl_sync(0xffffffffu, key[i], 31);
-            const int r = 32 * i + lane;
-            if (r > before) key[i] = lane == 0 ? carry : up;
-            if (r == before) key[i] = k;
-            carry = last;
+        for (int e = 0; e < kPer; ++e) {
+            const float y = usable(v[e]);
+            if (fabsf(y) < kHuge) rest = fmaxf(rest, y);
+            else high = fmaxf(high, y);
         }
     }
-};
+    const float c_new = fmaxf(s.c, ceilf(rest * kLog2e)), h_new = fmaxf(s.huge, high);
+    if (s.c > kNegInf) s.sum *= exp2_fast(s.c - c_new);
+    if (s.huge > kNegInf) s.huge_sum *= exp2_fast((s.huge - h_new) * kLog2e);
+    s.c = c_new;
+    s.huge = h_new;
+#pragma unroll
+    for (int i = 0; i < kLoads * 4; ++i) {
+        float v[kPer];
+        Logit<T>::unpack(words[i], v);
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+            const float y = usable(v[e]);
+            if (fabsf(y) < kHuge) s.sum += exp2_fast(fmaf(y, kLog2e, -c_new));
+            else if (y > kNegInf) s.huge_sum += exp2_fast((y - h_new) * kLog2e);
+        }
+    }
+    return fmaxf(rest, high);
+}
 
-template <typename T, int kRegs>
-__global__ void __launch_bounds__(kScanWarps * 32) beam_scan_kernel(const BeamParams p) {
-    constexpr int kVec = 16 / sizeof(T);
+// kBound groups of lanes give the bound; kBound >= k + 1.
+template <typename T, int kBound>
+__global__ void __launch_bounds__(kScanThreads, 4) beam_scan_kernel(const BeamParams p) {
+    constexpr int kVec = 16 / sizeof(T), kPer = Logit<T>::kPer;
+    constexpr int kStep = kLoads * 32 * kVec;
+    constexpr int kGroupLanes = kScanThreads / kBound;
+    __shared__ float s_most[kMaxSteps][kScanThreads];
+    __shared__ float s_group[kBound];
+    __shared__ float4 s_sums[kScanWarps];
+    __shared__ uint64_t s_key[kBuffer], s_red[kScanWarps];
+    __shared__ int s_keys;
     cudaTriggerProgrammaticLaunchCompletion();
-    const int lane = threadIdx.x & 31;
-    const int64_t unit = (int64_t)blockIdx.x * kScanWarps + (threadIdx.x >> 5);
-    const int64_t row = unit / p.segs;
-    if (row >= (int64_t)p.batch * p.beams) return;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int64_t row = blockIdx.x / p.segs;
     if (p.done && p.done[row]) return;  // beam_join takes its one candidate from the scores
-    const int seg = (int)(unit - row * p.segs), c1 = p.k + 1;
+    const int seg = (int)(blockIdx.x - row * p.segs), c1 = p.k + 1;
     const T* x = static_cast<const T*>(p.logits) + row * p.stride;
     // Loads are aligned: the row's first lies up to kVec - 1 elements before it.
     const int skew = (int)(((uintptr_t)x % 16) / sizeof(T));
     const int begin = seg * p.seg_len - skew;
-    const int end = min(p.vocab, begin + p.seg_len);
-    constexpr int kStep = kLoads * 32 * kVec;
+    const int end = p.vocab - begin < p.seg_len ? p.vocab : begin + p.seg_len;
+    const int first = begin + warp * kStep;  // steps of the warps take turns
+    constexpr int kTurn = kScanWarps * kStep;
 
-    TopList<kRegs> top;
-    top.clear();
-    uint64_t worst = 1;            // keys below it are not wanted; the list's last once it is full
-    float worst_value = kNegInf;
-    float c = kNegInf, sum = 0.f;  // sum of 2^(x log2 e - c) of this lane's logits
-    float huge = kNegInf, huge_sum = 0.f;
+    Sums s{kNegInf, 0.f, kNegInf, 0.f};
+    float group = kNegInf;
+    if (tid == 0) s_keys = 0;
 
     uint4 next[kLoads];
+    auto load = [&](int at) {
+        if (at >= 0 && at + kStep <= p.vocab) {
+            const uint4* src = reinterpret_cast<const uint4*>(x + at) + lane;
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) next[i] = load16(x, begin + (i * 32 + lane) * kVec, p.vocab);
-    for (int at = begin; at < end; at += kStep) {
-        float v[kLoads][kVec];
+            for (int i = 0; i < kLoads; ++i) next[i] = __ldcs(src + 32 * i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) next[i] = load16(x, at + (i * 32 + lane) * kVec, p.vocab);
+        }
+    };
+    if (first < end) load(first);
+    int steps = 0;
+    for (int at = first; at < end; at += kTurn, ++steps) {
+        uint32_t w[kLoads * 4];
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const uint32_t w[4] = {next[i].x, next[i].y, next[i].z, next[i].w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) Logit<T>::unpack(w[k], &v[i][k * (kVec / 4)]);
+            w[4 * i] = next[i].x; w[4 * i + 1] = next[i].y; w[4 * i + 2] = next[i].z; w[4 * i + 3] = next[i].w;
         }
-        if (at + kStep < end) {
+        if (at + kTurn < end) load(at + kTurn);
+        uint32_t mw = w[0];
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i) next[i] = load16(x, at + kStep + (i * 32 + lane) * kVec, p.vocab);
+        for (int i = 1; i < kLoads * 4; ++i) mw = Logit<T>::larger(mw, w[i]);
+        float m;
+        {
+            float v[kPer];
+            Logit<T>::unpack(mw, v);
+            m = kPer == 2 ? fmaxf(v[0], v[kPer - 1]) : v[0];
         }
-        float most[kLoads];  // of each load
-        float part = 0.f;
-        auto take = [&]() {
-            float m = kNegInf;
+        const float c_new = fmaxf(s.c, ceilf(m * kLog2e));
+        const float ref = c_new == kNegInf ? 0.f : c_new;
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                most[i] = v[i][0];
+        for (int i = 0; i < kLoads * 4; ++i) {
+            float v[kPer];
+            Logit<T>::unpack(w[i], v);
 #pragma unroll
-                for (int e = 1; e < kVec; ++e) most[i] = fmaxf(most[i], v[i][e]);
-                m = fmaxf(m, most[i]);
-            }
-            return m;
-        };
-        float m = take();
-        float c_new = fmaxf(c, ceilf(m * kLog2e));
-        float ref = c_new == kNegInf ? 0.f : c_new;
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i)
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) part += exp2f(fmaf(v[i][e], kLog2e, -ref));
-        if (__any_sync(0xffffffffu, !(m < kHuge) || part != part || (m < -kHuge && m > kNegInf))) {
-            // Something is not finite, or huge.
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i)
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) v[i][e] = usable(v[i][e]);
-            m = take();
-            float rest = kNegInf, high = kNegInf;  // largest of the others, and of the huge ones
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i)
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) {
-                    const float y = v[i][e];
-                    if (fabsf(y) < kHuge) rest = fmaxf(rest, y);
-                    else high = fmaxf(high, y);
-                }
-            c_new = fmaxf(c, ceilf(rest * kLog2e));
-            ref = c_new == kNegInf ? 0.f : c_new;
-            const float h_new = fmaxf(huge, high);
-            if (huge > kNegInf) huge_sum *= exp2f((huge - h_new) * kLog2e);
-            huge = h_new;
-            part = 0.f;
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i)
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) {
-                    const float y = v[i][e];
-                    if (fabsf(y) < kHuge) part += exp2f(fmaf(y, kLog2e, -ref));
-                    else if (y > kNegInf) huge_sum += exp2f((y - huge) * kLog2e);
-                }
+            for (int e = 0; e < kPer; ++e) acc[(i * kPer + e) & 3] += exp2_fast(fmaf(v[e], kLog2e, -ref));
         }
-        if (c > kNegInf) sum *= exp2f(c - ref);
-        c = c_new;
-        sum += part;
-
-        if (at == begin) {
-            // A bound for the list's last value from maxima of disjoint parts of this step.
-            if (kRegs == 1) {
-                int larger = 0;
-#pragma unroll 8
-                for (int i = 0; i < 32; ++i) {
-                    const float y = __shfl_sync(0xffffffffu, m, i);
-                    larger += y > m || (y == m && i < lane);
-                }
-                const unsigned who = __ballot_sync(0xffffffffu, larger == c1 - 1);
-                if (who) worst_value = __shfl_sync(0xffffffffu, m, __ffs(who) - 1);
-            } else {
-                int larger[kLoads] = {};
-                for (int i = 0; i < 32; ++i)
-#pragma unroll
-                    for (int j = 0; j < kLoads; ++j) {
-                        const float y = __shfl_sync(0xffffffffu, most[j], i);
-#pragma unroll
-                        for (int k = 0; k < kLoads; ++k) larger[k] += y > most[k] || (y == most[k] && (i < lane || (i == lane && j < k)));
-                    }
-#pragma unroll
-                for (int k = 0; k < kLoads; ++k) {
-                    const unsigned who = __ballot_sync(0xffffffffu, larger[k] == c1 - 1);
-                    if (who) worst_value = __shfl_sync(0xffffffffu, most[k], __ffs(who) - 1);
-                }
-            }
-            if (worst_value > kNegInf) worst = (uint64_t)ordered(worst_value) << 32;
+        const float part = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+        if (!(m < kHuge) || part != part || (m < -kHuge && m > kNegInf)) {
+            m = slow_sums<T>(x, at + lane * kVec, p.vocab, s);
+        } else {
+            if (s.c > kNegInf) s.sum *= exp2_fast(s.c - ref);
+            s.c = c_new;
+            s.sum += part;
         }
-        if (!__any_sync(0xffffffffu, m >= worst_value && m > kNegInf)) continue;
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            if (!__any_sync(0xffffffffu, most[i] >= worst_value)) continue;
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) {
-                const uint64_t k = v[i][e] > kNegInf ? key_of(v[i][e], (uint32_t)(at + (i * 32 + lane) * kVec + e)) : 0;
-                unsigned who = __ballot_sync(0xffffffffu, k > worst);
-                while (who) {
-                    const uint64_t one = __shfl_sync(0xffffffffu, k, __ffs(who) - 1);
-                    top.insert(one, lane);
-                    const uint64_t last = top.at(c1 - 1);
-                    if (last > worst) worst = last;
-                    who &= who - 1;
-                    who &= __ballot_sync(0xffffffffu, k > worst);
-                }
-            }
-            worst_value = worst >> 32 ? key_value(worst) : kNegInf;
-        }
+        s_most[steps][tid] = m;
+        group = fmaxf(group, m);
     }
+    const float mine = group;  // the largest of this lane
 
-    // The lanes' sums put together.
-    float c_all = c, h_all = huge;
+    // Sums and group maxima put together.
+#pragma unroll
+    for (int o = 1; o < kGroupLanes; o <<= 1) group = fmaxf(group, __shfl_xor_sync(0xffffffffu, group, o));
+    if (tid % kGroupLanes == 0) s_group[tid / kGroupLanes] = group;
+    float c_all = s.c, h_all = s.huge;
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
         c_all = fmaxf(c_all, __shfl_xor_sync(0xffffffffu, c_all, o));
         h_all = fmaxf(h_all, __shfl_xor_sync(0xffffffffu, h_all, o));
     }
-    sum = c > kNegInf ? sum * exp2f(c - c_all) : 0.f;
-    huge_sum = huge > kNegInf ? huge_sum * exp2f((huge - h_all) * kLog2e) : 0.f;
+    float sum = s.c > kNegInf ? s.sum * exp2_fast(s.c - c_all) : 0.f;
+    float huge_sum = s.huge > kNegInf ? s.huge_sum * exp2_fast((s.huge - h_all) * kLog2e) : 0.f;
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
         sum += __shfl_xor_sync(0xffffffffu, sum, o);
         huge_sum += __shfl_xor_sync(0xffffffffu, huge_sum, o);
     }
-    if (lane == 0) p.part[unit] = make_float4(c_all, sum, h_all, huge_sum);
+    if (lane == 0) s_sums[warp] = make_float4(c_all, sum, h_all, huge_sum);
+    __syncthreads();
+    if (tid == 0) {
+        float4 a = s_sums[0];
+        for (int i = 1; i < kScanWarps; ++i) {
+            const float4 y = s_sums[i];
+            const float c = fmaxf(a.x, y.x), h = fmaxf(a.z, y.z);
+            a.y = (a.x > kNegInf ? a.y * exp2_fast(a.x - c) : 0.f) + (y.x > kNegInf ? y.y * exp2_fast(y.x - c) : 0.f);
+            a.w = (a.z > kNegInf ? a.w * exp2_fast((a.z - h) * kLog2e) : 0.f) + (y.z > kNegInf ? y.w * exp2_fast((y.z - h) * kLog2e) : 0.f);
+            a.x = c;
+            a.z = h;
+        }
+        p.part[blockIdx.x] = a;
+    }
+    // The c1-th largest group maximum; every warp finds it for itself.
+    float bound = kNegInf;
 #pragma unroll
-    for (int i = 0; i < kRegs; ++i)
-        if (32 * i + lane < c1) p.cand[unit * c1 + 32 * i + lane] = top.key[i];
+    for (int r = 0; r < kBound / 32; ++r) {
+        const int me = r * 32 + lane;
+        const float g = s_group[me];
+        int larger = 0;
+#pragma unroll 8
+        for (int i = 0; i < kBound; ++i) {
+            const float y = s_group[i];
+            larger += y > g || (y == g && i < me);
+        }
+        const unsigned who = __ballot_sync(0xffffffffu, larger == c1 - 1);
+        if (who) bound = __shfl_sync(0xffffffffu, g, __ffs(who) - 1);
+    }
+    // The values of this lane that reach the bound.
+    auto each = [&](auto f) {
+        if (mine < bound || mine == kNegInf) return;
+        for (int t = 0; t < steps; ++t) {
+            if (s_most[t][tid] < bound) continue;
+            const int at = first + t * kTurn + lane * kVec;
+#pragma unroll 1
+            for (int i = 0; i < kLoads; ++i) {
+                const uint4 u = load16(x, at + i * 32 * kVec, p.vocab);
+                const uint32_t q[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float v[kPer];
+                    Logit<T>::unpack(q[j], v);
+#pragma unroll
+                    for (int e = 0; e < kPer; ++e)
+                        if (v[e] >= bound && fabsf(v[e]) < INFINITY)
+                            f(key_of(v[e], (uint32_t)(at + i * 32 * kVec + j * kPer + e)));
+                }
+            }
+        }
+    };
+    each([&](uint64_t k) {
+        const int place = atomicAdd(&s_keys, 1);
+        if (place < kBuffer) s_key[place] = k;
+    });
+    __syncthreads();
+    uint64_t* cand = p.cand + (int64_t)blockIdx.x * c1;
+    const int n = s_keys;
+    if (n <= kBuffer) {
+        for (int i = tid; i < n; i += kScanThreads) {
+            const uint64_t k = s_key[i];
+            int larger = 0;
+            for (int j = 0; j < n; ++j) larger += s_key[j] > k;
+            if (larger < c1) cand[larger] = k;
+        }
+        for (int r = n + tid; r < c1; r += kScanThreads) cand[r] = 0;
+    } else {
+        // Many equal values: c1 rounds of the largest key below the last one.
+        uint64_t under = ~0ull;
+        for (int r = 0; r < c1; ++r) {
+            uint64_t best = 0;
+            each([&](uint64_t k) { best = k < under && k > best ? k : best; });
+            best = warp_max(best);
+            __syncthreads();
+            if (lane == 0) s_red[warp] = best;
+            __syncthreads();
+            best = 0;
+            for (int i = 0; i < kScanWarps; ++i) best = s_red[i] > best ? s_red[i] : best;
+            if (tid == 0) cand[r] = best;
+            under = best;
+        }
+    }
 }
 
 struct Select {
@@ -413,20 +470,31 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamParam
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t b = blockIdx.x, row0 = b * p.beams;
     const int c1 = p.k + 1;
+    const uint32_t lists = (uint32_t)p.beams * p.segs, keys = lists * c1, per_beam = (uint32_t)p.segs * c1;
+    const uint64_t* cand = p.cand + row0 * p.segs * c1;
+    constexpr int kKeep = 4;  // keys of a thread that stay in registers
 
     for (int w = tid; w < p.beams; w += kJoinThreads) {
         score[w] = p.scores[row0 + w];
         done[w] = p.done && p.done[row0 + w];
     }
     cudaGridDependencySynchronize();
-    // lse of each beam: the segments' maxima and sums put together, one warp a beam.
+    uint64_t keep[kKeep];
+    const bool kept = keys <= kKeep * kJoinThreads;
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) keep[i] = kept && tid + i * kJoinThreads < keys ? cand[tid + i * kJoinThreads] : 0;
+    const uint64_t edge0 = (uint32_t)tid < lists ? cand[(uint32_t)tid * c1 + p.k] : 0;
+    // lse of each beam: the segments' sums put together, one warp a beam.
     for (int w = warp; w < p.beams; w += kJoinThreads / 32) {
         if (p.done && p.done[row0 + w]) continue;
         const float4* part = p.part + (row0 + w) * p.segs;
-        float c = kNegInf, h = kNegInf, sum = 0.f, huge = 0.f;
-        for (int i = lane; i < p.segs; i += 32) {
-            c = fmaxf(c, part[i].x);
-            h = fmaxf(h, part[i].z);
+        const float4 none = make_float4(kNegInf, 0.f, kNegInf, 0.f);
+        const float4 mine = lane < p.segs ? part[lane] : none;
+        float c = mine.x, h = mine.z, sum = 0.f, huge = 0.f;
+        for (int i = lane + 32; i < p.segs; i += 32) {
+            const float4 y = part[i];
+            c = fmaxf(c, y.x);
+            h = fmaxf(h, y.z);
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
@@ -434,7 +502,7 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamParam
             h = fmaxf(h, __shfl_xor_sync(0xffffffffu, h, o));
         }
         for (int i = lane; i < p.segs; i += 32) {
-            const float4 y = part[i];
+            const float4 y = i == lane ? mine : part[i];
             if (y.x > kNegInf) sum += y.y * exp2f(y.x - c);
             if (y.z > kNegInf) huge += y.w * exp2f((y.z - h) * kLog2e);
         }
@@ -450,23 +518,34 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamParam
     }
     __syncthreads();
 
-    const uint32_t lists = (uint32_t)p.beams * p.segs;
     auto total_key = [&](int w, float x, uint32_t t) -> uint64_t {
         const float total = score[w] + (x - lse[w]);
         return total > kNegInf ? key_of(total, (uint32_t)w * p.vocab + t) : 0;
     };
-    auto each = [&](auto f) {
-        for (uint32_t i = tid; i < lists * c1; i += kJoinThreads) {
-            const uint32_t list = i / c1;
-            const int w = list / p.segs;
-            if (done[w]) continue;
-            const uint64_t k = p.cand[row0 * p.segs * c1 + i];
-            if (k) f(total_key(w, key_value(k), key_index(k)));
-        }
-        if (tid < p.beams && done[tid] && score[tid] > kNegInf)
-            f(key_of(score[tid], (uint32_t)tid * p.vocab + p.eos));
+    auto total_of = [&](uint32_t i, uint64_t k) -> uint64_t {  // key number i as a total
+        const int w = i / per_beam;
+        return k && !done[w] ? total_key(w, key_value(k), key_index(k)) : 0;
     };
-    block_select(s, p.k, each, best);
+    const uint64_t ended = tid < p.beams && done[tid] && score[tid] > kNegInf
+                               ? key_of(score[tid], (uint32_t)tid * p.vocab + p.eos) : 0;
+    if (kept) {
+#pragma unroll
+        for (int i = 0; i < kKeep; ++i) keep[i] = total_of(tid + i * kJoinThreads, keep[i]);
+        block_select(s, p.k, [&](auto f) {
+#pragma unroll
+            for (int i = 0; i < kKeep; ++i)
+                if (keep[i]) f(keep[i]);
+            if (ended) f(ended);
+        }, best);
+    } else {
+        block_select(s, p.k, [&](auto f) {
+            for (uint32_t i = tid; i < keys; i += kJoinThreads) {
+                const uint64_t k = total_of(i, cand[i]);
+                if (k) f(k);
+            }
+            if (ended) f(ended);
+        }, best);
+    }
 
     // What the segments left out (see the head of this file): any total that would still
     // come before the k-th best is put in its place, largest first.
@@ -475,7 +554,7 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamParam
         __syncthreads();
         if (list0 + tid < lists) {
             const int w = (list0 + tid) / p.segs;
-            const uint64_t edge = done[w] ? 0 : p.cand[(row0 * p.segs + list0 + tid) * c1 + p.k];
+            const uint64_t edge = done[w] ? 0 : list0 == 0 ? edge0 : cand[(list0 + tid) * c1 + p.k];
             if (edge) {  // else nothing was left out
                 const uint64_t could = total_key(w, next_below<T>(key_value(edge)), 0);
                 // Whatever its index, it may come before the last.
@@ -489,7 +568,7 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamParam
             uint64_t more = 0;
             for (int a = 0; a < agains; ++a) {
                 const int list = again[a], w = list / p.segs, seg = list - w * p.segs;
-                const uint64_t edge = p.cand[(row0 * p.segs + list) * c1 + p.k];
+                const uint64_t edge = cand[(uint32_t)list * c1 + p.k];
                 const T* x = static_cast<const T*>(p.logits) + (row0 + w) * p.stride;
                 const int skew = (int)(((uintptr_t)x % 16) / sizeof(T));
                 const int lo = max(0, seg * p.seg_len - skew), hi = min(p.vocab, (seg + 1) * p.seg_len - skew);
@@ -525,12 +604,11 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamParam
 
 template <typename T>
 cudaError_t launch_type(const BeamParams& p, cudaStream_t stream) {
-    const int64_t warps = (int64_t)p.batch * p.beams * p.segs;
-    const dim3 grid((unsigned)((warps + kScanWarps - 1) / kScanWarps));
+    const dim3 grid((unsigned)((int64_t)p.batch * p.beams * p.segs));
     if (p.k < 32)
-        beam_scan_kernel<T, 1><<<grid, kScanWarps * 32, 0, stream>>>(p);
+        beam_scan_kernel<T, 32><<<grid, kScanThreads, 0, stream>>>(p);
     else
-        beam_scan_kernel<T, 3><<<grid, kScanWarps * 32, 0, stream>>>(p);
+        beam_scan_kernel<T, 128><<<grid, kScanThreads, 0, stream>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -547,14 +625,25 @@ cudaError_t launch_type(const BeamParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-// Values of a warp's segment: whole steps, the fewest with which all warps are resident at
-// once (five CTAs of four warps an SM by their registers), at most 16.
+// Values of a CTA's segment: whole steps of all its warps.  The fullest SM has n = ceil(CTAs /
+// SMs) CTAs, each as long as its steps and about three more at its ends, and issues 0.036 of
+// its peak for each resident warp up to 0.8 of it (measured on 32 x 8 rows of 131072 bf16
+// values).
 int beam_seg_len(int64_t rows, int32_t vocab, int elem, int sm_count) {
-    const int step = kLoads * 32 * 16 / elem;
-    const int64_t steps = (vocab + step - 1) / step;
-    int each = 1;
-    while (each < 16 && rows * ((steps + each - 1) / each) > 20ll * sm_count) ++each;
-    return step * each;
+    const int turn = kScanWarps * kLoads * 32 * 16 / elem;
+    int best = 1;
+    double least = 1e30;
+    for (int each = 1; each <= kMaxSteps; ++each) {
+        const int64_t segs = (vocab + (int64_t)each * turn - 1) / ((int64_t)each * turn), ctas = rows * segs;
+        const int64_t n = (ctas + sm_count - 1) / sm_count;
+        const double rate = 0.036 * kScanWarps * (double)(n < 4 ? n : 4);
+        const double cost = (double)n * (each + 3) / (rate < 0.8 ? rate : 0.8);
+        if (cost < least) {
+            least = cost;
+            best = each;
+        }
+    }
+    return turn * best;
 }
 
 cudaError_t launch_beam(const BeamParams& p, cudaStream_t stream) {

@@ -435,8 +435,8 @@ kda_status kda_beam_select(int32_t batch, int32_t beams, int32_t vocab, int32_t 
     return guarded([&] {
         if (batch < 0 || beams < 1 || beams > 64 || num_out < 1 || num_out > 64)
             return fail(KDA_ERR_INVALID_ARGUMENT, "batch must be >= 0, beams and num_out in [1, 64] (got %d, %d, %d)", batch, beams, num_out);
-        if (vocab < 1 || (int64_t)beams * vocab > 0x7fffffff || (int64_t)batch * beams > (1 << 30))
-            return fail(KDA_ERR_INVALID_ARGUMENT, "vocab must be >= 1, beams * vocab at most 2^31 - 1, batch * beams at most 2^30 (got %d)", vocab);
+        if (vocab < 1 || (int64_t)beams * vocab > (1 << 30) || (int64_t)batch * beams > (1 << 30))
+            return fail(KDA_ERR_INVALID_ARGUMENT, "vocab must be >= 1, beams * vocab at most 2^30, batch * beams at most 2^30 (got %d)", vocab);
         if (logits_dtype != KDA_LOGITS_F32 && logits_dtype != KDA_LOGITS_BF16 && logits_dtype != KDA_LOGITS_F16)
             return fail(KDA_ERR_INVALID_ARGUMENT, "unknown logits_dtype %d", logits_dtype);
         if (logits_stride < vocab || logits_stride > (int64_t)1 << 32)

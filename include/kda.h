@@ -423,7 +423,7 @@ kda_status kda_kvcache_attention(const kda_kvcache* cache, const void* q, int32_
  *               -inf, -1, -1
  *   new_done    uint8 [batch][num_out] or NULL: 1 where the token is eos, the parent was
  *               finished, or the place is empty
- * 1 <= beams, num_out <= 64; beams * vocab <= 2^31 - 1; outputs must not overlap inputs. */
+ * 1 <= beams, num_out <= 64; beams * vocab <= 2^30; outputs must not overlap inputs. */
 #define KDA_LOGITS_F32 0
 #define KDA_LOGITS_BF16 1
 #define KDA_LOGITS_F16 2
