@@ -47,11 +47,10 @@ struct PagePlan {
     int32_t* new_refs;
     int32_t* page_map;        // compact
     int32_t* num_live;        // compact
-    // scratch (page_plan_scratch ints)
+    // scratch
     int32_t* held;            // [pages]
     int32_t* first;           // [pages]
     int32_t* list;            // [pages]: free pages in order
-    int32_t* counts;          // [32]
     int32_t* copies;          // [1]: pairs in src / dst
     int32_t* src;             // [rows * width] (compact: [pages])
     int32_t* dst;

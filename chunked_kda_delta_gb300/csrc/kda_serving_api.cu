@@ -137,8 +137,7 @@ kda_status run_plan(kda::PagePlan p, int mode, bool compact, const kda::PoolSet&
     char* ws = nullptr;
     if ((st = scratch(dev, stream, (64 + 3 * (size_t)p.pages + 2 * pairs) * 4, &ws)) != KDA_OK) return st;
     int32_t* at = reinterpret_cast<int32_t*>(ws);
-    p.counts = at;
-    p.copies = at + 32;
+    p.copies = at;
     p.held = at + 64;
     p.first = p.held + p.pages;
     p.list = p.first + p.pages;

@@ -109,7 +109,33 @@ def test_fork_large_plan_matches_loops():
     K.kda_get_device_status()
 
 
-@pytest.mark.parametrize("rows,width,pages", [(3, 4, 20), (1, 1, 1), (40, 130, 9000), (5, 3, 4)])
+def test_more_pages_than_shared_memory_holds():
+    rng = np.random.default_rng(6)
+    rows, width, pages = 50, 40, 140001
+    order = rng.permutation(pages)
+    tables = order[: rows * width].reshape(rows, width).copy()
+    tables[1:, :9] = tables[0, :9]
+    refs = np.bincount(tables.ravel(), minlength=pages)
+    parents = rng.integers(0, rows, rows)
+    lens = np.full(rows, 9 * 16 + 3)
+    want_t, want_r, copies = ref.fork(tables, refs, parents, lens, 16)
+    pool = torch.arange(pages, device="cuda", dtype=torch.int32).view(-1, 1)
+    nt, nr = K.kda_pages_fork(dev(tables), dev(refs), dev(parents), lens=dev(lens), page_tokens=16, pools=[pool])
+    assert np.array_equal(nt.cpu().numpy(), want_t) and np.array_equal(nr.cpu().numpy(), want_r)
+    want = np.arange(pages)
+    for a, b in copies:
+        want[b] = a
+    assert np.array_equal(pool[:, 0].cpu().numpy(), want)
+    want_t, want_r, want_m, n, _ = ref.compact(tables, refs)
+    ct, cr, pm, live = K.kda_pages_compact(dev(tables), dev(refs))
+    assert np.array_equal(ct.cpu().numpy(), want_t) and np.array_equal(cr.cpu().numpy(), want_r)
+    assert np.array_equal(pm.cpu().numpy(), want_m) and live.item() == n
+    want_t, want_r = ref.alloc(tables[:, :20], refs, np.full(rows, 20))
+    at, ar = K.kda_pages_alloc(dev(np.ascontiguousarray(tables[:, :20])), dev(refs), dev(np.full(rows, 20)))
+    assert np.array_equal(at.cpu().numpy(), want_t) and np.array_equal(ar.cpu().numpy(), want_r)
+
+
+@pytest.mark.parametrize("rows,width,pages", [(3, 4, 20), (1, 1, 1), (40, 130, 9000), (5, 3, 4), (9, 30, 16385), (9, 30, 32768), (9, 30, 65537)])
 def test_alloc_and_free(rows, width, pages):
     rng = np.random.default_rng(rows)
     tables = np.full((rows, width), -1)
