@@ -5,6 +5,14 @@
 // codes = e4m3(x / s).  HBM-bound: 2 bytes read and 1 written per value.  The new values stay
 // in registers between the maximum and the quotients, so they are read once.  A block owns a
 // (page, head) of k or v, so no two write the same scale.
+//
+// The definition's quotient is the correctly rounded one.  Values of a block share their
+// divisor, so it is formed from the correctly rounded reciprocal r by Markstein's theorem
+// (IBM J. Res. Dev. 34, 1990): q = rn(x r), then rn(q + rn(x - q s) r) is the correctly rounded
+// x / s wherever no intermediate leaves the normal range and s's fraction is not all
+// ones -- three operations a value instead of a full division (86 us for 30.7k tokens of 8
+// heads with divisions, where instructions and not bytes were the bound).  Other scales,
+// and blocks with values that are not finite, take the division.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -48,16 +56,24 @@ __device__ __forceinline__ float2 values2(uint32_t codes) {
     return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// Largest finite magnitude; `odd` is set where a value is not finite.
-__device__ __forceinline__ float largest(const float (&x)[8], bool& odd) {
+// Largest magnitude of eight values as packed; +inf or NaN patterns compare above all finite ones.
+template <typename T>
+__device__ __forceinline__ uint32_t largest2(const uint4& w) {  // halves: largest of the even and the odd values
+    const uint32_t m = 0x7fff7fffu;
+    return __vmaxu2(__vmaxu2(w.x & m, w.y & m), __vmaxu2(w.z & m, w.w & m));
+}
+template <typename T>
+__device__ __forceinline__ float top_of(uint32_t halves) {  // as a float: inf or NaN where some value is
+    const uint32_t u = max(halves & 0xffffu, halves >> 16);
+    return Act<T>::two(u).x;
+}
+// Largest finite magnitude.
+__device__ __forceinline__ float largest(const float (&x)[8]) {
     float a = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const float m = fabsf(x[i]);
-        if (m < INFINITY)
-            a = fmaxf(a, m);
-        else
-            odd = true;
+        if (m < INFINITY) a = fmaxf(a, m);
     }
     return a;
 }
@@ -68,10 +84,25 @@ __device__ __forceinline__ float quotient(float x, float s) {
     if (fabsf(x) == INFINITY) return copysignf(kCodeMax, x);
     return s > 0.f ? __fdiv_rn(x, s) : 0.f;
 }
+// Whether the short quotient is exact for every finite |x| <= 448 s: quotients too small for it
+// (|x| below 2^-100, or x / s below the least code) round to the code 0 all the same.
+__device__ __forceinline__ bool short_division(float s) {
+    return s > 0x1p-80f && s < 0x1p80f && (__float_as_uint(s) & 0x7fffffu) != 0x7fffffu;
+}
+__device__ __forceinline__ float short_quotient(float x, float s, float r) {
+    const float q = __fmul_rn(x, r), y = fmaf(fmaf(-q, s, x), r, q);
+    return __uint_as_float(__float_as_uint(y) | (__float_as_uint(x) & 0x80000000u));  // -0 / s is -0
+}
 __device__ __forceinline__ uint2 encode(const float (&x)[8], float s) {
     uint32_t c[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) c[i] = code2(quotient(x[2 * i], s), quotient(x[2 * i + 1], s));
+    return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+}
+__device__ __forceinline__ uint2 encode_short(const float (&x)[8], float s, float r) {
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = code2(short_quotient(x[2 * i], s, r), short_quotient(x[2 * i + 1], s, r));
     return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
 // Eight older codes of scale `was` rounded again for scale `now`.
@@ -108,12 +139,13 @@ __global__ void __launch_bounds__(kStepWarps * 32) append_step_kernel(const __gr
     const bool mine = lane < kLanes;
     float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     const T* src = static_cast<const T*>(p.x[which]) + row * p.stride[which] + (int64_t)head * kDim;
-    if (mine) unpack<T>(reinterpret_cast<const uint4*>(src)[lane], x);
-    bool odd = false;
-    float a = largest(x, odd);
+    uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+    if (mine) raw = reinterpret_cast<const uint4*>(src)[lane];
+    unpack<T>(raw, x);
+    if (!(top_of<T>(largest2<T>(raw)) < INFINITY)) report(c.status, kStatusNonfinite);
+    float a = largest(x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-    if (odd) report(c.status, kStatusNonfinite);
 
     const int off = len % c.page_tokens;
     const int64_t block = (int64_t)page * c.heads + head;
@@ -187,21 +219,28 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
     const T* src = static_cast<const T*>(p.x[which]) + (begin + first - len) * stride + (int64_t)head * kDim;
     const int at = tid % kLanes, t0 = tid / kLanes;
 
+    bool finite = true;  // all values of this thread
     uint4 raw[kPasses];
 #pragma unroll
     for (int k = 0; k < kPasses; ++k) {
         const int t = t0 + k * kRows;
         raw[k] = t < n ? __ldcs(reinterpret_cast<const uint4*>(src + t * stride) + at) : make_uint4(0u, 0u, 0u, 0u);
     }
-    float a = 0.f;
-    bool odd = false;
+    uint32_t most = 0;
 #pragma unroll
-    for (int k = 0; k < kPasses; ++k) {
-        float x[8];
-        unpack<T>(raw[k], x);
-        a = fmaxf(a, largest(x, odd));
+    for (int k = 0; k < kPasses; ++k) most = __vmaxu2(most, largest2<T>(raw[k]));
+    float a = top_of<T>(most);
+    if (!(a < INFINITY)) {
+        report(c.status, kStatusNonfinite);
+        a = 0.f;
+#pragma unroll
+        for (int k = 0; k < kPasses; ++k) {
+            float x[8];
+            unpack<T>(raw[k], x);
+            a = fmaxf(a, largest(x));
+        }
+        finite = false;
     }
-    if (odd) report(c.status, kStatusNonfinite);
 #pragma unroll
     for (int o = 16; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
     if (lane == 0) red[tid >> 5] = a;
@@ -222,12 +261,23 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
         }
     }
     if (tid == 0) *scale = s;
+    if (finite && short_division(s)) {
+        const float r = __frcp_rn(s);
 #pragma unroll
-    for (int k = 0; k < kPasses; ++k) {
-        const int t = t0 + k * kRows;
-        float x[8];
-        unpack<T>(raw[k], x);
-        if (t < n) reinterpret_cast<uint2*>(codes + (int64_t)(off + t) * kDim)[at] = encode(x, s);
+        for (int k = 0; k < kPasses; ++k) {
+            const int t = t0 + k * kRows;
+            float x[8];
+            unpack<T>(raw[k], x);
+            if (t < n) reinterpret_cast<uint2*>(codes + (int64_t)(off + t) * kDim)[at] = encode_short(x, s, r);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < kPasses; ++k) {
+            const int t = t0 + k * kRows;
+            float x[8];
+            unpack<T>(raw[k], x);
+            if (t < n) reinterpret_cast<uint2*>(codes + (int64_t)(off + t) * kDim)[at] = encode(x, s);
+        }
     }
 }
 

@@ -23,10 +23,14 @@
 // enters as its ratio to the largest one met, so weights stay in [0, 1].  Running maximum,
 // sums, outputs and the joined parts are fp32.
 //
-// Work split: every item has one tile (128 keys, 32 a warp) per 128 cached tokens; the CTAs
-// take equal contiguous shares of all tiles of all items in order, however long the rows
-// are.  An item that lies in one share is written at once; the parts of the others are joined
-// by a second launch.
+// Work split: warps work alone.  The items' cached tokens, cut into slabs of 32 (16 where an
+// item has 32 query rows), are numbered through all items; every resident warp takes an equal
+// contiguous share, however long the rows are.  An item inside one share is written at once;
+// the parts of the others, in the layout of the product's fragments, are joined by a second
+// launch.  (With four warps sharing each tile and joining in shared memory at every item's end
+// the loads paused there: 141 us instead of 128 for 64 rows of up to 8192 tokens, 8 heads.  Asking L2 for codes two to eight slabs
+// ahead made it 1 to 35% slower, slabs of 16 keys with four CTAs an SM 5%, two CTAs without
+// spills 10%.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -37,8 +41,11 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 128, kWarps = 4;
-constexpr int kTile = 128, kSlab = 32;  // keys of a tile, and of a warp in it
+constexpr int kMaxListed = 1024;  // rows whose prefix fits in shared memory
 constexpr float kNegInf = -INFINITY;
+
+// Keys of a slab for items of `cols` query rows.
+__host__ __device__ constexpr int slab_keys(int cols) { return cols >= 32 ? 16 : 32; }
 
 __device__ __forceinline__ uint32_t widen2(uint32_t codes) {  // two e4m3 codes (low 16 bits)
     uint32_t h;
@@ -66,13 +73,16 @@ template <> struct Act<__nv_bfloat16> {
     static __device__ __forceinline__ float2 two(uint32_t w) {
         return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
     }
-    static __device__ __forceinline__ __nv_bfloat16 from(float x) { return __float2bfloat16_rn(x); }
+    static __device__ __forceinline__ uint32_t pack(float a, float b) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
 };
 template <> struct Act<__half> {
     static __device__ __forceinline__ float2 two(uint32_t w) {
         return __half22float2(*reinterpret_cast<const __half2*>(&w));
     }
-    static __device__ __forceinline__ __half from(float x) { return __float2half_rn(x); }
+    static __device__ __forceinline__ uint32_t pack(float a, float b) { return pack_half2(a, b); }
 };
 
 // New tokens of row r: [begin, begin + n); n = 0 for malformed offsets.
@@ -97,10 +107,10 @@ __device__ __forceinline__ int row_length(const CacheParams& c, int r) {
     if (len < 0 || len > room) report(c.status, kStatusBadIndex);
     return len < 0 ? 0 : len > room ? (int)room : len;
 }
-__device__ __forceinline__ int row_tiles(int len) { return len > kTile ? (len + kTile - 1) / kTile : 1; }
+__device__ __forceinline__ int row_slabs(int len, int keys) { return len > keys ? (len + keys - 1) / keys : 1; }
 
-// first[r] = tiles of all items of the rows before r; first[rows] = all.  Items of a row: column
-// blocks (kCols query rows each) by key/value heads.  The whole block calls it; s: 5 values.
+// first[r] = slabs of all items of the rows before r; first[rows] = all.  Items of a row: column
+// blocks (cols query rows each) by key/value heads.  The whole block calls it; s: one value a warp.
 __device__ void scan_rows(const AttentionParams& p, int cols, int64_t* first, int64_t* s) {
     const CacheParams& c = p.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -112,7 +122,7 @@ __device__ void scan_rows(const AttentionParams& p, int cols, int64_t* first, in
         if (r < c.rows) {
             int64_t begin;
             const int n = row_tokens(c, r, begin);
-            w = ((int64_t)n * group + cols - 1) / cols * c.heads * row_tiles(row_length(c, r));
+            w = ((int64_t)n * group + cols - 1) / cols * c.heads * row_slabs(row_length(c, r), slab_keys(cols));
         }
         int64_t x = w;
 #pragma unroll
@@ -143,78 +153,97 @@ __device__ __forceinline__ int row_of(const int64_t* first, int rows, int64_t w)
     return lo;
 }
 
-struct Item {
-    int row, head, block;  // cache row, key/value head, column block
-    int n, len, tiles;     // new tokens, cached tokens and tiles of the row
-    int64_t begin;         // first new token
-    int64_t first;         // first work number
-};
-__device__ __forceinline__ Item item_of(const AttentionParams& p, const int64_t* first, int64_t w) {
-    Item it;
-    it.row = row_of(first, p.c.rows, w);
-    it.n = row_tokens(p.c, it.row, it.begin);
-    it.len = row_length(p.c, it.row);
-    it.tiles = row_tiles(it.len);
-    const int64_t i = (w - first[it.row]) / it.tiles;
-    it.head = (int)(i % p.c.heads);
-    it.block = (int)(i / p.c.heads);
-    it.first = first[it.row] + i * it.tiles;
-    return it;
+// Slabs of one warp's share.
+__device__ __forceinline__ int64_t share_of(int64_t all, int warps) { return (all + warps - 1) / warps; }
+
+// Codes of 16 keys, widened, against the query rows: acc += K Q^T.  q(step, nt) gives the two
+// registers of a reduction step.
+template <int kHalves, int kNT, typename Q>
+__device__ __forceinline__ void product_k(float (&acc)[kNT][4], const uint4 (&k)[2][kHalves], Q q) {
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h) {
+        const uint32_t a[4] = {k[0][h].x, k[0][h].y, k[0][h].z, k[0][h].w};
+        const uint32_t b[4] = {k[1][h].x, k[1][h].y, k[1][h].z, k[1][h].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t a0 = widen2(a[j]), a2 = widen2(a[j] >> 16), a1 = widen2(b[j]), a3 = widen2(b[j] >> 16);
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt) {
+                const uint2 y = q(4 * h + j, nt);
+                mma16816(acc[nt], a0, a1, a2, a3, y.x, y.y);
+            }
+        }
+    }
 }
 
-// Largest share of one CTA, and the CTA that work number w falls to.
-__device__ __forceinline__ int64_t share_of(int64_t all, int ctas) { return (all + ctas - 1) / ctas; }
-
 template <typename T, int kDim, int kNT>
-__global__ void __launch_bounds__(kThreads) attention_kernel(const AttentionParams p) {
+__global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(const __grid_constant__ AttentionParams p) {
     constexpr int kCols = 8 * kNT;
+    constexpr int kKeys = slab_keys(kCols), kBlk = kKeys / 16;
     constexpr int kHalves = kDim / 64;   // 16-byte loads of a key by a thread
     constexpr int kSteps = kDim / 16;    // reduction steps of S^T
     constexpr int kMT = kDim / 16;       // 16-channel tiles of O^T
     constexpr int kVWords = kDim / 32;   // 4-byte words of a V load
-    constexpr int kPad = kDim + 4;
-    extern __shared__ __align__(16) unsigned char smem_raw[];
-    float* s_o = reinterpret_cast<float*>(smem_raw);                 // [warps][kCols][kPad]
-    float* s_ml = s_o + kWarps * kCols * kPad;                       // [warps][kCols][2]
-    __shared__ int64_t s_scan[kWarps];
+    constexpr bool kQShared = kNT > 2;   // q does not fit in registers beside the sums
+    __shared__ int64_t s_first[kMaxListed + 1], s_scan[kWarps];
+    __shared__ uint2 s_q[kQShared ? kWarps : 1][kQShared ? kSteps * kNT : 1][32];
 
     const CacheParams& c = p.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int group = p.q_heads / c.heads;
     const int page_shift = __ffs(c.page_tokens) - 1;
+    const int64_t block_bytes = (int64_t)c.page_tokens * kDim;
 
-    // Every CTA needs the rows' prefix; each one writes the same values.
-    scan_rows(p, kCols, p.first_work, s_scan);
+    // Every CTA needs the rows' prefix; past kMaxListed rows all write the same values to the
+    // scratch.
+    int64_t* first = c.rows <= kMaxListed ? s_first : p.first_work;
+    scan_rows(p, kCols, first, s_scan);
     __syncthreads();
-    const int64_t all = p.first_work[c.rows];
-    const int64_t per = share_of(all, p.ctas);
-    int64_t w = per * blockIdx.x;
-    const int64_t w_end = min(all, w + per);
-    const int64_t w_begin = w;
+    if (blockIdx.x == 0 && c.rows <= kMaxListed)
+        for (int r = tid; r <= c.rows; r += kThreads) p.first_work[r] = s_first[r];
+    cudaTriggerProgrammaticLaunchCompletion();
+    const int64_t all = first[c.rows];
+    const int64_t per = share_of(all, p.ctas * kWarps);
+    const int64_t unit = (int64_t)blockIdx.x * kWarps + warp;
+    const int64_t w_begin = per * unit, w_end = min(all, w_begin + per);
 
-    while (w < w_end) {
-        const Item it = item_of(p, p.first_work, w);
-        const int64_t item_end = it.first + it.tiles;
-        const int tile0 = (int)(w - it.first);
-        int tile1 = (int)(min(item_end, w_end) - it.first);
+    for (int64_t w = w_begin; w < w_end;) {
+        const int row = row_of(first, c.rows, w);
+        int64_t begin;
+        const int n = row_tokens(c, row, begin), len = row_length(c, row), slabs = row_slabs(len, kKeys);
+        const int64_t i_row = (w - first[row]) / slabs, item = first[row] + i_row * slabs, item_end = item + slabs;
+        const int head = (int)(i_row % c.heads), block = (int)(i_row / c.heads);
+        const int slab0 = (int)(w - item);
 
-        // Columns of this thread: kNT pairs (8 nt + 2 t, + 1) for S^T and O^T, rows g for q.
-        const int rows_all = it.n * group, row0 = it.block * kCols;
-        // Last key any column of this block sees, plus one.
-        const int last_token = (min(rows_all, row0 + kCols) - 1) / group;
-        const int seen_max = min(it.len, max(0, it.len - it.n + last_token + 1));
-        tile1 = min(tile1, (seen_max + kTile - 1) / kTile);
-        const int first_token = row0 / group;
-        const int seen_min = max(0, min(it.len, it.len - it.n + first_token + 1));
+        const int rows_all = n * group, row0 = block * kCols;
+        // Keys that any, and that every, column of this block sees.
+        const int seen_max = min(len, max(0, len - n + (min(rows_all, row0 + kCols) - 1) / group + 1));
+        const int seen_min = max(0, min(len, len - n + row0 / group + 1));
+        const int slab1 = min((int)(min(item_end, w_end) - item), (seen_max + kKeys - 1) / kKeys);
 
-        uint32_t q[kNT][kSteps][2];
+        // Page and scales of the 16 keys of block number b; lane l holds block b0 + l.
+        const int32_t* table = c.tables + (int64_t)row * c.width;
+        auto page_at = [&](int b) {
+            const int key = b * 16;
+            if (key >= seen_max) return -1;
+            const int32_t x = table[key >> page_shift];
+            if (x < 0 || x >= c.pages) {
+                report(c.status, kStatusBadIndex);
+                return -1;
+            }
+            return x;
+        };
+        constexpr int kBatch = 32 / kBlk;  // slabs whose pages a warp holds
+        int32_t pages = page_at(slab0 * kBlk + lane), pages_next = -1;
+
+        uint32_t q[kQShared ? 1 : kNT][kQShared ? 1 : kSteps][2];
         float q_scale[kNT];  // of column 8 nt + g
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
             const int f = row0 + nt * 8 + g;
             const bool there = f < rows_all;
-            const T* src = static_cast<const T*>(p.q) + (it.begin + (there ? f / group : 0)) * p.q_stride +
-                           (int64_t)(it.head * group + (there ? f % group : 0)) * kDim;
+            const T* src = static_cast<const T*>(p.q) + (begin + (there ? f / group : 0)) * p.q_stride +
+                           (int64_t)(head * group + (there ? f % group : 0)) * kDim;
             float x[kHalves][16];
             float a = 0.f;
 #pragma unroll
@@ -242,10 +271,20 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttentionPara
             for (int h = 0; h < kHalves; ++h)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    q[nt][4 * h + j][0] = pack_half2(x[h][4 * j] * up, x[h][4 * j + 1] * up);
-                    q[nt][4 * h + j][1] = pack_half2(x[h][4 * j + 2] * up, x[h][4 * j + 3] * up);
+                    const uint32_t y0 = pack_half2(x[h][4 * j] * up, x[h][4 * j + 1] * up);
+                    const uint32_t y1 = pack_half2(x[h][4 * j + 2] * up, x[h][4 * j + 3] * up);
+                    if constexpr (kQShared) {
+                        s_q[warp][(4 * h + j) * kNT + nt][lane] = make_uint2(y0, y1);
+                    } else {
+                        q[nt][4 * h + j][0] = y0;
+                        q[nt][4 * h + j][1] = y1;
+                    }
                 }
         }
+        auto q_at = [&](int step, int nt) {
+            if constexpr (kQShared) return s_q[warp][step * kNT + nt][lane];  // this lane's own
+            else return make_uint2(q[nt][step][0], q[nt][step][1]);
+        };
         // What each column sees and its factor, for this thread's column pairs.
         int seen[kNT][2];
         float factor[kNT][2];
@@ -254,7 +293,7 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttentionPara
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int f = row0 + nt * 8 + 2 * t + i;
-                seen[nt][i] = f < rows_all ? max(0, min(it.len, it.len - it.n + f / group + 1)) : 0;
+                seen[nt][i] = f < rows_all ? max(0, min(len, len - n + f / group + 1)) : 0;
                 factor[nt][i] = __shfl_sync(0xffffffffu, q_scale[nt], (2 * t + i) * 4);
             }
 
@@ -267,105 +306,116 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttentionPara
             for (int j = 0; j < kMT; ++j) o[nt][j][0] = o[nt][j][1] = o[nt][j][2] = o[nt][j][3] = 0.f;
         }
 
-        const int32_t* table = c.tables + (int64_t)it.row * c.width;
-        // Page of the 16 keys from `key` on; -1 past what any column sees.
-        auto page_at = [&](int key) {
-            if (key >= seen_max) return -1;
-            const int32_t x = table[key >> page_shift];
-            if (x < 0 || x >= c.pages) {
-                if (lane == 0) report(c.status, kStatusBadIndex);
-                return -1;
-            }
-            return x;
-        };
-        auto block_of = [&](int32_t page, int key) {  // element offset of `key`'s codes
-            return (((int64_t)page * c.heads + it.head) * c.page_tokens + (key & (c.page_tokens - 1))) * kDim;
-        };
-        int32_t pg[2];
-        uint4 kr[2][2][kHalves];  // [16-key tile][key g, g + 8][channel half]
-        auto load_k = [&](int key0) {
+        auto scale_of = [&](const float* scales, int32_t page) { return page < 0 ? 0.f : scales[(int64_t)page * c.heads + head]; };
+        float k_scales = scale_of(c.k_scale, pages), v_scales = scale_of(c.v_scale, pages);
+        int b0 = slab0 * kBlk;  // block of lane 0
+
+        uint4 kr[kBlk][2][kHalves];  // [16 keys][key g, g + 8][channel half]
+        uint32_t vr[kBlk][4][kVWords];  // keys 2t, 2t + 1, 2t + 8, 2t + 9 of each 16
+        auto load_k = [&](int slab) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                pg[i] = page_at(key0 + 16 * i);
+            for (int i = 0; i < kBlk; ++i) {
+                const int b = slab * kBlk + i;
+                const int32_t page = __shfl_sync(0xffffffffu, pages, b - b0);
+                if (page >= 0) {
+                    const uint8_t* src = c.k_codes + ((int64_t)page * c.heads + head) * block_bytes +
+                                         ((b * 16 & (c.page_tokens - 1)) + g) * kDim + 16 * t;
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const uint8_t* src = pg[i] < 0 ? nullptr : c.k_codes + block_of(pg[i], key0 + 16 * i + 8 * r + g) + 16 * t;
+                    for (int r = 0; r < 2; ++r)
 #pragma unroll
-                    for (int h = 0; h < kHalves; ++h)
-                        kr[i][r][h] = src ? __ldg(reinterpret_cast<const uint4*>(src + 64 * h)) : make_uint4(0u, 0u, 0u, 0u);
+                        for (int h = 0; h < kHalves; ++h) kr[i][r][h] = __ldg(reinterpret_cast<const uint4*>(src + 8 * r * kDim + 64 * h));
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+#pragma unroll
+                        for (int h = 0; h < kHalves; ++h) kr[i][r][h] = make_uint4(0u, 0u, 0u, 0u);
                 }
             }
         };
-        int key0 = tile0 * kTile + warp * kSlab;
-        if (tile0 < tile1) load_k(key0);
-        for (int tile = tile0; tile < tile1; ++tile, key0 += kTile) {
-            const int32_t cur[2] = {pg[0], pg[1]};
-            // V of this slab: keys 2t, 2t + 1, 2t + 8, 2t + 9 of each 16, zero where unseen.
-            uint32_t vr[2][4][kVWords];
-            float ks[2], vs[2];
+        auto load_v = [&](int slab) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int64_t s_at = cur[i] < 0 ? 0 : (int64_t)cur[i] * c.heads + it.head;
-                ks[i] = cur[i] < 0 ? 0.f : c.k_scale[s_at];
-                vs[i] = cur[i] < 0 ? 0.f : c.v_scale[s_at];
+            for (int i = 0; i < kBlk; ++i) {
+                const int b = slab * kBlk + i, key0 = b * 16;
+                const int32_t page = __shfl_sync(0xffffffffu, pages, b - b0);
+                const uint8_t* src = c.v_codes + ((int64_t)max(page, 0) * c.heads + head) * block_bytes +
+                                     ((key0 & (c.page_tokens - 1)) + 2 * t) * kDim + kVWords * 4 * g;
+                const bool whole = page >= 0 && key0 + 16 <= seen_max;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const int key = key0 + 16 * i + 2 * t + (r & 1) + 8 * (r >> 1);
+                    const int key = 2 * t + (r & 1) + 8 * (r >> 1), off = ((r & 1) + 8 * (r >> 1)) * kDim;
 #pragma unroll
-                    for (int x = 0; x < kVWords; ++x) vr[i][r][x] = 0u;
-                    if (cur[i] >= 0 && key < seen_max) {
-                        const uint8_t* src = c.v_codes + block_of(cur[i], key) + kVWords * 4 * g;
+                    for (int x = 0; x < kVWords; ++x) vr[i][r][x] = 0u;  // what no column sees stays out
+                    if (whole || (page >= 0 && key0 + key < seen_max)) {
                         if constexpr (kVWords == 4) {
-                            const uint4 v = __ldg(reinterpret_cast<const uint4*>(src));
+                            const uint4 v = __ldg(reinterpret_cast<const uint4*>(src + off));
                             vr[i][r][0] = v.x; vr[i][r][1] = v.y; vr[i][r][2] = v.z; vr[i][r][3] = v.w;
                         } else {
-                            const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
+                            const uint2 v = __ldg(reinterpret_cast<const uint2*>(src + off));
                             vr[i][r][0] = v.x; vr[i][r][1] = v.y;
                         }
                     }
                 }
             }
-            float sc[kNT][2][4];
+        };
+        if (slab0 < slab1) {
+            load_k(slab0);
+            load_v(slab0);
+        }
+        if (slab1 - slab0 > kBatch) pages_next = page_at(b0 + 32 + lane);
+        for (int slab = slab0; slab < slab1; ++slab) {
+            float ks[kBlk], vs[kBlk];
+            bool missing = false;
 #pragma unroll
-            for (int nt = 0; nt < kNT; ++nt)
+            for (int i = 0; i < kBlk; ++i) {
+                const int from = slab * kBlk + i - b0;
+                ks[i] = __shfl_sync(0xffffffffu, k_scales, from);
+                vs[i] = __shfl_sync(0xffffffffu, v_scales, from);
+                missing |= __shfl_sync(0xffffffffu, pages, from) < 0;
+            }
+            const int32_t pages_now = pages;
+            const int b_now = b0;
+            float sc[kBlk][kNT][4];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) sc[nt][i][0] = sc[nt][i][1] = sc[nt][i][2] = sc[nt][i][3] = 0.f;
+            for (int i = 0; i < kBlk; ++i) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int h = 0; h < kHalves; ++h) {
-                    const uint32_t a[4] = {kr[i][0][h].x, kr[i][0][h].y, kr[i][0][h].z, kr[i][0][h].w};
-                    const uint32_t b[4] = {kr[i][1][h].x, kr[i][1][h].y, kr[i][1][h].z, kr[i][1][h].w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t a0 = widen2(a[j]), a2 = widen2(a[j] >> 16), a1 = widen2(b[j]), a3 = widen2(b[j] >> 16);
-#pragma unroll
-                        for (int nt = 0; nt < kNT; ++nt)
-                            mma16816(sc[nt][i], a0, a1, a2, a3, q[nt][4 * h + j][0], q[nt][4 * h + j][1]);
-                    }
+                for (int nt = 0; nt < kNT; ++nt) sc[i][nt][0] = sc[i][nt][1] = sc[i][nt][2] = sc[i][nt][3] = 0.f;
+                product_k<kHalves, kNT>(sc[i], kr[i], q_at);
+            }
+            // The next slab's pages, then its K while this one's weights are worked out.
+            if (slab + 1 < slab1) {
+                if ((slab + 1) * kBlk - b0 == 32) {
+                    pages = pages_next;
+                    k_scales = scale_of(c.k_scale, pages);
+                    v_scales = scale_of(c.v_scale, pages);
+                    b0 += 32;
+                    if ((b0 + 32) / kBlk < slab1) pages_next = page_at(b0 + 32 + lane);
                 }
-            if (tile + 1 < tile1) load_k(key0 + kTile);
+                load_k(slab + 1);
+            }
 
-            // Running maximum of each column over this slab's 32 keys.
-            const bool edge = key0 + kSlab > seen_min || cur[0] < 0 || cur[1] < 0;
-            const float ref_new = fmaxf(ref, fmaxf(vs[0], vs[1]));
-            const float ref_inv = ref_new > 0.f ? 1.f / ref_new : 0.f;
-            const float wv[2] = {vs[0] * ref_inv, vs[1] * ref_inv}, shrink = ref * ref_inv;
+            const int key0 = slab * kKeys;
+            const bool edge = key0 + kKeys > seen_min || missing;
+            float ref_new = ref;
+#pragma unroll
+            for (int i = 0; i < kBlk; ++i) ref_new = fmaxf(ref_new, vs[i]);
+            const float ref_inv = ref_new > 0.f ? 1.f / ref_new : 0.f, shrink = ref * ref_inv;
             ref = ref_new;
-            uint32_t pf[kNT][2][2];
+            uint32_t pf[kBlk][kNT][2];
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt) {
                 float top[2] = {kNegInf, kNegInf};
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < kBlk; ++i) {
+                    const float fk[2] = {factor[nt][0] * ks[i], factor[nt][1] * ks[i]};
+                    const bool gone = edge && __shfl_sync(0xffffffffu, pages_now, slab * kBlk + i - b_now) < 0;
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        const int col = x & 1, key = key0 + 16 * i + g + 8 * (x >> 1);
-                        float y = sc[nt][i][x] * (factor[nt][col] * ks[i]);
-                        if (edge && (cur[i] < 0 || key >= seen[nt][col])) y = kNegInf;
-                        sc[nt][i][x] = y;
-                        top[col] = fmaxf(top[col], y);
+                        float y = sc[i][nt][x] * fk[x & 1];
+                        if (edge && (gone || key0 + 16 * i + g + 8 * (x >> 1) >= seen[nt][x & 1])) y = kNegInf;
+                        sc[i][nt][x] = y;
+                        top[x & 1] = fmaxf(top[x & 1], y);
                     }
+                }
                 float fix[2];
 #pragma unroll
                 for (int col = 0; col < 2; ++col) {
@@ -379,16 +429,17 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttentionPara
                     top[col] = m_use;
                 }
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
+                for (int i = 0; i < kBlk; ++i) {
+                    const float wv = vs[i] * ref_inv;
                     float e[4];
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        e[x] = exp2f(sc[nt][i][x] - top[x & 1]);
+                        e[x] = exp2f(sc[i][nt][x] - top[x & 1]);
                         l[nt][x & 1] += e[x];
-                        e[x] *= wv[i];
+                        e[x] *= wv;
                     }
-                    pf[nt][i][0] = transpose8x8(pack_half2(e[0], e[1]));
-                    pf[nt][i][1] = transpose8x8(pack_half2(e[2], e[3]));
+                    pf[i][nt][0] = transpose8x8(pack_half2(e[0], e[1]));
+                    pf[i][nt][1] = transpose8x8(pack_half2(e[2], e[3]));
                 }
                 const float f0 = fix[0] * shrink, f1 = fix[1] * shrink;
                 if (__any_sync(0xffffffffu, f0 != 1.f || f1 != 1.f)) {
@@ -402,7 +453,7 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttentionPara
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < kBlk; ++i)
 #pragma unroll
                 for (int x = 0; x < kVWords; ++x) {
                     // Codes of channels d, d + 1 (then d + 2, d + 3) of two neighbouring keys.
@@ -413,72 +464,58 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const AttentionPara
                         const uint32_t lo = y ? lo1 : lo0, hi = y ? hi1 : hi0;
                         const uint32_t a0 = widen2(lo), a1 = widen2(lo >> 16), a2 = widen2(hi), a3 = widen2(hi >> 16);
 #pragma unroll
-                        for (int nt = 0; nt < kNT; ++nt) mma16816(o[nt][2 * x + y], a0, a1, a2, a3, pf[nt][i][0], pf[nt][i][1]);
+                        for (int nt = 0; nt < kNT; ++nt) mma16816(o[nt][2 * x + y], a0, a1, a2, a3, pf[i][nt][0], pf[i][nt][1]);
                     }
                 }
+            if (slab + 1 < slab1) load_v(slab + 1);
         }
 
-        // The four warps' parts into shared memory, then joined by columns.
         // o[nt][j][x] is channel 4 kVWords g + 2 j + x / 2 of column 8 nt + 2 t + x % 2.
+        const bool whole = w == item && item_end <= w_end;
+        const int64_t slot = 2 * unit + (w == w_begin ? 0 : 1);
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
 #pragma unroll
-            for (int col = 0; col < 2; ++col) {
+            for (int col = 0; col < 2; ++col)
 #pragma unroll
                 for (int s = 4; s <= 16; s <<= 1) l[nt][col] += __shfl_xor_sync(0xffffffffu, l[nt][col], s);
-                float* ml = s_ml + (warp * kCols + nt * 8 + 2 * t + col) * 2;
-                if (g == 0) {
-                    ml[0] = m[nt][col];
-                    ml[1] = l[nt][col];
+            if (whole) {
+#pragma unroll
+                for (int col = 0; col < 2; ++col) {
+                    const int f = row0 + nt * 8 + 2 * t + col;
+                    if (f >= rows_all) continue;
+                    const float by = l[nt][col] > 0.f ? ref / l[nt][col] : 0.f;
+                    T* out = static_cast<T*>(p.out) + (begin + f / group) * p.out_stride + (int64_t)(head * group + f % group) * kDim + kVWords * 4 * g;
+#pragma unroll
+                    for (int j = 0; j < kMT; ++j)
+                        *reinterpret_cast<uint32_t*>(out + 2 * j) = Act<T>::pack(o[nt][j][col] * by, o[nt][j][2 + col] * by);
                 }
-                float* dst = s_o + (warp * kCols + nt * 8 + 2 * t + col) * kPad + kVWords * 4 * g;
+            } else {
+                float4* part = reinterpret_cast<float4*>(p.part_o) + (slot * kNT + nt) * kMT * 32 + lane;
 #pragma unroll
                 for (int j = 0; j < kMT; ++j)
-                    *reinterpret_cast<float2*>(dst + 2 * j) = make_float2(o[nt][j][col] * ref, o[nt][j][2 + col] * ref);
+                    part[32 * j] = make_float4(o[nt][j][0] * ref, o[nt][j][1] * ref, o[nt][j][2] * ref, o[nt][j][3] * ref);
+                if (g == 0)
+                    reinterpret_cast<float4*>(p.part_ml)[(slot * kNT + nt) * 4 + t] = make_float4(m[nt][0], l[nt][0], m[nt][1], l[nt][1]);
             }
         }
-        __syncthreads();
-        const bool whole = w == it.first && item_end <= w_end;
-        const int64_t slot = 2 * (int64_t)blockIdx.x + (w == w_begin ? 0 : 1);
-        for (int x = tid; x < kCols * kDim; x += kThreads) {
-            const int col = x / kDim, d = x % kDim, f = row0 + col;
-            if (f >= rows_all) break;
-            float top = kNegInf, sum = 0.f, acc = 0.f;
-#pragma unroll
-            for (int k = 0; k < kWarps; ++k) top = fmaxf(top, s_ml[(k * kCols + col) * 2]);
-#pragma unroll
-            for (int k = 0; k < kWarps; ++k) {
-                const float mk = s_ml[(k * kCols + col) * 2];
-                const float e = mk == kNegInf ? 0.f : exp2f(mk - top);
-                sum += e * s_ml[(k * kCols + col) * 2 + 1];
-                if (e > 0.f) acc += e * s_o[(k * kCols + col) * kPad + d];
-            }
-            if (whole) {
-                T* out = static_cast<T*>(p.out) + (it.begin + f / group) * p.out_stride + (int64_t)(it.head * group + f % group) * kDim;
-                out[d] = Act<T>::from(sum > 0.f ? acc / sum : 0.f);
-            } else {
-                p.part_o[(slot * kCols + col) * kDim + d] = acc;
-                if (d == 0) {
-                    p.part_ml[(slot * kCols + col) * 2] = top;
-                    p.part_ml[(slot * kCols + col) * 2 + 1] = sum;
-                }
-            }
-        }
-        __syncthreads();  // shared memory is written again for the next item
         w = item_end;
     }
 }
 
-// Joins the parts of the items that lie in several CTAs' shares: blockIdx.x counts items,
-// blockIdx.y columns.
-template <typename T, int kDim, int kCols>
-__global__ void __launch_bounds__(kDim) attention_join_kernel(const AttentionParams p) {
-    cudaGridDependencySynchronize();
+// Joins the parts of the items that lie in several warps' shares.  blockIdx.x counts items,
+// blockIdx.y column tiles; a warp has 16 channels of 8 columns, in the fragments' layout.
+// kSplit (items of many parts): blockIdx.z is the channel tile, and the warps share the parts.
+constexpr int kJoinSplit = 8;  // warps that share the parts
+
+template <typename T, int kDim, int kNT, bool kSplit>
+__global__ void __launch_bounds__(kSplit ? kJoinSplit * 32 : kDim * 2) attention_join_kernel(const __grid_constant__ AttentionParams p) {
+    constexpr int kCols = 8 * kNT, kMT = kDim / 16, kVWords = kDim / 32;
+    __shared__ float4 s_o[kSplit ? kJoinSplit : 1][32], s_ml[kSplit ? kJoinSplit : 1][32];
     const CacheParams& c = p.c;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int nt = blockIdx.y, j = kSplit ? blockIdx.z : warp;
     const int group = p.q_heads / c.heads;
-    const int64_t all = p.first_work[c.rows], per = share_of(all, p.ctas);
-    // Items are counted as rows * heads * blocks when every row has the same number of column
-    // blocks (one token a row), else by walking the rows.
     int64_t i = blockIdx.x;
     int row = 0;
     if (!c.cu) {
@@ -500,64 +537,91 @@ __global__ void __launch_bounds__(kDim) attention_join_kernel(const AttentionPar
     if (row >= c.rows || i < 0) return;
     int64_t begin;
     const int n = row_tokens(c, row, begin);
-    const int tiles = row_tiles(row_length(c, row));
-    const int64_t w0 = p.first_work[row] + i * tiles, w1 = w0 + tiles;
-    if (w1 > p.first_work[row + 1]) return;
-    const int64_t c0 = w0 / per, c1 = (w1 - 1) / per;
-    if (c0 == c1) return;
+    const int slabs = row_slabs(row_length(c, row), slab_keys(kCols));
+    cudaGridDependencySynchronize();
+    const int64_t all = p.first_work[c.rows], w_row = p.first_work[row], w_next = p.first_work[row + 1];
+    const int64_t per = share_of(all, p.ctas * kWarps);
+    const int64_t w0 = w_row + i * slabs, w1 = w0 + slabs;
+    if (w1 > w_next) return;
+    const int64_t u0 = w0 / per, u1 = (w1 - 1) / per;
+    if (u0 == u1) return;
     const int head = (int)(i % c.heads), block = (int)(i / c.heads);
-    const int col = blockIdx.y, f = block * kCols + col, d = threadIdx.x;
-    if (f >= n * group) return;
-    float top = kNegInf, sum = 0.f, acc = 0.f;
-    for (int64_t k = c0; k <= c1; ++k) {
-        const int64_t slot = 2 * k + (k * per >= w0 ? 0 : 1);
-        const float mk = p.part_ml[(slot * kCols + col) * 2], lk = p.part_ml[(slot * kCols + col) * 2 + 1];
-        const float ok = p.part_o[(slot * kCols + col) * kDim + d];
-        if (mk == kNegInf) continue;
-        const float m = fmaxf(top, mk), a = exp2f(top - m), b = exp2f(mk - m);
-        top = m;
-        sum = sum * a + lk * b;
-        acc = acc * a + ok * b;
-    }
-    T* out = static_cast<T*>(p.out) + (begin + f / group) * p.out_stride + (int64_t)(head * group + f % group) * kDim;
-    out[d] = Act<T>::from(sum > 0.f ? acc / sum : 0.f);
-}
 
-template <int kDim, int kNT>
-constexpr size_t smem_bytes() {
-    return (size_t)kWarps * 8 * kNT * (kDim + 4 + 2) * sizeof(float);
+    float top[2] = {kNegInf, kNegInf}, sum[2] = {0.f, 0.f}, acc[4] = {0.f, 0.f, 0.f, 0.f};
+    auto add = [&](const float4& ml, const float4& o) {
+        const float mk[2] = {ml.x, ml.z}, lk[2] = {ml.y, ml.w}, ok[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+        for (int col = 0; col < 2; ++col) {
+            const float m = fmaxf(top[col], mk[col]), use = m == kNegInf ? 0.f : m;
+            const float a = exp2f(top[col] - use), b = exp2f(mk[col] - use);
+            top[col] = m;
+            sum[col] = sum[col] * a + lk[col] * b;
+            acc[col] = acc[col] * a + ok[col] * b;
+            acc[2 + col] = acc[2 + col] * a + ok[2 + col] * b;
+        }
+    };
+    constexpr int kAhead = 8;
+    const int64_t step = kSplit ? kJoinSplit : 1;
+    for (int64_t k = u0 + (kSplit ? warp : 0); k <= u1; k += kAhead * step) {
+        float4 ml[kAhead], o[kAhead];
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) {
+            const int64_t u = k + x * step;
+            if (u > u1) continue;
+            const int64_t slot = 2 * u + (u * per >= w0 ? 0 : 1);
+            ml[x] = reinterpret_cast<const float4*>(p.part_ml)[(slot * kNT + nt) * 4 + t];
+            o[x] = reinterpret_cast<const float4*>(p.part_o)[((slot * kNT + nt) * kMT + j) * 32 + lane];
+        }
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x)
+            if (k + x * step <= u1) add(ml[x], o[x]);
+    }
+    if (kSplit) {
+        s_o[warp][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        s_ml[warp][lane] = make_float4(top[0], sum[0], top[1], sum[1]);
+        __syncthreads();
+        if (warp) return;
+        for (int x = 1; x < kJoinSplit; ++x) add(s_ml[x][lane], s_o[x][lane]);
+    }
+#pragma unroll
+    for (int col = 0; col < 2; ++col) {
+        const int f = block * kCols + nt * 8 + 2 * t + col;
+        if (f >= n * group) continue;
+        const float by = sum[col] > 0.f ? 1.f / sum[col] : 0.f;
+        T* out = static_cast<T*>(p.out) + (begin + f / group) * p.out_stride + (int64_t)(head * group + f % group) * kDim + kVWords * 4 * g + 2 * j;
+        *reinterpret_cast<uint32_t*>(out) = Act<T>::pack(acc[col] * by, acc[2 + col] * by);
+    }
 }
 
 template <typename T, int kDim, int kNT>
 cudaError_t launch_one(const AttentionParams& p, cudaStream_t stream) {
     const CacheParams& c = p.c;
     constexpr int kCols = 8 * kNT;
-    attention_kernel<T, kDim, kNT><<<p.ctas, kThreads, smem_bytes<kDim, kNT>(), stream>>>(p);
+    attention_kernel<T, kDim, kNT><<<p.ctas, kThreads, 0, stream>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int64_t group = p.q_heads / c.heads;
     const int64_t items = c.cu ? (c.tokens * group / kCols + c.rows) * c.heads
                                : (int64_t)c.rows * c.heads * ((group + kCols - 1) / kCols);
+    // Fewer items than SMs leave SMs idle and have many parts each.
+    const bool split = items * kNT < p.sm_count;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)items, kCols);
-    cfg.blockDim = dim3(kDim);
+    cfg.gridDim = dim3((unsigned)items, kNT, split ? kDim / 16 : 1);
+    cfg.blockDim = dim3(split ? kJoinSplit * 32 : kDim * 2);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attention_join_kernel<T, kDim, kCols>, p);
+    if (split) return cudaLaunchKernelEx(&cfg, attention_join_kernel<T, kDim, kNT, true>, p);
+    return cudaLaunchKernelEx(&cfg, attention_join_kernel<T, kDim, kNT, false>, p);
 }
 
 template <typename T, int kDim, int kNT>
 int resident() {
     int n = 0;
-    if (cudaFuncSetAttribute(attention_kernel<T, kDim, kNT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)smem_bytes<kDim, kNT>()) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attention_kernel<T, kDim, kNT>, kThreads,
-                                                      smem_bytes<kDim, kNT>()) != cudaSuccess ||
-        n < 1) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attention_kernel<T, kDim, kNT>, kThreads, 0) != cudaSuccess || n < 1) {
         cudaGetLastError();
         n = 1;
     }
@@ -586,8 +650,10 @@ int attention_cols(int64_t tokens, int32_t rows, int32_t group) {
 }
 
 size_t attention_scratch(int32_t rows, int32_t dim, int cols, int ctas) {
-    return ((size_t)rows + 1) * 8 + 16 + (size_t)2 * ctas * cols * (dim + 2) * 4;
+    return ((size_t)rows + 1) * 8 + 16 + (size_t)2 * ctas * kWarps * cols * (dim + 2) * 4;
 }
+
+size_t attention_slots(int ctas) { return (size_t)2 * ctas * kWarps; }
 
 int attention_ctas(int32_t dim, int cols, bool f16, int sm_count) {
     int n;

@@ -93,11 +93,12 @@ struct AttentionParams {
     float scale;              // times log2(e)
     // scratch
     int64_t* first_work;      // [rows + 1]
-    float* part_o;            // [2 * ctas][kCols][dim]
-    float* part_ml;           // [2 * ctas][kCols][2]
-    int32_t ctas;
+    float* part_o;            // [slots][cols * dim], in the layout of the product's fragments
+    float* part_ml;           // [slots][cols][2]: maximum and sum
+    int32_t ctas, sm_count;
 };
 size_t attention_scratch(int32_t rows, int32_t dim, int cols, int ctas);
+size_t attention_slots(int ctas);
 int attention_cols(int64_t tokens, int32_t rows, int32_t group);
 int attention_ctas(int32_t dim, int cols, bool f16, int sm_count);
 cudaError_t launch_attention(const AttentionParams& p, int cols, bool f16, cudaStream_t stream);

@@ -409,12 +409,13 @@ kda_status kda_kvcache_attention(const kda_kvcache* cache, const void* q, int32_
         const int cols = kda::attention_cols(num_tokens, cache->rows, group);
         kda::AttentionParams p{};
         p.c = cache_params(cache, num_tokens, lens, cu_tokens, di->status);
+        p.sm_count = di->sm_count;
         p.ctas = kda::attention_ctas(cache->head_dim, cols, f16, di->sm_count);
         char* ws = nullptr;
         if ((st = scratch(dev, stream, kda::attention_scratch(cache->rows, cache->head_dim, cols, p.ctas), &ws)) != KDA_OK) return st;
         p.part_o = reinterpret_cast<float*>(ws);
-        p.part_ml = p.part_o + (size_t)2 * p.ctas * cols * cache->head_dim;
-        p.first_work = reinterpret_cast<int64_t*>(p.part_ml + (size_t)2 * p.ctas * cols * 2);
+        p.part_ml = p.part_o + kda::attention_slots(p.ctas) * cols * cache->head_dim;
+        p.first_work = reinterpret_cast<int64_t*>(p.part_ml + kda::attention_slots(p.ctas) * cols * 2);
         p.q = q;
         p.out = out;
         p.q_stride = q_stride;

@@ -227,6 +227,32 @@ def test_append_many_rows():
     check_append(rng, 1, 64, 16, rng.integers(0, 40, rows).tolist(), rng.integers(0, 40, rows).tolist(), "bf16")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_append_of_blocks_of_every_size(dtype):
+    # largest magnitudes from the type's least to its greatest values, quotients at and around
+    # the codes' rounding boundaries, divisors whose fraction is all ones
+    g = torch.Generator().manual_seed(1)
+    blocks, hkv, page, d = 400, 2, 16, 64
+    least, most = (-133, 127) if dtype == "bf16" else (-24, 15)
+    size = torch.exp2(torch.linspace(least, most, blocks, dtype=torch.float64)).repeat_interleave(page)[:, None, None]
+    x = torch.rand(blocks * page, hkv, d, generator=g, dtype=torch.float64) * 2 - 1
+    x[::3] = torch.round(x[::3] * 240) / 240  # multiples of the largest value's simple fractions
+    x[::page, :, 0] = 1
+    x = (x * size).to(DT[dtype])
+    tab = np.arange(blocks)[:, None]
+    kc = np.zeros((blocks, hkv, page, d), np.uint8)
+    ks = np.zeros((blocks, hkv), np.float32)
+    cache = gpu_cache(kc, kc.copy(), ks, ks.copy(), tab)
+    lens = torch.zeros(blocks, dtype=torch.int32, device="cuda")
+    K.kda_get_device_status()
+    K.kda_kvcache_append(x.cuda(), x.cuda(), *cache, lens, cu_tokens=cu_of([page] * blocks))
+    assert K.kda_get_device_status() == 0
+    ref.append(x.float().numpy(), kc, ks, tab, [0] * blocks, [page] * blocks, page)
+    assert np.array_equal(cache[2].cpu().numpy(), ks)
+    assert np.array_equal(cache[0].view(torch.uint8).cpu().numpy(), kc)
+    assert torch.equal(cache[0].view(torch.uint8), cache[1].view(torch.uint8))
+
+
 @pytest.mark.parametrize("cu", [False, True])
 def test_append_of_values_that_are_not_finite(cu):
     def spoil(xs):
