@@ -88,6 +88,8 @@ _lock = threading.Lock()
 def load_library(path: Optional[str] = None, build_if_missing: bool = False) -> ctypes.CDLL:
     """Load ``libkda.so`` (built by :mod:`chunked_kda_delta_gb300.build`)."""
     global _lib
+    if path is None and _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib

@@ -13,49 +13,80 @@ from typing import Optional, Sequence
 
 import torch
 
-from .kda import KdaKvCache, KdaPageShape, KdaPool, _check, _ptr, load_library
+from .kda import KdaKvCache, KdaPageShape, KdaPool, _check, load_library
 
 _ACT_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
 _LOGIT_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_I32, _F32 = torch.int32, torch.float32
+_BYTES = (torch.bool, torch.uint8)
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+
+# These calls are shorter on the GPU than on the host in a decoding step, so the marshalling is
+# kept lean: no context manager where the device is current already, the raw stream handle.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream, device):
     if stream is None:
-        stream = torch.cuda.current_stream(device).cuda_stream
-    elif isinstance(stream, torch.cuda.Stream):
-        stream = stream.cuda_stream
-    return ctypes.c_void_p(int(stream))
+        if _raw_stream is not None:
+            return _raw_stream(device.index)
+        return torch.cuda.current_stream(device).cuda_stream
+    if isinstance(stream, torch.cuda.Stream):
+        return stream.cuda_stream
+    return int(stream)
+
+
+def _run(function, device, *args):
+    """Calls `function` with `device` current."""
+    if torch.cuda.current_device() == device.index:
+        status = function(*args)
+    else:
+        with torch.cuda.device(device):
+            status = function(*args)
+    if status:
+        _check(load_library(), status)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _vector(name, t, dtypes, shape, device):
     """A contiguous tensor of one of these types and exactly this shape on `device`."""
-    if not isinstance(dtypes, tuple):
+    if (t.dtype in dtypes if type(dtypes) is tuple else t.dtype is dtypes) and t.shape == shape \
+            and t.device == device and t.is_contiguous():
+        return
+    if type(dtypes) is not tuple:
         dtypes = (dtypes,)
-    if t.dtype not in dtypes or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} must be a contiguous {dtypes[0]} tensor on {device}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t
+    raise ValueError(f"{name} must be a contiguous {dtypes[0]} tensor on {device}")
 
 
 def _pages(tables, refs):
-    if tables.device.type != "cuda":
+    shape, device = tables.shape, tables.device
+    if device.type != "cuda":
         raise ValueError("tables must be on cuda")
-    if tables.dim() != 2 or tables.shape[1] < 1:
+    if len(shape) != 2 or shape[1] < 1:
         raise ValueError("tables must be [rows, width]")
-    if refs.dim() != 1:
+    pages = refs.shape
+    if len(pages) != 1:
         raise ValueError("refs must be [pages]")
-    _vector("tables", tables, torch.int32, tables.shape, tables.device)
-    _vector("refs", refs, torch.int32, refs.shape, tables.device)
-    return KdaPageShape(tables.shape[0], tables.shape[1], refs.shape[0])
+    _vector("tables", tables, _I32, shape, device)
+    _vector("refs", refs, _I32, pages, device)
+    return KdaPageShape(shape[0], shape[1], pages[0])
 
 
 def _results(tables, refs, new_tables, new_refs):
-    for name, t, like in (("new_tables", new_tables, tables), ("new_refs", new_refs, refs)):
-        if t is not None:
-            _vector(name, t, torch.int32, like.shape, like.device)
-    return (torch.empty_like(tables) if new_tables is None else new_tables,
-            torch.empty_like(refs) if new_refs is None else new_refs)
+    if new_tables is None:
+        new_tables = torch.empty_like(tables)
+    else:
+        _vector("new_tables", new_tables, _I32, tables.shape, tables.device)
+    if new_refs is None:
+        new_refs = torch.empty_like(refs)
+    else:
+        _vector("new_refs", new_refs, _I32, refs.shape, refs.device)
+    return new_tables, new_refs
 
 
 def _pools(pools: Sequence[torch.Tensor], pages: int, device, layers_first: bool):
@@ -64,20 +95,20 @@ def _pools(pools: Sequence[torch.Tensor], pages: int, device, layers_first: bool
         raise ValueError("pools must be a sequence of tensors")
     lead = 1 if layers_first else 0
     table = (KdaPool * max(1, len(pools)))()
-    for x, t in zip(table, pools):
-        if t.device != device or t.dim() <= lead or t.shape[lead] != pages:
+    for i, t in enumerate(pools):
+        shape, stride = t.shape, t.stride()
+        if t.device != device or len(shape) <= lead or shape[lead] != pages:
             raise ValueError(f"a pool must be a tensor on {device} with {pages} pages in dim {lead}")
         inner = 1
-        for size, stride in zip(reversed(t.shape[lead + 1:]), reversed(t.stride()[lead + 1:])):
-            if size != 1 and stride != inner:
+        for dim in range(len(shape) - 1, lead, -1):
+            if shape[dim] != 1 and stride[dim] != inner:
                 raise ValueError("the pages of a pool must be contiguous")
-            inner *= size
+            inner *= shape[dim]
         elem = t.element_size()
-        x.base, x.page_bytes, x.page_stride = t.data_ptr(), inner * elem, t.stride(lead) * elem
-        if pages <= 1:
-            x.page_stride = max(x.page_stride, x.page_bytes)
-        x.layers = t.shape[0] if layers_first else 1
-        x.layer_stride = t.stride(0) * elem if layers_first else 0
+        inner *= elem
+        step = stride[lead] * elem
+        table[i] = KdaPool(t.data_ptr(), inner, max(step, inner) if pages <= 1 else step,
+                           stride[0] * elem if layers_first else 0, shape[0] if layers_first else 1)
     return table
 
 
@@ -92,12 +123,10 @@ def kda_pages_alloc(tables: torch.Tensor, refs: torch.Tensor, want: torch.Tensor
     """
     lib = load_library()
     shape = _pages(tables, refs)
-    _vector("want", want, torch.int32, (shape.rows,), tables.device)
+    _vector("want", want, _I32, (shape.rows,), tables.device)
     new_tables, new_refs = _results(tables, refs, new_tables, new_refs)
-    with torch.cuda.device(tables.device):
-        _check(lib, lib.kda_pages_alloc(ctypes.byref(shape), _ptr(tables), _ptr(refs), _ptr(want),
-                                        _ptr(new_tables), _ptr(new_refs),
-                                        _stream(stream, tables.device)))
+    _run(lib.kda_pages_alloc, tables.device, ctypes.byref(shape), _ptr(tables), _ptr(refs),
+         _ptr(want), _ptr(new_tables), _ptr(new_refs), _stream(stream, tables.device))
     return new_tables, new_refs
 
 
@@ -108,12 +137,10 @@ def kda_pages_free(tables: torch.Tensor, refs: torch.Tensor, drop: torch.Tensor,
     ``(new_tables, new_refs)``."""
     lib = load_library()
     shape = _pages(tables, refs)
-    _vector("drop", drop, (torch.bool, torch.uint8), (shape.rows,), tables.device)
+    _vector("drop", drop, _BYTES, (shape.rows,), tables.device)
     new_tables, new_refs = _results(tables, refs, new_tables, new_refs)
-    with torch.cuda.device(tables.device):
-        _check(lib, lib.kda_pages_free(ctypes.byref(shape), _ptr(tables), _ptr(refs), _ptr(drop),
-                                       _ptr(new_tables), _ptr(new_refs),
-                                       _stream(stream, tables.device)))
+    _run(lib.kda_pages_free, tables.device, ctypes.byref(shape), _ptr(tables), _ptr(refs),
+         _ptr(drop), _ptr(new_tables), _ptr(new_refs), _stream(stream, tables.device))
     return new_tables, new_refs
 
 
@@ -132,18 +159,16 @@ def kda_pages_fork(tables: torch.Tensor, refs: torch.Tensor, parents: torch.Tens
     """
     lib = load_library()
     shape = _pages(tables, refs)
-    _vector("parents", parents, torch.int32, (shape.rows,), tables.device)
+    _vector("parents", parents, _I32, (shape.rows,), tables.device)
     if page_tokens > 0 and lens is None:
         raise ValueError("lens is needed with page_tokens")
     if lens is not None:
-        _vector("lens", lens, torch.int32, (shape.rows,), tables.device)
+        _vector("lens", lens, _I32, (shape.rows,), tables.device)
     table = _pools(pools, shape.pages, tables.device, layers_first)
     new_tables, new_refs = _results(tables, refs, new_tables, new_refs)
-    with torch.cuda.device(tables.device):
-        _check(lib, lib.kda_pages_fork(ctypes.byref(shape), _ptr(tables), _ptr(refs),
-                                       _ptr(parents), _ptr(lens), int(page_tokens), table,
-                                       len(pools), _ptr(new_tables), _ptr(new_refs),
-                                       _stream(stream, tables.device)))
+    _run(lib.kda_pages_fork, tables.device, ctypes.byref(shape), _ptr(tables), _ptr(refs),
+         _ptr(parents), _ptr(lens), int(page_tokens), table, len(pools), _ptr(new_tables),
+         _ptr(new_refs), _stream(stream, tables.device))
     return new_tables, new_refs
 
 
@@ -162,11 +187,9 @@ def kda_pages_compact(tables: torch.Tensor, refs: torch.Tensor,
     new_tables, new_refs = _results(tables, refs, new_tables, new_refs)
     page_map = torch.empty_like(refs)
     num_live = torch.empty(1, dtype=torch.int32, device=refs.device)
-    with torch.cuda.device(tables.device):
-        _check(lib, lib.kda_pages_compact(ctypes.byref(shape), _ptr(tables), _ptr(refs), table,
-                                          len(pools), _ptr(new_tables), _ptr(new_refs),
-                                          _ptr(page_map), _ptr(num_live),
-                                          _stream(stream, tables.device)))
+    _run(lib.kda_pages_compact, tables.device, ctypes.byref(shape), _ptr(tables), _ptr(refs),
+         table, len(pools), _ptr(new_tables), _ptr(new_refs), _ptr(page_map), _ptr(num_live),
+         _stream(stream, tables.device))
     return new_tables, new_refs, page_map, num_live
 
 
@@ -179,50 +202,53 @@ def kda_pages_copy(src: torch.Tensor, dst: torch.Tensor, pools: Sequence[torch.T
     lib = load_library()
     if src.device.type != "cuda" or src.dim() != 1:
         raise ValueError("src must be [count] on cuda")
-    _vector("src", src, torch.int32, src.shape, src.device)
-    _vector("dst", dst, torch.int32, src.shape, src.device)
+    _vector("src", src, _I32, src.shape, src.device)
+    _vector("dst", dst, _I32, src.shape, src.device)
     if len(pools) == 0:
         return
     lead = 1 if layers_first else 0
     pages = pools[0].shape[lead] if pools[0].dim() > lead else -1
     table = _pools(pools, pages, src.device, layers_first)
-    with torch.cuda.device(src.device):
-        _check(lib, lib.kda_pages_copy(pages, src.shape[0], _ptr(src), _ptr(dst), table,
-                                       len(pools), _stream(stream, src.device)))
+    _run(lib.kda_pages_copy, src.device, pages, src.shape[0], _ptr(src), _ptr(dst), table,
+         len(pools), _stream(stream, src.device))
 
 
 def _cache(k_codes, v_codes, k_scale, v_scale, tables, lens, cu_tokens):
-    device = k_codes.device
+    device, shape = k_codes.device, k_codes.shape
     if device.type != "cuda":
         raise ValueError("k_codes must be on cuda")
-    if k_codes.dim() != 4:
+    if len(shape) != 4:
         raise ValueError("k_codes must be [pages, heads, page_tokens, head_dim]")
-    pages, heads, page_tokens, dim = k_codes.shape
-    for name, t in (("k_codes", k_codes), ("v_codes", v_codes)):
-        _vector(name, t, (torch.float8_e4m3fn, torch.uint8), k_codes.shape, device)
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        _vector(name, t, torch.float32, (pages, heads), device)
-    if tables.dim() != 2 or tables.shape[1] < 1:
+    pages, heads, page_tokens, dim = shape
+    _vector("k_codes", k_codes, _CODES, shape, device)
+    _vector("v_codes", v_codes, _CODES, shape, device)
+    scales = (pages, heads)
+    _vector("k_scale", k_scale, _F32, scales, device)
+    _vector("v_scale", v_scale, _F32, scales, device)
+    table = tables.shape
+    if len(table) != 2 or table[1] < 1:
         raise ValueError("tables must be [rows, width]")
-    _vector("tables", tables, torch.int32, tables.shape, device)
-    rows, width = tables.shape
-    _vector("lens", lens, torch.int32, (rows,), device)
+    _vector("tables", tables, _I32, table, device)
+    rows, width = table
+    _vector("lens", lens, _I32, (rows,), device)
     if cu_tokens is not None:
-        _vector("cu_tokens", cu_tokens, torch.int32, (rows + 1,), device)
-    p = lambda t: t.data_ptr()  # noqa: E731
-    return KdaKvCache(p(k_codes), p(v_codes), p(k_scale), p(v_scale), pages, page_tokens, heads, dim,
-                      p(tables), rows, width)
+        _vector("cu_tokens", cu_tokens, _I32, (rows + 1,), device)
+    return KdaKvCache(k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                      pages, page_tokens, heads, dim, tables.data_ptr(), rows, width), device, heads, dim
 
 
 def _act(name, t, heads, dim, device):
-    """[tokens, heads, head_dim] with contiguous heads; returns the token stride."""
+    """[tokens, heads, head_dim] with contiguous heads; returns tokens, heads, token stride."""
+    shape = t.shape
     if t.dtype not in _ACT_DTYPES or t.device != device:
         raise ValueError(f"{name} must be bf16 or fp16 on {device}")
-    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or t.shape[2] != dim:
+    if len(shape) != 3 or (heads is not None and shape[1] != heads) or shape[2] != dim:
         raise ValueError(f"{name} must be [tokens, {heads if heads else 'heads'}, {dim}]")
-    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != dim)):
+    tokens, heads, _ = shape
+    stride = t.stride()
+    if tokens and heads and (stride[2] != 1 or (heads > 1 and stride[1] != dim)):
         raise ValueError(f"the heads of {name} must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * dim
+    return tokens, heads, stride[0] if tokens > 1 else heads * dim
 
 
 def kda_kvcache_append(k: torch.Tensor, v: torch.Tensor, k_codes: torch.Tensor,
@@ -239,15 +265,14 @@ def kda_kvcache_append(k: torch.Tensor, v: torch.Tensor, k_codes: torch.Tensor,
     gives each row's share of the new tokens; without it every row has one.
     """
     lib = load_library()
-    cache = _cache(k_codes, v_codes, k_scale, v_scale, tables, lens, cu_tokens)
-    if k.dtype != v.dtype or k.shape != v.shape:
+    cache, device, heads, dim = _cache(k_codes, v_codes, k_scale, v_scale, tables, lens, cu_tokens)
+    if k.dtype is not v.dtype or k.shape != v.shape:
         raise ValueError("k and v must have the same type and shape")
-    ks = _act("k", k, cache.num_kv_heads, cache.head_dim, k_codes.device)
-    vs = _act("v", v, cache.num_kv_heads, cache.head_dim, k_codes.device)
-    with torch.cuda.device(k_codes.device):
-        _check(lib, lib.kda_kvcache_append(ctypes.byref(cache), _ptr(k), _ptr(v),
-                                           _ACT_DTYPES[k.dtype], ks, vs, k.shape[0], _ptr(lens),
-                                           _ptr(cu_tokens), _stream(stream, k_codes.device)))
+    tokens, _, ks = _act("k", k, heads, dim, device)
+    _, _, vs = _act("v", v, heads, dim, device)
+    _run(lib.kda_kvcache_append, device, ctypes.byref(cache), k.data_ptr(), v.data_ptr(),
+         _ACT_DTYPES[k.dtype], ks, vs, tokens, lens.data_ptr(), _ptr(cu_tokens),
+         _stream(stream, device))
 
 
 def kda_kvcache_attention(q: torch.Tensor, k_codes: torch.Tensor, v_codes: torch.Tensor,
@@ -263,20 +288,18 @@ def kda_kvcache_attention(q: torch.Tensor, k_codes: torch.Tensor, v_codes: torch
     zeros.  ``out`` may have a token stride of its own.
     """
     lib = load_library()
-    cache = _cache(k_codes, v_codes, k_scale, v_scale, tables, lens, cu_tokens)
-    qs = _act("q", q, None, cache.head_dim, k_codes.device)
+    cache, device, _, dim = _cache(k_codes, v_codes, k_scale, v_scale, tables, lens, cu_tokens)
+    tokens, heads, qs = _act("q", q, None, dim, device)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    elif out.dtype != q.dtype or out.shape != q.shape:
-        raise ValueError("out must have q's type and shape")
-    os_ = _act("out", out, q.shape[1], cache.head_dim, k_codes.device)
-    if scale is None:
-        scale = cache.head_dim ** -0.5
-    with torch.cuda.device(k_codes.device):
-        _check(lib, lib.kda_kvcache_attention(ctypes.byref(cache), _ptr(q), q.shape[1],
-                                              _ACT_DTYPES[q.dtype], qs, q.shape[0], _ptr(lens),
-                                              _ptr(cu_tokens), ctypes.c_float(scale), _ptr(out),
-                                              os_, _stream(stream, k_codes.device)))
+        out = torch.empty((tokens, heads, dim), dtype=q.dtype, device=device)
+        os_ = heads * dim
+    else:
+        if out.dtype is not q.dtype or out.shape != q.shape:
+            raise ValueError("out must have q's type and shape")
+        os_ = _act("out", out, heads, dim, device)[2]
+    _run(lib.kda_kvcache_attention, device, ctypes.byref(cache), q.data_ptr(), heads,
+         _ACT_DTYPES[q.dtype], qs, tokens, lens.data_ptr(), _ptr(cu_tokens),
+         dim ** -0.5 if scale is None else scale, out.data_ptr(), os_, _stream(stream, device))
     return out
 
 
@@ -294,26 +317,28 @@ def kda_beam_select(logits: torch.Tensor, scores: torch.Tensor, num_out: Optiona
     Places that no candidate is left for get -inf, -1, -1.
     """
     lib = load_library()
-    if logits.device.type != "cuda" or logits.dim() != 3 or logits.dtype not in _LOGIT_DTYPES:
+    device, shape = logits.device, logits.shape
+    if device.type != "cuda" or len(shape) != 3 or logits.dtype not in _LOGIT_DTYPES:
         raise ValueError("logits must be fp32, bf16 or fp16 [batch, beams, vocab] on cuda")
-    batch, beams, vocab = logits.shape
-    device = logits.device
-    stride = logits.stride(1) if beams > 1 else logits.stride(0) if batch > 1 else vocab
-    if logits.numel() and ((vocab > 1 and logits.stride(2) != 1) or
-                           (batch > 1 and logits.stride(0) != beams * stride)):
+    batch, beams, vocab = shape
+    steps = logits.stride()
+    stride = steps[1] if beams > 1 else steps[0] if batch > 1 else vocab
+    if batch and beams and ((vocab > 1 and steps[2] != 1) or (batch > 1 and steps[0] != beams * stride)):
         raise ValueError("logits must have contiguous rows at one stride")
-    _vector("scores", scores, torch.float32, (batch, beams), device)
+    rows = (batch, beams)
+    _vector("scores", scores, _F32, rows, device)
     if done is not None:
-        _vector("done", done, (torch.bool, torch.uint8), (batch, beams), device)
+        _vector("done", done, _BYTES, rows, device)
     k = beams if num_out is None else int(num_out)
     if k < 1:
         raise ValueError("num_out must be at least 1")
-    new_scores = torch.empty((batch, k), dtype=torch.float32, device=device)
-    tokens, parents = (torch.empty((batch, k), dtype=torch.int32, device=device) for _ in range(2))
-    new_done = None if done is None else torch.empty((batch, k), dtype=done.dtype, device=device)
-    with torch.cuda.device(device):
-        _check(lib, lib.kda_beam_select(batch, beams, vocab, k, _ptr(logits),
-                                        _LOGIT_DTYPES[logits.dtype], stride, _ptr(scores),
-                                        _ptr(done), int(eos), _ptr(new_scores), _ptr(tokens),
-                                        _ptr(parents), _ptr(new_done), _stream(stream, device)))
+    size = (batch, k)
+    new_scores = torch.empty(size, dtype=_F32, device=device)
+    tokens = torch.empty(size, dtype=_I32, device=device)
+    parents = torch.empty(size, dtype=_I32, device=device)
+    new_done = None if done is None else torch.empty(size, dtype=done.dtype, device=device)
+    _run(lib.kda_beam_select, device, batch, beams, vocab, k, logits.data_ptr(),
+         _LOGIT_DTYPES[logits.dtype], stride, scores.data_ptr(), _ptr(done), eos,
+         new_scores.data_ptr(), tokens.data_ptr(), parents.data_ptr(), _ptr(new_done),
+         _stream(stream, device))
     return (new_scores, tokens, parents) if done is None else (new_scores, tokens, parents, new_done)
