@@ -31,31 +31,16 @@
 // the loads paused there: 141 us instead of 128 for 64 rows of up to 8192 tokens, 8 heads.  Asking L2 for codes two to eight slabs
 // ahead made it 1 to 35% slower, slabs of 16 keys with four CTAs an SM 5%, two CTAs without
 // spills 10%.)
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <math.h>
-
-#include "kda_serving.cuh"
+#include "kda_kvcache_attention.cuh"
 
 namespace kda {
 namespace {
 
 constexpr int kThreads = 128, kWarps = 4;
 constexpr int kMaxListed = 1024;  // rows whose prefix fits in shared memory
-constexpr float kNegInf = -INFINITY;
-
 // Keys of a slab for items of `cols` query rows.
 __host__ __device__ constexpr int slab_keys(int cols) { return cols >= 32 ? 16 : 32; }
 
-__device__ __forceinline__ uint32_t widen2(uint32_t codes) {  // two e4m3 codes (low 16 bits)
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
-    return h;
-}
-__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -68,93 +53,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <typename T> struct Act;
-template <> struct Act<__nv_bfloat16> {
-    static __device__ __forceinline__ float2 two(uint32_t w) {
-        return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
-    }
-    static __device__ __forceinline__ uint32_t pack(float a, float b) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-        return *reinterpret_cast<const uint32_t*>(&h);
-    }
-};
-template <> struct Act<__half> {
-    static __device__ __forceinline__ float2 two(uint32_t w) {
-        return __half22float2(*reinterpret_cast<const __half2*>(&w));
-    }
-    static __device__ __forceinline__ uint32_t pack(float a, float b) { return pack_half2(a, b); }
-};
-
-// New tokens of row r: [begin, begin + n); n = 0 for malformed offsets.
-__device__ __forceinline__ int row_tokens(const CacheParams& c, int r, int64_t& begin) {
-    if (!c.cu) {
-        begin = r;
-        return 1;
-    }
-    begin = c.cu[r];
-    const int64_t end = c.cu[r + 1];
-    if (begin < 0 || end < begin || end > c.tokens || (r == 0 && begin != 0)) {
-        report(c.status, kStatusBadSeqlens);
-        return 0;
-    }
-    if (r == c.rows - 1 && end != c.tokens) report(c.status, kStatusBadSeqlens);
-    return (int)(end - begin);
-}
-// Cached tokens of row r that its table has places for.
-__device__ __forceinline__ int row_length(const CacheParams& c, int r) {
-    const int len = c.lens[r];
-    const int64_t room = (int64_t)c.width * c.page_tokens;
-    if (len < 0 || len > room) report(c.status, kStatusBadIndex);
-    return len < 0 ? 0 : len > room ? (int)room : len;
-}
 __device__ __forceinline__ int row_slabs(int len, int keys) { return len > keys ? (len + keys - 1) / keys : 1; }
-
-// first[r] = slabs of all items of the rows before r; first[rows] = all.  Items of a row: column
-// blocks (cols query rows each) by key/value heads.  The whole block calls it; s: one value a warp.
-__device__ void scan_rows(const AttentionParams& p, int cols, int64_t* first, int64_t* s) {
-    const CacheParams& c = p.c;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int group = p.q_heads / c.heads;
-    int64_t base = 0;
-    for (int r0 = 0; r0 < c.rows; r0 += kThreads) {
-        const int r = r0 + tid;
-        int64_t w = 0;
-        if (r < c.rows) {
-            int64_t begin;
-            const int n = row_tokens(c, r, begin);
-            w = ((int64_t)n * group + cols - 1) / cols * c.heads * row_slabs(row_length(c, r), slab_keys(cols));
-        }
-        int64_t x = w;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-        }
-        if (lane == 31) s[warp] = x;
-        __syncthreads();
-        int64_t before = base;
-        for (int i = 0; i < warp; ++i) before += s[i];
-        if (r < c.rows) first[r] = before + x - w;
-        for (int i = 0; i < kWarps; ++i) base += s[i];
-        __syncthreads();
-    }
-    if (tid == 0) first[c.rows] = base;
-}
-
-// The row that work number w belongs to: the last with first[row] <= w (rows without work
-// share their number with the next).
-__device__ __forceinline__ int row_of(const int64_t* first, int rows, int64_t w) {
-    int lo = 0, hi = rows;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (first[mid] <= w) lo = mid;
-        else hi = mid;
-    }
-    return lo;
-}
-
-// Slabs of one warp's share.
-__device__ __forceinline__ int64_t share_of(int64_t all, int warps) { return (all + warps - 1) / warps; }
 
 // Codes of 16 keys, widened, against the query rows: acc += K Q^T.  q(step, nt) gives the two
 // registers of a reduction step.
@@ -197,7 +96,11 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(c
     // Every CTA needs the rows' prefix; past kMaxListed rows all write the same values to the
     // scratch.
     int64_t* first = c.rows <= kMaxListed ? s_first : p.first_work;
-    scan_rows(p, kCols, first, s_scan);
+    scan_rows<kThreads>(c.rows, first, s_scan, [&](int r) {  // items: column blocks by key/value heads
+        int64_t begin;
+        const int n = row_tokens(c, r, begin);
+        return ((int64_t)n * group + kCols - 1) / kCols * c.heads * row_slabs(row_length(c, r), kKeys);
+    });
     __syncthreads();
     if (blockIdx.x == 0 && c.rows <= kMaxListed)
         for (int r = tid; r <= c.rows; r += kThreads) p.first_work[r] = s_first[r];
@@ -262,9 +165,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(c
                 }
             a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
             a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
-            // a in [2^e, 2^(e+1)): times 2^(14 - e); e limited so that both factors are normal.
-            int e = a > 0.f && a < INFINITY ? ilogbf(a) : 0;
-            e = max(e, -100);
+            const int e = row_exponent(a);
             const float up = exp2f((float)(14 - e));
             q_scale[nt] = exp2f((float)(e - 14)) * p.scale;
 #pragma unroll
@@ -517,24 +418,8 @@ __global__ void __launch_bounds__(kSplit ? kJoinSplit * 32 : kDim * 2) attention
     const int nt = blockIdx.y, j = kSplit ? blockIdx.z : warp;
     const int group = p.q_heads / c.heads;
     int64_t i = blockIdx.x;
-    int row = 0;
-    if (!c.cu) {
-        const int blocks = (group + kCols - 1) / kCols;
-        row = (int)(i / ((int64_t)c.heads * blocks));
-        i -= (int64_t)row * c.heads * blocks;
-    } else {
-        // Item numbers by an upper bound: row r's first item is number
-        // (cu[r] * group / kCols + r) * heads (its blocks are at most n * group / kCols + 1).
-        int lo = 0, hi = c.rows;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (((int64_t)c.cu[mid] * group / kCols + mid) * c.heads <= i) lo = mid;
-            else hi = mid;
-        }
-        row = lo;
-        i -= ((int64_t)c.cu[row] * group / kCols + row) * c.heads;
-    }
-    if (row >= c.rows || i < 0) return;
+    int row;
+    if (!joined_item(c, group, kCols, i, row)) return;
     int64_t begin;
     const int n = row_tokens(c, row, begin);
     const int slabs = row_slabs(row_length(c, row), slab_keys(kCols));
@@ -601,8 +486,7 @@ cudaError_t launch_one(const AttentionParams& p, cudaStream_t stream) {
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int64_t group = p.q_heads / c.heads;
-    const int64_t items = c.cu ? (c.tokens * group / kCols + c.rows) * c.heads
-                               : (int64_t)c.rows * c.heads * ((group + kCols - 1) / kCols);
+    const int64_t items = joined_items(c, group, kCols);
     // Fewer items than SMs leave SMs idle and have many parts each.
     const bool split = items * kNT < p.sm_count;
     cudaLaunchConfig_t cfg = {};
@@ -618,14 +502,18 @@ cudaError_t launch_one(const AttentionParams& p, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, attention_join_kernel<T, kDim, kNT, false>, p);
 }
 
+// CTAs an SM holds; the same on every device the library runs on.
 template <typename T, int kDim, int kNT>
 int resident() {
-    int n = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attention_kernel<T, kDim, kNT>, kThreads, 0) != cudaSuccess || n < 1) {
-        cudaGetLastError();
-        n = 1;
-    }
-    return n;
+    static const int count = [] {
+        int n = 0;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attention_kernel<T, kDim, kNT>, kThreads, 0) != cudaSuccess || n < 1) {
+            cudaGetLastError();
+            n = 1;
+        }
+        return n;
+    }();
+    return count;
 }
 
 template <typename T, int kDim>
@@ -643,19 +531,18 @@ int resident_cols(int cols) {
 
 }  // namespace
 
-// Query rows of an item: as few of 8, 16 and 32 as hold one row's (token, head) pairs.
+// Query rows of an item: as few of 8, 16 and 32 as hold one row's (token, head) pairs, or 128
+// on tcgen05 where a row has more than kFewRows of them.
+constexpr int kFewRows = 32;
 int attention_cols(int64_t tokens, int32_t rows, int32_t group) {
     const int64_t each = (tokens + rows - 1) / rows * group;
-    return each <= 8 ? 8 : each <= 16 ? 16 : 32;
-}
-
-size_t attention_scratch(int32_t rows, int32_t dim, int cols, int ctas) {
-    return ((size_t)rows + 1) * 8 + 16 + (size_t)2 * ctas * kWarps * cols * (dim + 2) * 4;
+    return each <= 8 ? 8 : each <= 16 ? 16 : each <= kFewRows ? 32 : kBlockRows;
 }
 
 size_t attention_slots(int ctas) { return (size_t)2 * ctas * kWarps; }
 
 int attention_ctas(int32_t dim, int cols, bool f16, int sm_count) {
+    if (cols == kBlockRows) return 2 * sm_count;
     int n;
     if (dim == 64) n = f16 ? resident_cols<__half, 64>(cols) : resident_cols<__nv_bfloat16, 64>(cols);
     else n = f16 ? resident_cols<__half, 128>(cols) : resident_cols<__nv_bfloat16, 128>(cols);
@@ -663,6 +550,7 @@ int attention_ctas(int32_t dim, int cols, bool f16, int sm_count) {
 }
 
 cudaError_t launch_attention(const AttentionParams& p, int cols, bool f16, cudaStream_t stream) {
+    if (cols == kBlockRows) return launch_block_attention(p, f16, stream);
     if (p.c.dim == 64)
         return f16 ? launch_cols<__half, 64>(p, cols, stream) : launch_cols<__nv_bfloat16, 64>(p, cols, stream);
     return f16 ? launch_cols<__half, 128>(p, cols, stream) : launch_cols<__nv_bfloat16, 128>(p, cols, stream);

@@ -399,7 +399,7 @@ kda_status kda_kvcache_attention(const kda_kvcache* cache, const void* q, int32_
                                  {"cu_tokens", {cu_tokens, ((size_t)cache->rows + 1) * 4}}})) != KDA_OK)
             return st;
         const int32_t group = num_q_heads / cache->num_kv_heads;
-        if ((num_tokens * group / 8 + cache->rows) * cache->num_kv_heads > 0x7fffffff)
+        if (num_tokens * group > 0x7fffff00 || (num_tokens * group / 8 + cache->rows) * cache->num_kv_heads > 0x7fffffff)
             return fail(KDA_ERR_INVALID_ARGUMENT, "too many tokens for one launch");
         int dev = 0;
         DeviceInfo* di = nullptr;
@@ -411,11 +411,12 @@ kda_status kda_kvcache_attention(const kda_kvcache* cache, const void* q, int32_
         p.c = cache_params(cache, num_tokens, lens, cu_tokens, di->status);
         p.sm_count = di->sm_count;
         p.ctas = kda::attention_ctas(cache->head_dim, cols, f16, di->sm_count);
+        const size_t parts = (cols == kda::kBlockRows ? (size_t)2 * p.ctas : kda::attention_slots(p.ctas)) * cols;
         char* ws = nullptr;
-        if ((st = scratch(dev, stream, kda::attention_scratch(cache->rows, cache->head_dim, cols, p.ctas), &ws)) != KDA_OK) return st;
+        if ((st = scratch(dev, stream, parts * (cache->head_dim + 2) * 4 + ((size_t)cache->rows + 1) * 8, &ws)) != KDA_OK) return st;
         p.part_o = reinterpret_cast<float*>(ws);
-        p.part_ml = p.part_o + kda::attention_slots(p.ctas) * cols * cache->head_dim;
-        p.first_work = reinterpret_cast<int64_t*>(p.part_ml + kda::attention_slots(p.ctas) * cols * 2);
+        p.part_ml = p.part_o + parts * cache->head_dim;
+        p.first_work = reinterpret_cast<int64_t*>(p.part_ml + parts * 2);
         p.q = q;
         p.out = out;
         p.q_stride = q_stride;

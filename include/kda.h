@@ -397,8 +397,8 @@ kda_status kda_kvcache_append(const kda_kvcache* cache, const void* k, const voi
  *   cu_tokens     device int32 [rows + 1] or NULL: one token for each row, num_tokens = rows
  *   scale         finite
  * Codes at positions below lens[r] must be finite (the append writes no others); what a page
- * holds past them is never used.  Positions whose page is missing are skipped and
- * recorded as KDA_ERR_INVALID_ARGUMENT. */
+ * holds past them is never used.  Scales of pages in use are finite and not negative.  Positions
+ * whose page is missing are skipped and recorded as KDA_ERR_INVALID_ARGUMENT. */
 kda_status kda_kvcache_attention(const kda_kvcache* cache, const void* q, int32_t num_q_heads,
                                  int32_t act_dtype, int64_t q_stride, int64_t num_tokens,
                                  const int32_t* lens, const int32_t* cu_tokens, float scale,
