@@ -1164,10 +1164,11 @@ kda_status kda_decode_paged(const kda_shape* shape, const uint16_t* q, const uin
         return fail(KDA_ERR_INVALID_ARGUMENT, "state_pages must be a 4-byte aligned pointer");
     if (pages < 0 || (pages > 0 && (!states || !aligned(states, 16))))
         return fail(KDA_ERR_INVALID_ARGUMENT, "states must be a 16-byte aligned pool of pages >= 0");
-    if (page_stride < page_elems || page_stride % 8 != 0 || page_stride > (int64_t)1 << 40)
+    if (page_stride < page_elems || page_stride % 8 != 0 ||
+        (pages > 0 && page_stride > ((int64_t)1 << 46) / pages))
         return fail(KDA_ERR_INVALID_ARGUMENT,
-                    "page_stride must be a multiple of 8, at least num_heads * 128 * 128 (got %lld)",
-                    (long long)page_stride);
+                    "page_stride must be a multiple of 8, at least num_heads * 128 * 128, and pages * "
+                    "page_stride at most 2^46 (got %lld)", (long long)page_stride);
     const size_t pool = pages > 0 ? ((size_t)(pages - 1) * page_stride + page_elems) * elem : 0;
     const Sizes sz = sizes_of(pr, elem);
     const Range others[] = {{q, sz.q}, {k, sz.k}, {v, sz.v}, {g, sz.g}, {beta, sz.beta}, {out, sz.out},

@@ -1,5 +1,5 @@
 // kda_kvcache_attention.cu -- causal attention over the 8-bit paged cache, for one or a few
-// new tokens a row.
+// new tokens a row (up to 16 query rows for a key/value head; kda_kvcache_block.cu takes more).
 //
 // Query rows (token, query head of a group) that share a key/value head go through the cache
 // together: an item is kCols = 8 kNT such rows of one (row, key/value head), so the codes are
@@ -23,14 +23,14 @@
 // enters as its ratio to the largest one met, so weights stay in [0, 1].  Running maximum,
 // sums, outputs and the joined parts are fp32.
 //
-// Work split: warps work alone.  The items' cached tokens, cut into slabs of 32 (16 where an
-// item has 32 query rows), are numbered through all items; every resident warp takes an equal
-// contiguous share, however long the rows are.  An item inside one share is written at once;
-// the parts of the others, in the layout of the product's fragments, are joined by a second
-// launch.  (With four warps sharing each tile and joining in shared memory at every item's end
-// the loads paused there: 141 us instead of 128 for 64 rows of up to 8192 tokens, 8 heads.  Asking L2 for codes two to eight slabs
-// ahead made it 1 to 35% slower, slabs of 16 keys with four CTAs an SM 5%, two CTAs without
-// spills 10%.)
+// Work split: warps work alone.  The items' cached tokens, cut into slabs of 32, are numbered
+// through all items; every resident warp takes an equal contiguous share, however long the rows
+// are.  An item inside one share is written at once; the parts of the others, in the layout of
+// the product's fragments, are joined by a second launch.  (With four warps sharing each tile
+// and joining in shared memory at every item's end the loads paused there: 141 us instead of
+// 128 for 64 rows of up to 8192 tokens, 8 heads.  Asking L2 for codes two to eight slabs ahead
+// made it 1 to 35% slower, slabs of 16 keys with four CTAs an SM 5%, two CTAs without spills
+// 10%.)
 #include "kda_kvcache_attention.cuh"
 
 namespace kda {
@@ -38,8 +38,7 @@ namespace {
 
 constexpr int kThreads = 128, kWarps = 4;
 constexpr int kMaxListed = 1024;  // rows whose prefix fits in shared memory
-// Keys of a slab for items of `cols` query rows.
-__host__ __device__ constexpr int slab_keys(int cols) { return cols >= 32 ? 16 : 32; }
+constexpr int kKeys = 32, kBlk = kKeys / 16;  // keys of a slab, and blocks of 16 in it
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
@@ -53,7 +52,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ int row_slabs(int len, int keys) { return len > keys ? (len + keys - 1) / keys : 1; }
+__device__ __forceinline__ int row_slabs(int len) { return len > kKeys ? (len + kKeys - 1) / kKeys : 1; }
 
 // Codes of 16 keys, widened, against the query rows: acc += K Q^T.  q(step, nt) gives the two
 // registers of a reduction step.
@@ -78,14 +77,11 @@ __device__ __forceinline__ void product_k(float (&acc)[kNT][4], const uint4 (&k)
 template <typename T, int kDim, int kNT>
 __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(const __grid_constant__ AttentionParams p) {
     constexpr int kCols = 8 * kNT;
-    constexpr int kKeys = slab_keys(kCols), kBlk = kKeys / 16;
     constexpr int kHalves = kDim / 64;   // 16-byte loads of a key by a thread
     constexpr int kSteps = kDim / 16;    // reduction steps of S^T
     constexpr int kMT = kDim / 16;       // 16-channel tiles of O^T
     constexpr int kVWords = kDim / 32;   // 4-byte words of a V load
-    constexpr bool kQShared = kNT > 2;   // q does not fit in registers beside the sums
     __shared__ int64_t s_first[kMaxListed + 1], s_scan[kWarps];
-    __shared__ uint2 s_q[kQShared ? kWarps : 1][kQShared ? kSteps * kNT : 1][32];
 
     const CacheParams& c = p.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -99,7 +95,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(c
     scan_rows<kThreads>(c.rows, first, s_scan, [&](int r) {  // items: column blocks by key/value heads
         int64_t begin;
         const int n = row_tokens(c, r, begin);
-        return ((int64_t)n * group + kCols - 1) / kCols * c.heads * row_slabs(row_length(c, r), kKeys);
+        return ((int64_t)n * group + kCols - 1) / kCols * c.heads * row_slabs(row_length(c, r));
     });
     __syncthreads();
     if (blockIdx.x == 0 && c.rows <= kMaxListed)
@@ -113,7 +109,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(c
     for (int64_t w = w_begin; w < w_end;) {
         const int row = row_of(first, c.rows, w);
         int64_t begin;
-        const int n = row_tokens(c, row, begin), len = row_length(c, row), slabs = row_slabs(len, kKeys);
+        const int n = row_tokens(c, row, begin), len = row_length(c, row), slabs = row_slabs(len);
         const int64_t i_row = (w - first[row]) / slabs, item = first[row] + i_row * slabs, item_end = item + slabs;
         const int head = (int)(i_row % c.heads), block = (int)(i_row / c.heads);
         const int slab0 = (int)(w - item);
@@ -139,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(c
         constexpr int kBatch = 32 / kBlk;  // slabs whose pages a warp holds
         int32_t pages = page_at(slab0 * kBlk + lane), pages_next = -1;
 
-        uint32_t q[kQShared ? 1 : kNT][kQShared ? 1 : kSteps][2];
+        uint32_t q[kNT][kSteps][2];
         float q_scale[kNT];  // of column 8 nt + g
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
@@ -172,20 +168,11 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(c
             for (int h = 0; h < kHalves; ++h)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const uint32_t y0 = pack_half2(x[h][4 * j] * up, x[h][4 * j + 1] * up);
-                    const uint32_t y1 = pack_half2(x[h][4 * j + 2] * up, x[h][4 * j + 3] * up);
-                    if constexpr (kQShared) {
-                        s_q[warp][(4 * h + j) * kNT + nt][lane] = make_uint2(y0, y1);
-                    } else {
-                        q[nt][4 * h + j][0] = y0;
-                        q[nt][4 * h + j][1] = y1;
-                    }
+                    q[nt][4 * h + j][0] = pack_half2(x[h][4 * j] * up, x[h][4 * j + 1] * up);
+                    q[nt][4 * h + j][1] = pack_half2(x[h][4 * j + 2] * up, x[h][4 * j + 3] * up);
                 }
         }
-        auto q_at = [&](int step, int nt) {
-            if constexpr (kQShared) return s_q[warp][step * kNT + nt][lane];  // this lane's own
-            else return make_uint2(q[nt][step][0], q[nt][step][1]);
-        };
+        auto q_at = [&](int step, int nt) { return make_uint2(q[nt][step][0], q[nt][step][1]); };
         // What each column sees and its factor, for this thread's column pairs.
         int seen[kNT][2];
         float factor[kNT][2];
@@ -224,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(c
 #pragma unroll
                     for (int r = 0; r < 2; ++r)
 #pragma unroll
-                        for (int h = 0; h < kHalves; ++h) kr[i][r][h] = __ldg(reinterpret_cast<const uint4*>(src + 8 * r * kDim + 64 * h));
+                        for (int h = 0; h < kHalves; ++h) kr[i][r][h] = load_codes16(src + 8 * r * kDim + 64 * h);
                 } else {
 #pragma unroll
                     for (int r = 0; r < 2; ++r)
@@ -248,10 +235,10 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(c
                     for (int x = 0; x < kVWords; ++x) vr[i][r][x] = 0u;  // what no column sees stays out
                     if (whole || (page >= 0 && key0 + key < seen_max)) {
                         if constexpr (kVWords == 4) {
-                            const uint4 v = __ldg(reinterpret_cast<const uint4*>(src + off));
+                            const uint4 v = load_codes16(src + off);
                             vr[i][r][0] = v.x; vr[i][r][1] = v.y; vr[i][r][2] = v.z; vr[i][r][3] = v.w;
                         } else {
-                            const uint2 v = __ldg(reinterpret_cast<const uint2*>(src + off));
+                            const uint2 v = load_codes8(src + off);
                             vr[i][r][0] = v.x; vr[i][r][1] = v.y;
                         }
                     }
@@ -422,7 +409,7 @@ __global__ void __launch_bounds__(kSplit ? kJoinSplit * 32 : kDim * 2) attention
     if (!joined_item(c, group, kCols, i, row)) return;
     int64_t begin;
     const int n = row_tokens(c, row, begin);
-    const int slabs = row_slabs(row_length(c, row), slab_keys(kCols));
+    const int slabs = row_slabs(row_length(c, row));
     cudaGridDependencySynchronize();
     const int64_t all = p.first_work[c.rows], w_row = p.first_work[row], w_next = p.first_work[row + 1];
     const int64_t per = share_of(all, p.ctas * kWarps);
@@ -519,24 +506,25 @@ int resident() {
 template <typename T, int kDim>
 cudaError_t launch_cols(const AttentionParams& p, int cols, cudaStream_t stream) {
     if (cols == 8) return launch_one<T, kDim, 1>(p, stream);
-    if (cols == 16) return launch_one<T, kDim, 2>(p, stream);
-    return launch_one<T, kDim, 4>(p, stream);
+    return launch_one<T, kDim, 2>(p, stream);
 }
 template <typename T, int kDim>
 int resident_cols(int cols) {
     if (cols == 8) return resident<T, kDim, 1>();
-    if (cols == 16) return resident<T, kDim, 2>();
-    return resident<T, kDim, 4>();
+    return resident<T, kDim, 2>();
 }
 
 }  // namespace
 
-// Query rows of an item: as few of 8, 16 and 32 as hold one row's (token, head) pairs, or 128
-// on tcgen05 where a row has more than kFewRows of them.
-constexpr int kFewRows = 32;
+// Query rows of an item: 8 or 16 where they hold one row's (token, head) pairs, else 128 on
+// tcgen05.  Items of 32 rows here, against tcgen05, with 24 or 32 pairs a row and 4 key/value
+// heads: 64 rows of 4096 tokens 87 against 67 us (head_dim 64) and 129 against 108 (128), 16 rows
+// of 4096 tokens 36 against 31 and 46 against 43, only 4 rows of 1000 tokens 15 against 22 and
+// 20 against 25.  With 16 pairs and 64 rows of 4096 tokens items of 16 take 52 and 66 us.
+constexpr int kFewRows = 16;
 int attention_cols(int64_t tokens, int32_t rows, int32_t group) {
     const int64_t each = (tokens + rows - 1) / rows * group;
-    return each <= 8 ? 8 : each <= 16 ? 16 : each <= kFewRows ? 32 : kBlockRows;
+    return each <= 8 ? 8 : each <= kFewRows ? 16 : kBlockRows;
 }
 
 size_t attention_slots(int ctas) { return (size_t)2 * ctas * kWarps; }

@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
                                      (((tile * kKeys + mine * 16) & (c.page_tokens - 1)) + lane % 8) * kDim + lane / 8 * 16;
 #pragma unroll
                 for (int i = 0; i < kLoads; ++i)
-                    raw[i] = page >= 0 && lane % 8 + 8 * (i % 2) < keys ? __ldg(reinterpret_cast<const uint4*>(src + i % 2 * 8 * kDim + i / 2 * 64))
+                    raw[i] = page >= 0 && lane % 8 + 8 * (i % 2) < keys ? load_codes16(src + i % 2 * 8 * kDim + i / 2 * 64)
                                                                         : make_uint4(0u, 0u, 0u, 0u);
             };
             auto widen = [](const uint4& r, uint4& lo, uint4& hi) {

@@ -89,6 +89,10 @@ kda_status make_pools(const kda_pool* pools, int32_t n, int32_t pages, kda::Pool
         if (used && !a.base) return fail(KDA_ERR_INVALID_ARGUMENT, "pool %d: base is NULL", i);
         if (used && (a.page_stride < a.page_bytes || a.page_stride > (int64_t)1 << 40))
             return fail(KDA_ERR_INVALID_ARGUMENT, "pool %d: page_stride is smaller than page_bytes", i);
+        // Offsets stay below 2^47.
+        if (used && (a.page_stride > ((int64_t)1 << 46) / pages ||
+                     (a.layers > 1 && (a.layer_stride < 0 || a.layer_stride > ((int64_t)1 << 46) / a.layers))))
+            return fail(KDA_ERR_INVALID_ARGUMENT, "pool %d: page_stride or layer_stride is too large", i);
         const int64_t extent = used ? (int64_t)(pages - 1) * a.page_stride + a.page_bytes : 0;
         // Layers either follow one another or lie inside each other's page stride.
         if (used && a.layers > 1 && a.layer_stride < extent &&

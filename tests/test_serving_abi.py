@@ -51,7 +51,8 @@ def test_pool_rules(lib):
     good = KdaPool(0x100000, 64, 64, 640, 2)
     assert fork(lib, pools=[good]) not in (INVALID, ALIAS)
     for bad in (KdaPool(None, 64, 64, 640, 1), KdaPool(0x100000, 64, 32, 640, 1), KdaPool(0x100000, -1, 64, 640, 1),
-                KdaPool(0x100000, 64, 64, 640, -1), KdaPool(0x100000, 64, 64, 320, 2)):
+                KdaPool(0x100000, 64, 64, 640, -1), KdaPool(0x100000, 64, 64, 320, 2),
+                KdaPool(0x100000, 64, 1 << 46, 640, 1), KdaPool(0x100000, 64, 64, 1 << 50, 2), KdaPool(0x100000, 64, 64, -640, 2)):
         assert fork(lib, pools=[bad]) == INVALID
     # layers inside the page stride ([pages][layers] order) are fine
     assert fork(lib, pools=[KdaPool(0x100000, 64, 128, 64, 2)]) not in (INVALID, ALIAS)
@@ -144,7 +145,7 @@ def test_paged_decode_rules(lib):
     assert call(shape=(2, 1, 0, 2, 128, 4)) == INVALID       # grouped query heads
     assert call(shape=(2, 1, 0, 4, 128, 2), stride=65536) not in (INVALID, ALIAS)
     assert call(states=None) == INVALID and call(states=0x70000008) == INVALID and call(pages=-1) == INVALID
-    assert call(stride=16384) == INVALID and call(stride=32772) == INVALID
+    assert call(stride=16384) == INVALID and call(stride=32772) == INVALID and call(stride=1 << 46) == INVALID
     assert call(at=None) == INVALID and call(at=0x78000002) == INVALID and call(dt=2) == INVALID
     assert call(out=0x70000100) == ALIAS and call(at=0x70000000) == ALIAS
 
