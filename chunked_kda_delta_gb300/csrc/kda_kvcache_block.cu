@@ -13,7 +13,7 @@
 // a thread and spills); two CTAs an SM.  S(j + 1) is computed and V(j) widened while the softmax
 // of tile j runs.  (One kind of warps for
 // everything, two threads a row, took 4300 cycles a tile: 1000 of them issuing, the rest
-// waiting for each other at three barriers; 159 us instead of 90 for 8 pieces of up to 512
+// waiting for each other at three barriers; 159 us instead of 88 for 8 pieces of up to 512
 // tokens, 16 heads of 64 over 4, 4096 cached.)
 // O is rescaled only when a row's maximum has grown by more than 2^8 (or a page's v scale by
 // more than 2^4) over the one in use: weights stay below 2^12 in fp16 and the sums are the
@@ -37,7 +37,7 @@ constexpr int kThreads = kSoft + kWiden;
 constexpr int kMaxListed = 512;           // rows whose prefix fits in shared memory
 constexpr float kGrowth = 8.f;            // log2 of how far a maximum may grow
 constexpr uint32_t kColS = 0, kColO = 128, kColumns = 256;  // tensor memory: S and P twice, O
-constexpr int64_t kWaitLimit = 1ll << 22;
+constexpr int64_t kWaitLimit = 1ll << 20;
 // Two CTAs an SM and no third: the tensor memory is for two.
 constexpr size_t kSmemBytes = 80 * 1024;
 
@@ -94,8 +94,8 @@ __device__ __forceinline__ void commit_one(uint32_t bar) {
         : "memory");
 }
 
-// Named barriers for the issuing warp: K is widened; V is, and P is written.
-constexpr uint32_t kBarK = 1, kBarP = 2;
+// Named barriers for the issuing warp: K is widened; V is, and P is written; q is there.
+constexpr uint32_t kBarK = 1, kBarP = 2, kBarQ = 3;
 
 // fp16 operands, fp32 result; `b_rows`: B's rows are the reduction (channel-major).
 __host__ __device__ constexpr uint32_t idesc_f16(int n, bool b_rows) {
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
     __shared__ int64_t s_first[kMaxListed + 1], s_scan[kThreads / 32];
     __shared__ __align__(16) Meta s_meta[4][kBlocks];
     __shared__ volatile int s_bad;  // a wait ran out
-    __shared__ __align__(8) uint64_t s_bar[2];
+    __shared__ __align__(8) uint64_t s_bar[3];
     __shared__ uint32_t s_tmem;
     unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     unsigned char* v_sm = smem;
@@ -145,10 +145,14 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
     const int group = p.q_heads / c.heads;
     const int page_shift = __ffs(c.page_tokens) - 1;
     const int64_t block_bytes = (int64_t)c.page_tokens * kDim;
-    const uint32_t bar_s = smem_u32(&s_bar[0]), bar_o = smem_u32(&s_bar[1]);
+    // S of a tile is there (one barrier for each buffer: S(j + 1) may be done before the softmax has
+    // seen S(j), and a barrier must not run two phases ahead of a waiter); O += P V is done.
+    const uint32_t bar_s = smem_u32(&s_bar[0]), bar_o = smem_u32(&s_bar[2]);
+    auto bar_of = [&](int j) { return bar_s + 8 * (j & 1); };  // j: tiles of the item so far
 
     if (tid == 0) {
-        mbar_init(bar_s, 1 + kBlocks);  // S is computed, and the widening warps' scales are there
+        mbar_init(bar_of(0), 1 + kBlocks);  // S is computed, and the widening warps' scales are there
+        mbar_init(bar_of(1), 1 + kBlocks);
         mbar_init(bar_o, 1);
         fence_mbar_init();
         s_bad = 0;
@@ -175,11 +179,18 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
     const uint32_t tmem = s_tmem, lanes = (uint32_t)(32 * (warp % 4)) << 16;
     const int64_t per = share_of(first[c.rows], p.ctas);
     const int64_t w_begin = per * blockIdx.x, w_end = min(first[c.rows], w_begin + per);
-    uint32_t phase_s = 0, phase_o = 0;
+    uint32_t phase_s = 0, phase_o = 0;  // (phase_s: a bit for each buffer)
     // After a wait that ran out, all others end at once and what follows is garbage.
-    auto wait = [&](uint32_t bar, uint32_t& phase) {
+    auto wait = [&](uint32_t bar, uint32_t phase) {
         if (!mbar_try_wait_now(bar, phase) && !mbar_wait_now(bar, phase, s_bad ? 1 : kWaitLimit)) s_bad = 1;
-        phase ^= 1;
+    };
+    auto wait_s = [&](int j) {
+        wait(bar_of(j), (phase_s >> (j & 1)) & 1);
+        phase_s ^= 1u << (j & 1);
+    };
+    auto wait_o = [&]() {
+        wait(bar_o, phase_o);
+        phase_o ^= 1;
     };
 
     for (int64_t w = w_begin; w < w_end;) {
@@ -223,33 +234,47 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
         if (soft) {
             const T* src = static_cast<const T*>(p.q) + (begin + (there ? f / group : 0)) * p.q_stride +
                            (int64_t)(head * group + (there ? f % group : 0)) * kDim;
-            float a = 0.f;
-            for (int i = 0; i < kDim / 8; ++i) {
-                const uint4 v = there ? reinterpret_cast<const uint4*>(src)[i] : make_uint4(0u, 0u, 0u, 0u);
-                const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+            // 64 channels in registers at a time; of 128 the first half is read again (L1).
+            uint4 raw[8];
+            auto read = [&](int half) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 y = Act<T>::two(u[k]);
-                    a = fmaxf(a, fmaxf(fabsf(y.x), fabsf(y.y)));
+                for (int i = 0; i < 8; ++i) raw[i] = there ? reinterpret_cast<const uint4*>(src)[8 * half + i] : make_uint4(0u, 0u, 0u, 0u);
+            };
+            float a = 0.f;
+#pragma unroll
+            for (int half = 0; half < kDim / 64; ++half) {
+                read(half);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 y = Act<T>::two(u[k]);
+                        a = fmaxf(a, fmaxf(fabsf(y.x), fabsf(y.y)));
+                    }
                 }
             }
             const int e = row_exponent(a);
             // The sign of the scale goes with q, so that factors are not negative.
             const float up = copysignf(exp2f((float)(14 - e)), p.scale);
             factor = exp2f((float)(e - 14)) * fabsf(p.scale);
-            for (int i = 0; i < kDim / 8; ++i) {
-                const uint4 v = there ? reinterpret_cast<const uint4*>(src)[i] : make_uint4(0u, 0u, 0u, 0u);
-                uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 y = Act<T>::two(u[k]);
-                    u[k] = pack_half2(y.x * up, y.y * up);
+            for (int half = kDim / 64 - 1; half >= 0; --half) {
+                if (half < kDim / 64 - 1) read(half);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 y = Act<T>::two(u[k]);
+                        u[k] = pack_half2(y.x * up, y.y * up);
+                    }
+                    *reinterpret_cast<uint4*>(q_sm + (tid / 8) * kSbo + (8 * half + i) * kLbo + (tid % 8) * 16) = make_uint4(u[0], u[1], u[2], u[3]);
                 }
-                *reinterpret_cast<uint4*>(q_sm + (tid / 8) * kSbo + i * kLbo + (tid % 8) * 16) = make_uint4(u[0], u[1], u[2], u[3]);
             }
             fence_proxy_async_smem();
+            named_bar_arrive(kBarQ, kSoft + 32);
         }
-        __syncthreads();  // q is there
 
         // Matrix instructions of the issuing warp: S of a tile into its buffer, O += P V.
         const uint64_t qd = sdesc(smem_u32(q_sm), kLbo, kSbo), kd = sdesc(smem_u32(k_sm), kLbo, kSbo);
@@ -259,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
 #pragma unroll
             for (int kk = 0; kk < kDim / 16; ++kk)  // (a step is 2 core matrices: 16 units of 16 bytes)
                 mma_ss_one(d, qd + kk * (2 * kLbo / 16), kd + kk * (2 * kLbo / 16), idesc_f16(kKeys, false), kk > 0);
-            commit_one(bar_s);
+            commit_one(bar_of(tile - tile0));
         };
         auto issue_o = [&](int tile) {
             const uint32_t a = tmem + kColS + ((tile - tile0) & 1) * kKeys;
@@ -314,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
                 }
                 if (lane == 0) {
                     s_meta[tile & 3][mine] = meta;
-                    mbar_arrive(bar_s);
+                    mbar_arrive(bar_of(tile - tile0));
                 }
                 fence_proxy_async_smem();
                 if (issuer) named_bar_sync(kBarK, kWiden);
@@ -331,18 +356,19 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
                 load(kr, c.k_codes, tile0, page, 16);
                 load(vr, c.v_codes, tile0, page, meta.v > 0.f ? seen_max - tile0 * kKeys - mine * 16 : 0);
                 put_k(kr, tile0, meta);
-                if (issuer) {
-                    tc_fence_after();
-                    issue_s(tile0);
-                }
                 load(kr, c.k_codes, tile0 + 1, page1, 16);
             }
+            if (issuer) {
+                named_bar_sync(kBarQ, kSoft + 32);
+                tc_fence_after();
+                if (tile0 < tile1) issue_s(tile0);
+            }
             for (int tile = tile0; tile < tile1; ++tile) {
-                wait(bar_s, phase_s);  // K's shared memory is free
+                wait_s(tile - tile0);  // K's shared memory is free
                 if (tile + 1 < tile1) put_k(kr, tile + 1, meta1);
                 // V's is, and the place of P(tile - 1), which S(tile + 1) takes: matrix instructions
                 // with different results are not ordered by themselves.
-                if (tile > tile0) wait(bar_o, phase_o);
+                if (tile > tile0) wait_o();
                 if (issuer && tile + 1 < tile1) {
                     tc_fence_after();
                     issue_s(tile + 1);
@@ -369,10 +395,10 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
                     named_bar_arrive(kBarP, kThreads);
                 }
             }
-            if (tile0 < tile1) wait(bar_o, phase_o);
+            if (tile0 < tile1) wait_o();
         } else {
             for (int tile = tile0; tile < tile1; ++tile) {
-                wait(bar_s, phase_s);
+                wait_s(tile - tile0);
                 tc_fence_after();
                 const uint32_t t_s = tmem + kColS + ((tile - tile0) & 1) * kKeys + lanes;
                 uint32_t sr[kKeys];
@@ -442,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
                     l += (sum[0] + sum[1]) * __fdividef(1.f, wv);
                 }
                 if (tile > tile0) {  // O += P V of the tile before is done
-                    wait(bar_o, phase_o);
+                    wait_o();
                     tc_fence_after();
                     if (__any_sync(0xffffffffu, fix_o != 1.f)) {
 #pragma unroll
@@ -462,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
                 tc_fence_before();
                 named_bar_arrive(kBarP, kThreads);
             }
-            if (tile0 < tile1) wait(bar_o, phase_o);
+            if (tile0 < tile1) wait_o();
             tc_fence_after();
         }
 

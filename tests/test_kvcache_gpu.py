@@ -81,6 +81,27 @@ def test_several_tokens(hq, hkv, d, page):
     check_attention(rng, len(lens), hq, hkv, d, page, lens, counts, "bf16")
 
 
+@pytest.mark.parametrize("d,page", [(128, 64), (64, 16)])
+def test_many_tokens_equal_single_tokens(d, page):
+    # the kernel for many tokens against the one for single tokens, which the tests above hold to
+    # 64 bits: several items and hundreds of tiles for every block
+    rng = np.random.default_rng(d)
+    rows, n, hq, hkv = 16, 24, 32, 4
+    lens = rng.integers(n, 3000, rows)
+    cache = gpu_cache(*make_cache(rng, rows, hkv, page, d, lens))
+    ln = torch.as_tensor(lens).to(torch.int32).cuda()
+    g = torch.Generator(device="cuda").manual_seed(d)
+    K.kda_get_device_status()
+    for _ in range(5):
+        q = torch.randn(rows, n, hq, d, generator=g, device="cuda").to(torch.bfloat16)
+        many = K.kda_kvcache_attention(q.view(rows * n, hq, d), *cache, ln, cu_tokens=cu_of([n] * rows)).view(rows, n, hq, d)
+        for i in range(n):
+            one = K.kda_kvcache_attention(q[:, i], *cache, ln - n + i + 1)
+            # both round to bf16 once (2^-8 between neighbours) and their weights to fp16
+            assert ((many[:, i].float() - one.float()).abs() <= 2.0 ** -7 * one.float().abs() + 2.0 ** -9).all()
+    assert K.kda_get_device_status() == 0
+
+
 def test_one_long_row_is_split():
     rng = np.random.default_rng(3)
     check_attention(rng, 2, 8, 1, 128, 64, [20000, 1], [1, 1], "fp16", cu=False)
