@@ -22,6 +22,7 @@
 #include "../../include/kda.h"
 #include "kda_host.cuh"
 #include "kda_internal.cuh"
+#include "kda_serving.cuh"
 
 using namespace kda::host;
 
@@ -1182,7 +1183,7 @@ kda_status kda_decode_paged(const kda_shape* shape, const uint16_t* q, const uin
     DeviceInfo* di = nullptr;
     if ((st = current_device(&dev, &di)) != KDA_OK) return st;
     if (pr.T_total == 0) return KDA_OK;
-    kda::DecodeParams p{};
+    kda::PagedDecodeParams p{};
     p.q = reinterpret_cast<const __nv_bfloat16*>(q);
     p.k = reinterpret_cast<const __nv_bfloat16*>(k);
     p.v = reinterpret_cast<const __nv_bfloat16*>(v);
@@ -1201,7 +1202,7 @@ kda_status kda_decode_paged(const kda_shape* shape, const uint16_t* q, const uin
     p.num_pages = pages;
     p.page_stride = page_stride;
     p.status = di->status;
-    const cudaError_t e = kda::launch_decode(p, (cudaStream_t)stream);
+    const cudaError_t e = kda::launch_decode_paged(p, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "paged decode kernel launch");
     return KDA_OK;
 }

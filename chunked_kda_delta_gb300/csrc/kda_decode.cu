@@ -16,6 +16,8 @@
 // state row is 512 contiguous bytes and the state sits in 64 registers per thread; two
 // CTAs per SM keep 128 KiB of loads in flight.  The reductions over key rows finish in
 // shared memory across the warps.  bf16 state: its own kernel below.
+#include <type_traits>
+
 #include "kda_internal.cuh"
 #include "kda_serving.cuh"
 
@@ -34,7 +36,7 @@ __device__ __forceinline__ void state_store(float* p, const float (&x)[4]) {
 }
 // Element offset of head hs of sequence n's states in a pool; false for an idle sequence,
 // whose output rows become zero.
-__device__ __forceinline__ bool paged_state(const DecodeParams& p, int64_t n, int hs, size_t& off) {
+__device__ __forceinline__ bool paged_state(const PagedDecodeParams& p, int64_t n, int hs, size_t& off) {
     const int32_t page = p.state_pages[n];
     if (page >= 0 && page < p.num_pages) {
         off = (size_t)page * p.page_stride + (size_t)hs * kD * kD;
@@ -43,16 +45,19 @@ __device__ __forceinline__ bool paged_state(const DecodeParams& p, int64_t n, in
     if (page >= 0 && threadIdx.x == 0) report(p.status, kStatusBadIndex);
     return false;
 }
-__device__ __forceinline__ void idle_output(const DecodeParams& p, int64_t n, int ho, int Ho) {
+__device__ __forceinline__ void idle_output(const PagedDecodeParams& p, int64_t n, int ho, int Ho) {
     if (threadIdx.x >= kD) return;
     for (int64_t t = 0; t < p.T; ++t)
         p.out[(((size_t)n * p.T + t) * Ho + ho) * kD + threadIdx.x] = __float2bfloat16_rn(0.f);
 }
 
+template <bool kPaged>
+using DecodeArgs = std::conditional_t<kPaged, PagedDecodeParams, DecodeParams>;
+
 // kPaged: states in a pool, updated in place.  kGrouped: unequal head counts (HeadMap); the equal-count instance keeps plain head
 // indexing (the map's arithmetic costs the bf16 kernel spills at its register cap).
 template <bool kGrouped, bool kPaged>
-__global__ void __launch_bounds__(kDecThreads, 2) kda_decode_kernel(const DecodeParams p) {
+__global__ void __launch_bounds__(kDecThreads, 2) kda_decode_kernel(const DecodeArgs<kPaged> p) {
     __shared__ float s_k[kD], s_q[kD], s_e[kD], s_v[kD], s_d[kD];
     __shared__ __align__(16) float s_red[2][kDecThreads / 32][kD];
     __shared__ float s_qk[kDecThreads / 32];
@@ -65,7 +70,9 @@ __global__ void __launch_bounds__(kDecThreads, 2) kda_decode_kernel(const Decode
     const HeadMap hm = kGrouped ? head_map(ho, p.H, Hq) : HeadMap{ho, ho, ho, true};
     const int r0 = warp * kDecRows, c0 = lane * 4;
     size_t soff = ((size_t)n * p.H + hm.hs) * kD * kD;
-    if (kPaged && !paged_state(p, n, hm.hs, soff)) return idle_output(p, n, ho, Ho);
+    if constexpr (kPaged) {
+        if (!paged_state(p, n, hm.hs, soff)) return idle_output(p, n, ho, Ho);
+    }
     soff += (size_t)r0 * kD + c0;
 
     float s[kDecRows][4];
@@ -175,7 +182,7 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 }
 
 template <bool kGrouped, bool kPaged>
-__global__ void __launch_bounds__(kDecB16Threads, 3) kda_decode_bf16_kernel(const DecodeParams p) {
+__global__ void __launch_bounds__(kDecB16Threads, 3) kda_decode_bf16_kernel(const DecodeArgs<kPaged> p) {
     __shared__ float s_k[kD], s_q[kD], s_e[kD], s_v[kD];
     __shared__ __align__(16) float s_d[kD];
     __shared__ __align__(16) float s_red[2][kDecB16Threads / 32][kD];
@@ -190,7 +197,9 @@ __global__ void __launch_bounds__(kDecB16Threads, 3) kda_decode_bf16_kernel(cons
     const HeadMap hm = kGrouped ? head_map(ho, p.H, Hq) : HeadMap{ho, ho, ho, true};
     const int rbase = warp * 32 + hw;  // this thread's rows: rbase + 2 i
     size_t soff = ((size_t)n * p.H + hm.hs) * kD * kD;
-    if (kPaged && !paged_state(p, n, hm.hs, soff)) return idle_output(p, n, ho, Ho);
+    if constexpr (kPaged) {
+        if (!paged_state(p, n, hm.hs, soff)) return idle_output(p, n, ho, Ho);
+    }
     soff += (size_t)rbase * kD + c0;
 
     uint4 s[kDecB16Rows];
@@ -301,28 +310,26 @@ __global__ void __launch_bounds__(kDecB16Threads, 3) kda_decode_bf16_kernel(cons
 namespace {
 
 template <bool kGrouped, bool kPaged>
-void launch_decode_one(const DecodeParams& p, dim3 grid, cudaStream_t stream) {
+void launch_decode_one(const DecodeArgs<kPaged>& p, dim3 grid, cudaStream_t stream) {
     if (p.state_bf16)
         kda_decode_bf16_kernel<kGrouped, kPaged><<<grid, dim3(kDecB16Threads), 0, stream>>>(p);
     else
         kda_decode_kernel<kGrouped, kPaged><<<grid, dim3(kDecThreads), 0, stream>>>(p);
 }
 
-}  // namespace
-
-cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream) {
+template <bool kPaged>
+cudaError_t launch_decode_any(const DecodeArgs<kPaged>& p, cudaStream_t stream) {
     const int64_t rows = (int64_t)p.N * (p.Hq > p.H ? p.Hq : p.H);
     if (rows == 0) return cudaSuccess;
     const dim3 grid((unsigned)rows);
-    const bool grouped = p.Hq != p.H;
-    if (p.state_pages) {
-        if (grouped) launch_decode_one<true, true>(p, grid, stream);
-        else launch_decode_one<false, true>(p, grid, stream);
-    } else {
-        if (grouped) launch_decode_one<true, false>(p, grid, stream);
-        else launch_decode_one<false, false>(p, grid, stream);
-    }
+    if (p.Hq != p.H) launch_decode_one<true, kPaged>(p, grid, stream);
+    else launch_decode_one<false, kPaged>(p, grid, stream);
     return cudaGetLastError();
 }
+
+}  // namespace
+
+cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream) { return launch_decode_any<false>(p, stream); }
+cudaError_t launch_decode_paged(const PagedDecodeParams& p, cudaStream_t stream) { return launch_decode_any<true>(p, stream); }
 
 }  // namespace kda

@@ -69,12 +69,6 @@ struct DecodeParams {
     int32_t Hq;               // heads of q; see HeadMap
     float scale;
     int32_t state_bf16;       // 1: states are bf16, else fp32
-    // Paged states (state_pages set): s0 == sfin is a pool, sequence n's states are at element
-    // state_pages[n] * page_stride; negative pages are idle sequences.
-    const int32_t* state_pages;
-    int32_t num_pages;
-    int64_t page_stride;
-    int32_t* status;
 };
 
 // Grouped heads.  H state heads (v, g, beta, states), Hq query heads, min(Hq, H) key

@@ -16,6 +16,17 @@ constexpr int32_t kStatusNonfinite = 9;
 // Records the first condition since the last read.
 __device__ __forceinline__ void report(int32_t* status, int32_t code) { atomicCAS(status, kStatusOk, code); }
 
+// ---- recurrent step on pages ------------------------------------------------------------
+// s0 == sfin is a pool: sequence n's states are at element state_pages[n] * page_stride;
+// negative pages are idle sequences.
+struct PagedDecodeParams : DecodeParams {
+    const int32_t* state_pages;
+    int32_t num_pages;
+    int64_t page_stride;
+    int32_t* status;
+};
+cudaError_t launch_decode_paged(const PagedDecodeParams& p, cudaStream_t stream);
+
 // ---- pages ----------------------------------------------------------------------------
 constexpr int kMaxPools = 64;
 
