@@ -267,77 +267,97 @@ __global__ void __launch_bounds__(kPlanThreads, 1) page_plan_kernel(const __grid
     if (!kGlobal) ptx::cluster_sync();  // shared memory stays until all have read it
 }
 
+// Exclusive prefix of a thread's value over the CTA; total in `total`.  s: 33 ints.
+__device__ __forceinline__ int block_prefix(int value, int* s, int& total) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int x = value;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) s[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        const int c = s[lane];
+        int y = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int z = __shfl_up_sync(0xffffffffu, y, o);
+            if (lane >= o) y += z;
+        }
+        s[lane] = y - c;
+        if (lane == 31) s[32] = y;
+    }
+    __syncthreads();
+    total = s[32];
+    return s[warp] + x - value;
+}
+
+// With n pages in use and r(x) of them below page x: a free page x < n is hole number x - r(x), a
+// page x >= n in use is mover number r(x) - r(n), and mover m goes to hole m.  One prefix sum, over
+// the runs of pages that the threads hold, gives all ranks.
 template <bool kGlobal>
 __global__ void __launch_bounds__(kPlanThreads, 1) page_compact_kernel(const __grid_constant__ PagePlan p, int shift) {
     extern __shared__ int32_t s_pages[];
-    __shared__ int s[33];
-    __shared__ Counts live_counts, counts;
+    __shared__ int s[33], s_below;  // r(n)
+    __shared__ Counts counts;
     cudaTriggerProgrammaticLaunchCompletion();
-    const int cta = blockIdx.x, ctas = gridDim.x, tid = threadIdx.x;
+    const int cta = blockIdx.x, ctas = gridDim.x, tid = threadIdx.x, mask = (1 << shift) - 1;
     const int entries = p.rows * p.width;
-    // The new number of each page; of a page that moves, -2 - its rank among those until the
-    // free pages are listed.
-    const PageArray<kGlobal> map{kGlobal ? p.page_map : s_pages, shift};
-    int32_t* holes_list = s_pages + (1 << shift);
+    const PageArray<kGlobal> map{kGlobal ? p.page_map : s_pages, shift}, holes{kGlobal ? p.list : s_pages + (1 << shift), shift};
+    int32_t* refs_here = s_pages + (2 << shift);
     int lo, hi;
     if (kGlobal) {
         share(p.pages, cta, ctas, lo, hi);
     } else {
         lo = min(p.pages, cta << shift);
         hi = min(p.pages, (cta + 1) << shift);
+        for (int x = lo + tid; x < hi; x += kPlanThreads) refs_here[x & mask] = p.refs[x];
+        __syncthreads();
     }
-    auto live = [&](int x) { return p.refs[x] > 0; };
-
-    int n = 0;
-    for (int b = lo; b < hi; b += kPlanThreads) n += __syncthreads_count(b + tid < hi && live(b + tid));
+    auto refs_of = [&](int x) { return kGlobal ? p.refs[x] : refs_here[x & mask]; };
+    const int run = (hi - lo + kPlanThreads - 1) / kPlanThreads;
+    const int x0 = min(hi, lo + tid * run), x1 = min(hi, x0 + run);
+    int mine = 0, total, n;
+    for (int x = x0; x < x1; ++x) mine += refs_of(x) > 0;
+    mine = block_prefix(mine, s, total);
     plan_sync<kGlobal>();  // every CTA runs: shared memory may be written
-    tell(live_counts, 0, n, cta, ctas);
+    tell(counts, 0, total, cta, ctas);
     plan_sync<kGlobal>();
-    before(live_counts, 0, cta, ctas, n);
-
-    // Free pages below n (holes) and pages in use from n on (movers) are equally many.
-    int holes = 0, movers = 0;
-    for (int b = lo; b < hi; b += kPlanThreads) {
-        const int x = b + tid;
-        holes += __syncthreads_count(x < hi && x < n && !live(x));
-        movers += __syncthreads_count(x < hi && x >= n && live(x));
+    const int r0 = before(counts, 0, cta, ctas, n) + mine;
+    int r = r0;
+    for (int x = x0; x < x1; ++x) {
+        if (x == n)
+            for (int c = 0; c < ctas; ++c) *at_cta(&s_below, c) = r;
+        if (refs_of(x) > 0) ++r;
+        else if (x < n) *holes.at(x - r) = x;
     }
-    tell(counts, 0, holes, cta, ctas);
-    tell(counts, 1, movers, cta, ctas);
+    if (n == p.pages && tid == 0) s_below = n;
     plan_sync<kGlobal>();
-    int moved, same;
-    const int hole_at = before(counts, 0, cta, ctas, moved);
-    int mover_at = before(counts, 1, cta, ctas, same), mine = 0;
-    for (int b = lo; b < hi; b += kPlanThreads) {
-        const int x = b + tid;
-        const bool use = x < hi && live(x), hole = x < hi && x < n && !use, mover = use && x >= n;
-        int total;
-        const int h = mine + block_rank(hole, s, total);
-        if (hole) (kGlobal ? p.list + hole_at : holes_list)[h] = x;
-        mine += total;
-        const int m = mover_at + block_rank(mover, s, total);
-        mover_at += total;
-        if (x < hi) {
-            map.own(x) = mover ? -2 - m : use ? x : -1;
-            if (!hole) p.new_refs[x] = use && !mover ? p.refs[x] : 0;
+    const int below = s_below;
+    r = r0;
+    for (int x = x0; x < x1; ++x) {
+        const int refs = refs_of(x);
+        int to = -1;
+        if (refs > 0) {
+            to = x;
+            if (x >= n) {
+                const int m = r - below;
+                to = holes.get(m);
+                p.src[m] = x;
+                p.dst[m] = to;
+                p.new_refs[to] = refs;
+            }
+            ++r;
         }
+        if (x >= n || refs > 0) p.new_refs[x] = x < n ? refs : 0;
+        if (!kGlobal) map.own(x) = to;
+        p.page_map[x] = to;
     }
     if (cta == 0 && tid == 0) {
-        *p.copies = moved;
+        *p.copies = n - below;
         *p.num_live = n;
-    }
-    plan_sync<kGlobal>();
-    for (int x = lo + tid; x < hi; x += kPlanThreads) {
-        int32_t to = map.own(x);
-        if (to < -1) {
-            const int m = -2 - to;
-            to = kGlobal ? __ldcg(p.list + m) : listed(holes_list, counts, 0, m);
-            p.src[m] = x;
-            p.dst[m] = to;
-            p.new_refs[to] = p.refs[x];
-            map.own(x) = to;
-        }
-        if (!kGlobal) p.page_map[x] = to;
     }
     plan_sync<kGlobal>();
     for (int e = cta * kPlanThreads + tid; e < entries; e += ctas * kPlanThreads) {
@@ -448,7 +468,7 @@ cudaError_t launch_page_plan(const PagePlan& p, int mode, cudaStream_t stream) {
 }
 
 cudaError_t launch_page_compact(const PagePlan& p, cudaStream_t stream) {
-    return launch_plan(page_compact_kernel<false>, page_compact_kernel<true>, 2, p, stream);
+    return launch_plan(page_compact_kernel<false>, page_compact_kernel<true>, 3, p, stream);
 }
 
 cudaError_t launch_page_copy(const PoolSet& pools, int32_t pages, const int32_t* src, const int32_t* dst,
