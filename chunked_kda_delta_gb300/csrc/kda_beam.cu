@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) beam_scan_kernel(const BeamPa
     __shared__ float s_group[kBound];
     __shared__ float4 s_sums[kScanWarps];
     __shared__ uint64_t s_key[kBuffer], s_red[kScanWarps];
-    __shared__ int s_keys;
+    __shared__ int s_keys, s_found, s_step[kBuffer];
     cudaTriggerProgrammaticLaunchCompletion();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t row = blockIdx.x / p.segs;
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) beam_scan_kernel(const BeamPa
 
     Sums s{kNegInf, 0.f, kNegInf, 0.f};
     float group = kNegInf;
-    if (tid == 0) s_keys = 0;
+    if (tid == 0) s_keys = s_found = 0;
 
     uint4 next[kLoads];
     auto load = [&](int at) {
@@ -324,16 +324,18 @@ __global__ void __launch_bounds__(kScanThreads, 4) beam_scan_kernel(const BeamPa
         const unsigned who = __ballot_sync(0xffffffffu, larger == c1 - 1);
         if (who) bound = __shfl_sync(0xffffffffu, g, __ffs(who) - 1);
     }
-    // The values of this lane that reach the bound.
+    // The values of this lane that reach the bound (where there are too many for the buffers).
     auto each = [&](auto f) {
         if (mine < bound || mine == kNegInf) return;
         for (int t = 0; t < steps; ++t) {
             if (s_most[t][tid] < bound) continue;
             const int at = first + t * kTurn + lane * kVec;
-#pragma unroll 1
+            uint4 u[kLoads];
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) u[i] = load16(x, at + i * 32 * kVec, p.vocab);
+#pragma unroll
             for (int i = 0; i < kLoads; ++i) {
-                const uint4 u = load16(x, at + i * 32 * kVec, p.vocab);
-                const uint32_t q[4] = {u.x, u.y, u.z, u.w};
+                const uint32_t q[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     float v[kPer];
@@ -346,14 +348,37 @@ __global__ void __launch_bounds__(kScanThreads, 4) beam_scan_kernel(const BeamPa
             }
         }
     };
-    each([&](uint64_t k) {
-        const int place = atomicAdd(&s_keys, 1);
-        if (place < kBuffer) s_key[place] = k;
-    });
+    // The steps that hold them are shared out to all threads, four to a step: a warp that held
+    // several would read them one after the other (5 us at the end of 32 x 8 rows of 131072).
+    if (mine >= bound && mine > kNegInf)
+        for (int t = 0; t < steps; ++t)
+            if (s_most[t][tid] >= bound && s_most[t][tid] > kNegInf) {
+                const int place = atomicAdd(&s_found, 1);
+                if (place < kBuffer) s_step[place] = t << 8 | tid;
+            }
+    __syncthreads();
+    const int found = s_found;
+    for (int i = tid / kLoads; i < min(found, kBuffer); i += kScanThreads / kLoads) {
+        const int t = s_step[i] >> 8, who = s_step[i] & 255;
+        const int at = begin + (who >> 5) * kStep + t * kTurn + ((tid % kLoads) * 32 + (who & 31)) * kVec;
+        const uint4 u = load16(x, at, p.vocab);
+        const uint32_t q[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float v[kPer];
+            Logit<T>::unpack(q[j], v);
+#pragma unroll
+            for (int e = 0; e < kPer; ++e)
+                if (v[e] >= bound && fabsf(v[e]) < INFINITY) {
+                    const int place = atomicAdd(&s_keys, 1);
+                    if (place < kBuffer) s_key[place] = key_of(v[e], (uint32_t)(at + j * kPer + e));
+                }
+        }
+    }
     __syncthreads();
     uint64_t* cand = p.cand + (int64_t)blockIdx.x * c1;
     const int n = s_keys;
-    if (n <= kBuffer) {
+    if (found <= kBuffer && n <= kBuffer) {
         for (int i = tid; i < n; i += kScanThreads) {
             const uint64_t k = s_key[i];
             int larger = 0;
