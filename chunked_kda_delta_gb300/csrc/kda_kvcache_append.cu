@@ -105,65 +105,93 @@ __device__ __forceinline__ uint2 encode_short(const float (&x)[8], float s, floa
     for (int i = 0; i < 4; ++i) c[i] = code2(short_quotient(x[2 * i], s, r), short_quotient(x[2 * i + 1], s, r));
     return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
-// Eight older codes of scale `was` rounded again for scale `now`.
-__device__ __forceinline__ uint2 again(uint2 w, float was, float now) {
-    const uint32_t u[4] = {w.x & 0xffffu, w.x >> 16, w.y & 0xffffu, w.y >> 16};
-    uint32_t c[4];
+// Rounds `bytes` older codes (a multiple of 16) of scale `was` again for the larger scale s; by
+// kThreads threads, four 16-byte loads of each in flight.
+template <int kThreads>
+__device__ __forceinline__ void grade_again(uint8_t* codes, int bytes, float was, float s, int tid) {
+    const bool quick = short_division(s);
+    const float r = __frcp_rn(s);
+    auto again = [&](uint32_t two) {
+        const float2 f = values2(two);
+        const float a = __fmul_rn(f.x, was), b = __fmul_rn(f.y, was);
+        return quick ? code2(short_quotient(a, s, r), short_quotient(b, s, r)) : code2(quotient(a, s), quotient(b, s));
+    };
+    for (int at = tid * 16; at < bytes; at += kThreads * 64) {
+        uint4 w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = values2(u[i]);
-        c[i] = code2(quotient(__fmul_rn(f.x, was), now), quotient(__fmul_rn(f.y, was), now));
+        for (int i = 0; i < 4; ++i)
+            if (at + i * kThreads * 16 < bytes) w[i] = *reinterpret_cast<const uint4*>(codes + at + i * kThreads * 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (at + i * kThreads * 16 >= bytes) continue;
+            uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) u[k] = again(u[k] & 0xffffu) | again(u[k] >> 16) << 16;
+            *reinterpret_cast<uint4*>(codes + at + i * kThreads * 16) = make_uint4(u[0], u[1], u[2], u[3]);
+        }
     }
-    return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
 
-// One token a row (the decode step): a warp per (row, head, k or v).
+// One token a row (the decode step): a warp per (row, head, k or v).  An open page whose scale
+// grows has its older codes rounded again by the whole block (by its warp alone the step took
+// 40 us where half of 256 x 8 pages grew, now 10; 6 where 7% grow, 4 where none does).
 constexpr int kStepWarps = 4;
 
 template <typename T, int kDim>
 __global__ void __launch_bounds__(kStepWarps * 32) append_step_kernel(const __grid_constant__ AppendParams p) {
     const CacheParams& c = p.c;
-    const int lane = threadIdx.x & 31;
-    const int64_t w = (int64_t)blockIdx.x * kStepWarps + (threadIdx.x >> 5);
-    if (w >= 2 * c.tokens * c.heads) return;
-    const int which = (int)(w & 1), head = (int)((w >> 1) % c.heads);
-    const int64_t row = (w >> 1) / c.heads;
-    const int32_t len = c.lens[row];
-    const int64_t slot = len < 0 ? c.width : len / c.page_tokens;
-    const int32_t page = slot < c.width ? c.tables[row * c.width + slot] : -1;
-    if (page < 0 || page >= c.pages) {
-        if (lane == 0) report(c.status, kStatusBadIndex);
-        return;
-    }
-    constexpr int kLanes = kDim / 8;
-    const bool mine = lane < kLanes;
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    const T* src = static_cast<const T*>(p.x[which]) + row * p.stride[which] + (int64_t)head * kDim;
-    uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-    if (mine) raw = reinterpret_cast<const uint4*>(src)[lane];
-    unpack<T>(raw, x);
-    if (!(top_of<T>(largest2<T>(raw)) < INFINITY)) report(c.status, kStatusNonfinite);
-    float a = largest(x);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-
-    const int off = len % c.page_tokens;
-    const int64_t block = (int64_t)page * c.heads + head;
-    float* scale = (which ? c.v_scale : c.k_scale) + block;
-    uint8_t* codes = (which ? c.v_codes : c.k_codes) + block * c.page_tokens * kDim;
-    float s = __fdiv_rn(a, kCodeMax);
-    if (off > 0) {
-        const float was = *scale;
-        if (s > was) {
-            uint2* old = reinterpret_cast<uint2*>(codes);
-            for (int i = lane; i < off * kLanes; i += 32) old[i] = again(old[i], was, s);
+    struct Growth {
+        uint8_t* codes;
+        int bytes;  // 0: none
+        float was, now;
+    };
+    __shared__ Growth s_growth[kStepWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t w = (int64_t)blockIdx.x * kStepWarps + warp;
+    Growth growth{nullptr, 0, 0.f, 0.f};
+    if (w < 2 * c.tokens * c.heads) {
+        const int which = (int)(w & 1), head = (int)((w >> 1) % c.heads);
+        const int64_t row = (w >> 1) / c.heads;
+        const int32_t len = c.lens[row];
+        const int64_t slot = len < 0 ? c.width : len / c.page_tokens;
+        const int32_t page = slot < c.width ? c.tables[row * c.width + slot] : -1;
+        if (page < 0 || page >= c.pages) {
+            if (lane == 0) report(c.status, kStatusBadIndex);
         } else {
-            s = was;
+            constexpr int kLanes = kDim / 8;
+            const bool mine = lane < kLanes;
+            float x[8];
+            const T* src = static_cast<const T*>(p.x[which]) + row * p.stride[which] + (int64_t)head * kDim;
+            uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+            if (mine) raw = reinterpret_cast<const uint4*>(src)[lane];
+            unpack<T>(raw, x);
+            if (!(top_of<T>(largest2<T>(raw)) < INFINITY)) report(c.status, kStatusNonfinite);
+            float a = largest(x);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+
+            const int off = len % c.page_tokens;
+            const int64_t block = (int64_t)page * c.heads + head;
+            float* scale = (which ? c.v_scale : c.k_scale) + block;
+            uint8_t* codes = (which ? c.v_codes : c.k_codes) + block * c.page_tokens * kDim;
+            float s = __fdiv_rn(a, kCodeMax);
+            if (off > 0) {
+                const float was = *scale;
+                if (s > was) growth = Growth{codes, off * kDim, was, s};
+                else s = was;
+                __syncwarp();  // every lane has read the scale
+            }
+            if (lane == 0) *scale = s;
+            if (mine) reinterpret_cast<uint2*>(codes + (int64_t)off * kDim)[lane] = encode(x, s);
         }
-        __syncwarp();  // every lane has read the scale
     }
-    if (lane == 0) *scale = s;
-    if (mine) reinterpret_cast<uint2*>(codes + (int64_t)off * kDim)[lane] = encode(x, s);
+    if (lane == 0) s_growth[warp] = growth;
+    if (!__syncthreads_or(growth.bytes)) return;
+#pragma unroll 1
+    for (int i = 0; i < kStepWarps; ++i) {
+        const Growth g = s_growth[i];
+        if (g.bytes) grade_again<kStepWarps * 32>(g.codes, g.bytes, g.was, g.now, threadIdx.x);
+    }
 }
 
 // Several tokens a row: a block of 128 threads per (touched page, head, k or v).  Row r's i-th
@@ -172,7 +200,7 @@ __global__ void __launch_bounds__(kStepWarps * 32) append_step_kernel(const __gr
 constexpr int kAppendThreads = 128;
 
 template <typename T, int kDim, int kPage>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, kDim * kPage <= 8192 ? 8 : 4) append_kernel(const __grid_constant__ AppendParams p) {
     const CacheParams& c = p.c;
     __shared__ float red[kAppendThreads / 32];
     constexpr int kLanes = kDim / 8, kRows = kAppendThreads / kLanes;  // tokens a pass
@@ -252,14 +280,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
 #pragma unroll
     for (int w = 0; w < kAppendThreads / 32; ++w) a = fmaxf(a, red[w]);
     float s = __fdiv_rn(a, kCodeMax);
-    if (off > 0) {
-        if (s > was) {
-            uint2* old = reinterpret_cast<uint2*>(codes);
-            for (int j = tid; j < off * kLanes; j += kAppendThreads) old[j] = again(old[j], was, s);
-        } else {
-            s = was;
-        }
-    }
+    const bool grown = off > 0 && s > was;
+    if (off > 0 && !grown) s = was;
     if (tid == 0) *scale = s;
     if (finite && short_division(s)) {
         const float r = __frcp_rn(s);
@@ -279,6 +301,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
             if (t < n) reinterpret_cast<uint2*>(codes + (int64_t)(off + t) * kDim)[at] = encode(x, s);
         }
     }
+    if (grown) grade_again<kAppendThreads>(codes, off * kDim, was, s, tid);  // the registers are free now
 }
 
 template <typename T, int kDim>
