@@ -3,7 +3,9 @@
 Each ``csrc/*.cu`` file is compiled in parallel with
 ``-gencode arch=compute_103a,code=sm_103a`` and linked into one shared
 library against the shared CUDA runtime (so a process that already loaded
-torch's ``libcudart.so.13`` shares a single runtime with it).  Run as
+torch's ``libcudart.so.13`` shares a single runtime with it).  Beside it,
+``csrc/binding/serving_binding.cpp`` becomes ``_build/_kda_serving.so``, the CPython
+extension that marshals torch tensors into the serving operators' ABI.  Run as
 ``python -m chunked_kda_delta_gb300.build``.
 """
 from __future__ import annotations
@@ -16,6 +18,7 @@ import platform
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -24,6 +27,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libkda.so")
 STAMP_PATH = LIB_PATH + ".stamp"
+BINDING_SRC = os.path.join(CSRC, "binding", "serving_binding.cpp")
+BINDING_PATH = os.path.join(BUILD_DIR, "_kda_serving.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -74,7 +79,57 @@ def _up_to_date(stamp: str) -> bool:
         return f.read().strip() == stamp
 
 
+def _binding_command(out: str):
+    import torch
+
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    nvcc = nvcc_path()
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
+    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               cuda, sysconfig.get_paths()["include"]]
+    libs = os.path.join(root, "lib")
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        raise RuntimeError("g++ not found; the serving binding needs a C++ compiler")
+    return [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden"] + \
+        [x for i in include for x in ("-isystem", i)] + [BINDING_SRC, "-o", out, "-L", libs, "-L", BUILD_DIR] + \
+        ["-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python", "-lkda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"]
+
+
+def build_binding(force: bool = False) -> str:
+    """Compile the serving operators' extension against the installed torch; returns its path.
+    Rebuilt when its source, the ABI header, torch, Python or the machine differ."""
+    import torch
+
+    h = hashlib.sha256()
+    for d in (BINDING_SRC, os.path.join(INCLUDE, "kda.h"), os.path.abspath(__file__)):
+        with open(d, "rb") as f:
+            h.update(f.read())
+    h.update(" ".join([torch.__version__, sys.version, platform.machine()]).encode())
+    stamp, path = h.hexdigest(), BINDING_PATH + ".stamp"
+    if not force and os.path.exists(BINDING_PATH) and os.path.exists(path):
+        with open(path) as f:
+            if f.read().strip() == stamp:
+                return BINDING_PATH
+    tmp = BINDING_PATH + f".tmp{os.getpid()}"
+    res = subprocess.run(_binding_command(tmp), capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed for {BINDING_SRC}:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, BINDING_PATH)
+    with open(path, "w") as f:
+        f.write(stamp + "\n")
+    return BINDING_PATH
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
+    """Compile every CUDA source and link ``libkda.so``, then the serving operators'
+    extension on it; returns the library path."""
+    path = build_library(force, verbose, extra_flags)
+    build_binding(force)
+    return path
+
+
+def build_library(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     """Compile every CUDA source and link ``libkda.so``; returns the library path."""
     flags = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                     "--expt-relaxed-constexpr",
