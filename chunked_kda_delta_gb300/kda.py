@@ -536,12 +536,15 @@ def kda_decode_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch
     if scale is None:
         scale = D ** -0.5
     _check_result("out", out, _out_shape(q, v), torch.bfloat16, "cuda")
-    if out is None:
-        out = torch.empty(_out_shape(q, v), dtype=q.dtype, device=q.device)
     if stream is None:
-        stream = torch.cuda.current_stream(q.device).cuda_stream
-    elif isinstance(stream, torch.cuda.Stream):
-        stream = stream.cuda_stream
+        stream = torch.cuda.current_stream(q.device)
+    elif not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), q.device)
+    if out is None:
+        with torch.cuda.stream(stream):  # memory that work of this stream alone may still use
+            out = torch.empty(_out_shape(q, v), dtype=q.dtype, device=q.device)
+        out.record_stream(torch.cuda.current_stream(q.device))
+    stream = stream.cuda_stream
     shape = KdaShape(B, T, 0, H, D, Hq)
     stride = states.stride(0) if states.shape[0] > 1 else H * D * D
     with torch.cuda.device(q.device):
