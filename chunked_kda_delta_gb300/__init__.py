@@ -1,9 +1,10 @@
-"""KDA forward prefill for GB300 (sm_103a): a C-ABI CUDA library and its thin binding.
+"""KDA prefill, decode and serving operators for GB300 (sm_103a): a C-ABI CUDA library and its
+thin binding.
 
 The compute lives in ``csrc/`` (hand-written CUDA for sm_103a) behind the C ABI
 declared in ``include/kda.h``; :mod:`chunked_kda_delta_gb300.kda` marshals torch
-tensors into that ABI through ctypes.  There is no CPU fallback: every entry
-point raises if the compiled library is missing.
+tensors into that ABI through ctypes, :mod:`chunked_kda_delta_gb300.serving` through a compiled
+extension.  There is no CPU fallback: every entry point raises if the compiled code is missing.
 """
 from .kda import (  # noqa: F401
     KdaError,

@@ -11,7 +11,9 @@
 // more than k + 1 of them, and their values that reach it are the candidates.  (Keeping sorted
 // lists while streaming, with a bound that rises, took 12 us more on 256 rows of 131072: some
 // warp always has a value to insert.)  beam_join, one CTA a request, puts the sums together and
-// ranks the candidates.
+// ranks the candidates.  32 x 8 beams of 131072 bf16 logits: 21 us (0.48 of the 67 MB at the copy
+// rate), 15 for the stream alone, with or without the exponentials; 4 beams of 32001: 8 us, the
+// latency of two launches.
 //
 // Candidates are 64-bit keys (value, complement of the index), all different: ranking them
 // by counting larger keys needs no sort and ties go to the lowest index.

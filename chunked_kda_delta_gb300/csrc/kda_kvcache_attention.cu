@@ -27,10 +27,12 @@
 // through all items; every resident warp takes an equal contiguous share, however long the rows
 // are.  An item inside one share is written at once; the parts of the others, in the layout of
 // the product's fragments, are joined by a second launch.  (With four warps sharing each tile
-// and joining in shared memory at every item's end the loads paused there: 141 us instead of
-// 128 for 64 rows of up to 8192 tokens, 8 heads.  Asking L2 for codes two to eight slabs ahead
+// and joining in shared memory at every item's end the loads paused there: 147 us instead of
+// 133 for 64 rows of up to 8192 tokens, 8 heads.  Asking L2 for codes two to eight slabs ahead
 // made it 1 to 35% slower, slabs of 16 keys with four CTAs an SM 5%, two CTAs without spills
-// 10%.)
+// 10%.)  Bound by HBM: that call takes 127 us, 0.83 of its bytes at the copy rate (718 MB), the join
+// and its tail with it; 4 rows of up to 131072 tokens, 4 heads, 71 us, 0.75; one row of 1000
+// tokens 8 us, two launches' latency.
 #include "kda_kvcache_attention.cuh"
 
 namespace kda {
