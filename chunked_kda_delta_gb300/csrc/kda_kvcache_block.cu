@@ -299,11 +299,13 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
             // This warp's 16 keys of each tile lie in one page.  Load number i of a lane: key
             // 8 (i % 2) + lane % 8, channels 16 (4 (i / 2) + lane / 8).
             const int mine = warp - kSoft / 32;
-            auto page_at = [&](int tile) {
+            auto entry_at = [&](int tile) {
                 const int key = tile * kKeys + mine * 16;
-                if (tile >= tile1 || key >= seen_max) return -1;
-                const int32_t x = table[key >> page_shift];
-                if (x >= 0 && x < c.pages) return x;
+                return tile >= tile1 || key >= seen_max ? -1 : table[key >> page_shift];
+            };
+            // (Looked at a tile after it was read: the wait for the table would hold up the loop.)
+            auto checked = [&](int32_t x) {
+                if (x < c.pages) return x;
                 if (lane == 0) report(c.status, kStatusBadIndex);
                 return -1;
             };
@@ -347,14 +349,15 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
             };
 
             // Pages, scales and codes are read a tile or two ahead.
-            int32_t page1 = page_at(tile0 + 1), page2 = page_at(tile0 + 2);
+            int32_t page0 = entry_at(tile0), page1 = entry_at(tile0 + 1), page2 = entry_at(tile0 + 2);
+            page0 = checked(page0);
+            page1 = checked(page1);
             Meta meta1 = meta_of(page1);  // of tile + 1
             uint4 kr[kLoads], vr[kLoads];
             if (tile0 < tile1) {
-                const int32_t page = page_at(tile0);
-                const Meta meta = meta_of(page);
-                load(kr, c.k_codes, tile0, page, 16);
-                load(vr, c.v_codes, tile0, page, meta.v > 0.f ? seen_max - tile0 * kKeys - mine * 16 : 0);
+                const Meta meta = meta_of(page0);
+                load(kr, c.k_codes, tile0, page0, 16);
+                load(vr, c.v_codes, tile0, page0, meta.v > 0.f ? seen_max - tile0 * kKeys - mine * 16 : 0);
                 put_k(kr, tile0, meta);
                 load(kr, c.k_codes, tile0 + 1, page1, 16);
             }
@@ -373,6 +376,7 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
                     tc_fence_after();
                     issue_s(tile + 1);
                 }
+                page2 = checked(page2);
                 load(kr, c.k_codes, tile + 2, page2, 16);
 #pragma unroll
                 for (int i = 0; i < kLoads; ++i) {
@@ -386,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
                 load(vr, c.v_codes, tile + 1, page1, meta1.v > 0.f ? seen_max - (tile + 1) * kKeys - mine * 16 : 0);
                 page1 = page2;
                 meta1 = meta_of(page1);
-                page2 = page_at(tile + 3);
+                page2 = entry_at(tile + 3);
                 if (issuer) {
                     named_bar_sync(kBarP, kThreads);
                     tc_fence_after();
