@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kScanThreads, 4) beam_scan_kernel(const BeamPa
     __shared__ float4 s_sums[kScanWarps];
     __shared__ uint64_t s_key[kBuffer], s_red[kScanWarps];
     __shared__ int s_keys, s_found, s_step[kBuffer];
-    cudaTriggerProgrammaticLaunchCompletion();
+    follow_stream();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int64_t row = blockIdx.x / p.segs;
     if (p.done && p.done[row]) return;  // beam_join takes its one candidate from the scores
@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamParam
         score[w] = p.scores[row0 + w];
         done[w] = p.done && p.done[row0 + w];
     }
-    cudaGridDependencySynchronize();
+    follow_stream();
     uint64_t keep[kKeep];
     const bool kept = keys <= kKeep * kJoinThreads;
 #pragma unroll
@@ -632,22 +632,9 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamParam
 template <typename T>
 cudaError_t launch_type(const BeamParams& p, cudaStream_t stream) {
     const dim3 grid((unsigned)((int64_t)p.batch * p.beams * p.segs));
-    if (p.k < 32)
-        beam_scan_kernel<T, 32><<<grid, kScanThreads, 0, stream>>>(p);
-    else
-        beam_scan_kernel<T, 128><<<grid, kScanThreads, 0, stream>>>(p);
-    cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_early(p.k < 32 ? beam_scan_kernel<T, 32> : beam_scan_kernel<T, 128>, grid, kScanThreads, 0, stream, 1, p);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.batch);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, beam_join_kernel<T>, p);
+    return launch_early(beam_join_kernel<T>, dim3(p.batch), kJoinThreads, 0, stream, 1, p);
 }
 
 }  // namespace

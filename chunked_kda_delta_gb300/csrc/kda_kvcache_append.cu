@@ -141,6 +141,7 @@ constexpr int kStepWarps = 4;
 
 template <typename T, int kDim>
 __global__ void __launch_bounds__(kStepWarps * 32) append_step_kernel(const __grid_constant__ AppendParams p) {
+    follow_stream();
     const CacheParams& c = p.c;
     struct Growth {
         uint8_t* codes;
@@ -203,6 +204,7 @@ constexpr int kAppendThreads = 128;
 
 template <typename T, int kDim, int kPage>
 __global__ void __launch_bounds__(kAppendThreads, kDim * kPage <= 8192 ? 8 : 4) append_kernel(const __grid_constant__ AppendParams p) {
+    follow_stream();
     const CacheParams& c = p.c;
     __shared__ float red[kAppendThreads / 32];
     constexpr int kLanes = kDim / 8, kRows = kAppendThreads / kLanes;  // tokens a pass
@@ -311,17 +313,14 @@ cudaError_t launch_dim(const AppendParams& p, cudaStream_t stream) {
     const CacheParams& c = p.c;
     if (!c.cu) {
         const int64_t warps = 2 * c.tokens * c.heads;
-        append_step_kernel<T, kDim><<<(unsigned)((warps + kStepWarps - 1) / kStepWarps), kStepWarps * 32, 0, stream>>>(p);
-        return cudaGetLastError();
+        return launch_early(append_step_kernel<T, kDim>, dim3((unsigned)((warps + kStepWarps - 1) / kStepWarps)), kStepWarps * 32, 0, stream, 1, p);
     }
     const dim3 grid((unsigned)(c.tokens / c.page_tokens + 2ll * c.rows), 2 * c.heads);
-    switch (c.page_tokens) {
-        case 16: append_kernel<T, kDim, 16><<<grid, kAppendThreads, 0, stream>>>(p); break;
-        case 32: append_kernel<T, kDim, 32><<<grid, kAppendThreads, 0, stream>>>(p); break;
-        case 64: append_kernel<T, kDim, 64><<<grid, kAppendThreads, 0, stream>>>(p); break;
-        default: append_kernel<T, kDim, 128><<<grid, kAppendThreads, 0, stream>>>(p); break;
-    }
-    return cudaGetLastError();
+    const auto kernel = c.page_tokens == 16   ? append_kernel<T, kDim, 16>
+                        : c.page_tokens == 32 ? append_kernel<T, kDim, 32>
+                        : c.page_tokens == 64 ? append_kernel<T, kDim, 64>
+                                              : append_kernel<T, kDim, 128>;
+    return launch_early(kernel, grid, kAppendThreads, 0, stream, 1, p);
 }
 
 }  // namespace

@@ -85,6 +85,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(c
     constexpr int kVWords = kDim / 32;   // 4-byte words of a V load
     __shared__ int64_t s_first[kMaxListed + 1], s_scan[kWarps];
 
+    follow_stream();
     const CacheParams& c = p.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int group = p.q_heads / c.heads;
@@ -102,7 +103,6 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(c
     __syncthreads();
     if (blockIdx.x == 0 && c.rows <= kMaxListed)
         for (int r = tid; r <= c.rows; r += kThreads) p.first_work[r] = s_first[r];
-    cudaTriggerProgrammaticLaunchCompletion();
     const int64_t all = first[c.rows];
     const int64_t per = share_of(all, p.ctas * kWarps);
     const int64_t unit = (int64_t)blockIdx.x * kWarps + warp;
@@ -408,11 +408,12 @@ __global__ void __launch_bounds__(kSplit ? kJoinSplit * 32 : kDim * 2) attention
     const int group = p.q_heads / c.heads;
     int64_t i = blockIdx.x;
     int row;
-    if (!joined_item(c, group, kCols, i, row)) return;
-    int64_t begin;
-    const int n = row_tokens(c, row, begin);
-    const int slabs = row_slabs(row_length(c, row));
-    cudaGridDependencySynchronize();
+    const bool there = joined_item(c, group, kCols, i, row);
+    int64_t begin = 0;
+    const int n = there ? row_tokens(c, row, begin) : 0;
+    const int slabs = there ? row_slabs(row_length(c, row)) : 0;
+    follow_stream();
+    if (!there) return;
     const int64_t all = p.first_work[c.rows], w_row = p.first_work[row], w_next = p.first_work[row + 1];
     const int64_t per = share_of(all, p.ctas * kWarps);
     const int64_t w0 = w_row + i * slabs, w1 = w0 + slabs;
@@ -471,24 +472,14 @@ template <typename T, int kDim, int kNT>
 cudaError_t launch_one(const AttentionParams& p, cudaStream_t stream) {
     const CacheParams& c = p.c;
     constexpr int kCols = 8 * kNT;
-    attention_kernel<T, kDim, kNT><<<p.ctas, kThreads, 0, stream>>>(p);
-    cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_early(attention_kernel<T, kDim, kNT>, dim3(p.ctas), kThreads, 0, stream, 1, p);
     if (e != cudaSuccess) return e;
     const int64_t group = p.q_heads / c.heads;
     const int64_t items = joined_items(c, group, kCols);
     // Fewer items than SMs leave SMs idle and have many parts each.
     const bool split = items * kNT < p.sm_count;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)items, kNT, split ? kDim / 16 : 1);
-    cfg.blockDim = dim3(split ? kJoinSplit * 32 : kDim * 2);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (split) return cudaLaunchKernelEx(&cfg, attention_join_kernel<T, kDim, kNT, true>, p);
-    return cudaLaunchKernelEx(&cfg, attention_join_kernel<T, kDim, kNT, false>, p);
+    return launch_early(split ? attention_join_kernel<T, kDim, kNT, true> : attention_join_kernel<T, kDim, kNT, false>,
+                        dim3((unsigned)items, kNT, split ? kDim / 16 : 1), split ? kJoinSplit * 32 : kDim * 2, 0, stream, 1, p);
 }
 
 // CTAs an SM holds; the same on every device the library runs on.

@@ -161,6 +161,7 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
         tmem_alloc(smem_u32(&s_tmem), kColumns);
         tmem_relinquish();
     }
+    follow_stream();
     int64_t* first = c.rows <= kMaxListed ? s_first : p.first_work;
     for (int r = warp; r < c.rows; r += kThreads / 32) {
         int64_t begin;
@@ -175,7 +176,6 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
     tc_fence_after();
     if (blockIdx.x == 0 && c.rows <= kMaxListed)
         for (int r = tid; r <= c.rows; r += kThreads) p.first_work[r] = s_first[r];
-    cudaTriggerProgrammaticLaunchCompletion();
     const uint32_t tmem = s_tmem, lanes = (uint32_t)(32 * (warp % 4)) << 16;
     const int64_t per = share_of(first[c.rows], p.ctas);
     const int64_t w_begin = per * blockIdx.x, w_end = min(first[c.rows], w_begin + per);
@@ -550,14 +550,15 @@ __global__ void __launch_bounds__(kRows) block_join_kernel(const __grid_constant
     const int group = p.q_heads / c.heads, tid = threadIdx.x, d0 = blockIdx.y * 16;
     int64_t i = blockIdx.x;
     int row;
-    if (!joined_item(c, group, kRows, i, row)) return;
-    int64_t begin;
-    const int n = row_tokens(c, row, begin), len = row_length(c, row), blocks = blocks_of(n, group);
-    if (blocks == 0 || i >= (int64_t)blocks * c.heads) return;
-    const int head = (int)(i / blocks), block = (int)(i % blocks);
+    const bool there = joined_item(c, group, kRows, i, row);
+    int64_t begin = 0;
+    const int n = there ? row_tokens(c, row, begin) : 0, len = there ? row_length(c, row) : 0, blocks = blocks_of(n, group);
+    const bool ours = blocks > 0 && i < (int64_t)blocks * c.heads;
+    const int head = ours ? (int)(i / blocks) : 0, block = ours ? (int)(i % blocks) : 0;
     const int64_t before = tiles_before(n, len, group, block);
-    const int tiles = tiles_of(block_seen(n, len, group, block));
-    cudaGridDependencySynchronize();
+    const int tiles = ours ? tiles_of(block_seen(n, len, group, block)) : 0;
+    follow_stream();
+    if (!ours) return;
     const int64_t per = share_of(p.first_work[c.rows], p.ctas);
     const int64_t each = (p.first_work[row + 1] - p.first_work[row]) / c.heads;
     const int64_t w0 = p.first_work[row] + head * each + before, w1 = w0 + tiles;
@@ -592,18 +593,9 @@ template <typename T, int kDim>
 cudaError_t launch_dim(const AttentionParams& p, cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(block_attention_kernel<T, kDim>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
     if (e != cudaSuccess) return e;
-    block_attention_kernel<T, kDim><<<p.ctas, kThreads, kSmemBytes, stream>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)joined_items(p.c, p.q_heads / p.c.heads, kRows), kDim / 16);
-    cfg.blockDim = dim3(kRows);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, block_join_kernel<T, kDim>, p);
+    e = launch_early(block_attention_kernel<T, kDim>, dim3(p.ctas), kThreads, kSmemBytes, stream, 1, p);
+    if (e != cudaSuccess) return e;
+    return launch_early(block_join_kernel<T, kDim>, dim3((unsigned)joined_items(p.c, p.q_heads / p.c.heads, kRows), kDim / 16), kRows, 0, stream, 1, p);
 }
 
 }  // namespace

@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) page_plan_kernel(const __grid
     extern __shared__ int32_t s_pages[];
     __shared__ int s[33];
     __shared__ Counts counts;
-    cudaTriggerProgrammaticLaunchCompletion();
+    follow_stream();
     const int cta = blockIdx.x, ctas = gridDim.x, tid = threadIdx.x;
     const int entries = p.rows * p.width;
     const PageArray<kGlobal> held{kGlobal ? p.held : s_pages, shift}, first{kGlobal ? p.first : s_pages + (1 << shift), shift};
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) page_compact_kernel(const __g
     extern __shared__ int32_t s_pages[];
     __shared__ int s[33], s_below;  // r(n)
     __shared__ Counts counts;
-    cudaTriggerProgrammaticLaunchCompletion();
+    follow_stream();
     const int cta = blockIdx.x, ctas = gridDim.x, tid = threadIdx.x, mask = (1 << shift) - 1;
     const int entries = p.rows * p.width;
     const PageArray<kGlobal> map{kGlobal ? p.page_map : s_pages, shift}, holes{kGlobal ? p.list : s_pages + (1 << shift), shift};
@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const __grid_co
                                                                  int32_t pages, const int32_t* src,
                                                                  const int32_t* dst, const int32_t* count,
                                                                  int32_t limit, int32_t* status) {
-    cudaGridDependencySynchronize();
+    follow_stream();
     const int64_t n = count ? *count : limit;
     for (int64_t w = blockIdx.x; w < n * pools.chunks; w += gridDim.x) {
         const int64_t i = w / pools.chunks;
@@ -440,23 +440,12 @@ cudaError_t launch_plan(K shared, K global, int arrays, const PagePlan& p, cudaS
     while (((int64_t)ctas << shift) < p.pages) ++shift;
     const bool fits = (1 << shift) <= kPlanPages;
     K kernel = fits ? shared : global;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(kPlanThreads);
-    cfg.dynamicSmemBytes = fits ? ((size_t)arrays * 4) << shift : 0;
-    cfg.stream = stream;
-    if (cfg.dynamicSmemBytes > 40 * 1024) {  // the static part counts too
+    const size_t smem = fits ? ((size_t)arrays * 4) << shift : 0;
+    if (smem > 40 * 1024) {  // the static part counts too
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, arrays * 4 * kPlanPages);
         if (e != cudaSuccess) return e;
     }
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ctas;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p, shift);
+    return launch_early(kernel, dim3(ctas), kPlanThreads, smem, stream, ctas, p, shift);
 }
 
 template <int kMode>
@@ -482,17 +471,7 @@ cudaError_t launch_page_copy(const PoolSet& pools, int32_t pages, const int32_t*
     if (limit <= 0 || pools.chunks == 0) return cudaSuccess;
     const int64_t most = (int64_t)limit * pools.chunks;
     const int grid = (int)(most < sm_count * 4ll ? most : sm_count * 4ll);
-    // Launched while the plan before it still runs; it waits for the plan's lists itself.
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kCopyThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, page_copy_kernel, pools, pages, src, dst, count, limit, status);
+    return launch_early(page_copy_kernel, dim3(grid), kCopyThreads, 0, stream, 1, pools, pages, src, dst, count, limit, status);
 }
 
 }  // namespace kda

@@ -16,6 +16,34 @@ constexpr int32_t kStatusNonfinite = 9;
 // Records the first condition since the last read.
 __device__ __forceinline__ void report(int32_t* status, int32_t code) { atomicCAS(status, kStatusOk, code); }
 
+// The serving operators' launches are a few microseconds each, so each may be set up while the
+// one before it in the stream runs: launched with launch_early, a kernel calls follow_stream before
+// it reads or writes anything that another launch writes, on every path.  There it waits until the
+// launches before it are complete; the one after it may be set up from then on, which is why all
+// that a kernel's own predecessor did not write may be read before the call.
+__device__ __forceinline__ void follow_stream() {
+    cudaGridDependencySynchronize();
+    cudaTriggerProgrammaticLaunchCompletion();
+}
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, int cluster, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ---- recurrent step on pages ------------------------------------------------------------
 // s0 == sfin is a pool: sequence n's states are at element state_pages[n] * page_stride;
 // negative pages are idle sequences.

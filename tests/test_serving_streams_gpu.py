@@ -72,3 +72,66 @@ def test_legacy_handles():
         got = call(handle)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_capture_after_other_work():
+    # Launches that may be set up early, captured behind a copy, behind another stream's work and
+    # first of all.
+    call = calls()["beam"]
+    want = call(None)
+    x = torch.zeros(1 << 20, device="cuda")
+    y = torch.zeros(1 << 20).pin_memory()
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    other.wait_stream(torch.cuda.current_stream())
+    call(other)  # (each stream has its workspace before the capture)
+    with torch.cuda.stream(side):
+        call(None)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            got = [call(None)]
+            x.copy_(y, non_blocking=True)
+            got.append(call(None))
+            other.wait_stream(side)
+            with torch.cuda.stream(other):
+                x.add_(1)
+                got.append(call(None))
+            side.wait_stream(other)
+            got.append(call(None))
+    g.replay()
+    torch.cuda.synchronize()
+    for r in got:
+        assert all(torch.equal(a, b) for a, b in zip(r, want))
+
+
+def test_chains_of_calls_without_waits():
+    # Each call reads what the one before it wrote: appends of a token, attention over it, forks
+    # of both, with nothing between them that would hold the stream up.
+    def run(wait):
+        gen = torch.Generator("cuda").manual_seed(11)
+        rows, page = 4, 16
+        tables, refs = torch.full((rows, 8), -1, dtype=torch.int32, device="cuda"), torch.zeros(64, dtype=torch.int32, device="cuda")
+        codes = [torch.zeros(64, 2, page, 64, dtype=torch.uint8, device="cuda") for _ in range(2)]
+        scales = [torch.zeros(64, 2, device="cuda") for _ in range(2)]
+        k, v, q, logits = (torch.randn(100, rows, *s, device="cuda", generator=gen) for s in ((2, 64), (2, 64), (4, 64), (300,)))
+        k, v, q = k.bfloat16(), v.bfloat16(), q.bfloat16()
+        lens = [torch.full((rows,), n, dtype=torch.int32, device="cuda") for n in range(102)]
+        scores, outs = torch.zeros(2, 2, device="cuda"), []
+        torch.cuda.synchronize()
+        for i in range(100):
+            tables, refs = K.kda_pages_alloc(tables, refs, lens[i // page + 1])
+            wait()
+            K.kda_kvcache_append(k[i], v[i], *codes, *scales, tables, lens[i])
+            wait()
+            outs.append(K.kda_kvcache_attention(q[i], *codes, *scales, tables, lens[i + 1]))
+            wait()
+            scores, tok, parents = K.kda_beam_select(logits[i].view(2, 2, 300), scores)
+            wait()
+            tables, refs = K.kda_pages_fork(tables, refs, parents.view(-1), lens=lens[i + 1], page_tokens=page, pools=codes + scales)
+            wait()
+            outs += [tok, parents, tables]
+        return outs
+    want = run(torch.cuda.synchronize)
+    for _ in range(5):
+        assert all(torch.equal(a, b) for a, b in zip(run(lambda: None), want))
+    assert K.kda_get_device_status() == 0
