@@ -8,7 +8,7 @@
 // row took 13 to 34 us each, most of it in the interpreter; here 6 to 18 (GB300).
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/EmptyTensor.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -96,10 +96,13 @@ struct Place {
         stream = own.stream();
     }
     Tensor empty(IntArrayRef shape, ScalarType type) const {
-        const auto options = at::TensorOptions().dtype(type).device(device);
-        if (own.stream() == current.stream()) return at::empty(shape, options);
+        // (The allocation itself: 0.3 to 0.6 us less a tensor than a call of at::empty.)
+        const auto allocate = [&] {
+            return Tensor(at::detail::empty_generic(shape, c10::cuda::CUDACachingAllocator::get(), c10::DispatchKeySet(c10::DispatchKey::CUDA), type, std::nullopt));
+        };
+        if (own.stream() == current.stream()) return allocate();
         const c10::cuda::CUDAStreamGuard set(own);
-        Tensor t = at::empty(shape, options);
+        Tensor t = allocate();
         if (t.numel()) c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), current);
         return t;
     }
