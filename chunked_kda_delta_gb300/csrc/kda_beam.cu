@@ -5,8 +5,11 @@
 // beam).  Its warps stream it in steps of four 16-byte loads a lane, the next step's loads
 // under way while they work on this one; a lane keeps a running sum of exponentials and
 // notes the largest value of each of its steps, nothing else.  Selection comes after the stream:
-// the lanes form 32 groups (128 where k + 1 does not fit), and the (k + 1)-th largest of the
-// groups' maxima is not above the segment's (k + 1)-th largest value.  Only the steps of lanes
+// the values form 32 groups by lane (128 by lane and load where k + 1 does not fit), and the
+// (k + 1)-th largest of the groups' maxima is not above the segment's (k + 1)-th largest value.
+// (Groups of neighbouring lanes of one warp are empty in short segments, the last of most
+// rows: without a bound all of their values are candidates, too many for the buffer, and the
+// rounds that are left then took 40 us for 16 beams of 1326 or 9077 logits instead of 9.)  Only the steps of lanes
 // whose noted maximum reaches that bound are read again, a few dozen bytes each and little
 // more than k + 1 of them, and their values that reach it are the candidates.  (Keeping sorted
 // lists while streaming, with a bound that rises, took 12 us more on 256 rows of 131072: some
@@ -205,9 +208,10 @@ template <typename T, int kBound>
 __global__ void __launch_bounds__(kScanThreads, 4) beam_scan_kernel(const BeamParams p) {
     constexpr int kVec = 16 / sizeof(T), kPer = Logit<T>::kPer;
     constexpr int kStep = kLoads * 32 * kVec;
-    constexpr int kGroupLanes = kScanThreads / kBound;
+    constexpr int kGroupsOf = kBound / 32;  // groups that a lane adds to: one, or one for each of its loads
+    static_assert(kGroupsOf == 1 || kGroupsOf == kLoads, "groups");
     __shared__ float s_most[kMaxSteps][kScanThreads];
-    __shared__ float s_group[kBound];
+    __shared__ float s_group[kScanWarps][kBound];
     __shared__ float4 s_sums[kScanWarps];
     __shared__ uint64_t s_key[kBuffer], s_red[kScanWarps];
     __shared__ int s_keys, s_found, s_step[kBuffer];
@@ -225,7 +229,10 @@ __global__ void __launch_bounds__(kScanThreads, 4) beam_scan_kernel(const BeamPa
     constexpr int kTurn = kScanWarps * kStep;
 
     Sums s{kNegInf, 0.f, kNegInf, 0.f};
-    float group = kNegInf;
+    float mine = kNegInf;  // the largest of this lane
+    float group[kGroupsOf];
+#pragma unroll
+    for (int i = 0; i < kGroupsOf; ++i) group[i] = kNegInf;
     if (tid == 0) s_keys = s_found = 0;
 
     uint4 next[kLoads];
@@ -248,15 +255,18 @@ __global__ void __launch_bounds__(kScanThreads, 4) beam_scan_kernel(const BeamPa
             w[4 * i] = next[i].x; w[4 * i + 1] = next[i].y; w[4 * i + 2] = next[i].z; w[4 * i + 3] = next[i].w;
         }
         if (at + kTurn < end) load(at + kTurn);
-        uint32_t mw = w[0];
-#pragma unroll
-        for (int i = 1; i < kLoads * 4; ++i) mw = Logit<T>::larger(mw, w[i]);
-        float m;
-        {
+        const auto value = [](uint32_t word) {
             float v[kPer];
-            Logit<T>::unpack(mw, v);
-            m = kPer == 2 ? fmaxf(v[0], v[kPer - 1]) : v[0];
+            Logit<T>::unpack(word, v);
+            return kPer == 2 ? fmaxf(v[0], v[kPer - 1]) : v[0];
+        };
+        uint32_t ml[kLoads], mw;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            ml[i] = Logit<T>::larger(Logit<T>::larger(w[4 * i], w[4 * i + 1]), Logit<T>::larger(w[4 * i + 2], w[4 * i + 3]));
+            mw = i ? Logit<T>::larger(mw, ml[i]) : ml[i];
         }
+        float m = value(mw);
         const float c_new = fmaxf(s.c, ceilf(m * kLog2e));
         const float ref = c_new == kNegInf ? 0.f : c_new;
         float acc[4] = {0.f, 0.f, 0.f, 0.f};
@@ -270,20 +280,25 @@ __global__ void __launch_bounds__(kScanThreads, 4) beam_scan_kernel(const BeamPa
         const float part = (acc[0] + acc[1]) + (acc[2] + acc[3]);
         if (!(m < kHuge) || part != part || (m < -kHuge && m > kNegInf)) {
             m = slow_sums<T>(x, at + lane * kVec, p.vocab, s);
+            group[0] = fmaxf(group[0], m);  // (of any one group)
         } else {
+            if constexpr (kGroupsOf == 1) {
+                group[0] = fmaxf(group[0], m);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i) group[i] = fmaxf(group[i], value(ml[i]));
+            }
             if (s.c > kNegInf) s.sum *= exp2_fast(s.c - ref);
             s.c = c_new;
             s.sum += part;
         }
         s_most[steps][tid] = m;
-        group = fmaxf(group, m);
+        mine = fmaxf(mine, m);
     }
-    const float mine = group;  // the largest of this lane
 
     // Sums and group maxima put together.
 #pragma unroll
-    for (int o = 1; o < kGroupLanes; o <<= 1) group = fmaxf(group, __shfl_xor_sync(0xffffffffu, group, o));
-    if (tid % kGroupLanes == 0) s_group[tid / kGroupLanes] = group;
+    for (int i = 0; i < kGroupsOf; ++i) s_group[warp][32 * i + lane] = group[i];
     float c_all = s.c, h_all = s.huge;
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
@@ -311,16 +326,23 @@ __global__ void __launch_bounds__(kScanThreads, 4) beam_scan_kernel(const BeamPa
         }
         p.part[blockIdx.x] = a;
     }
+    if (tid < kBound) {
+        float g = s_group[0][tid];
+#pragma unroll
+        for (int w = 1; w < kScanWarps; ++w) g = fmaxf(g, s_group[w][tid]);
+        s_group[0][tid] = g;
+    }
+    __syncthreads();
     // The c1-th largest group maximum; every warp finds it for itself.
     float bound = kNegInf;
 #pragma unroll
     for (int r = 0; r < kBound / 32; ++r) {
         const int me = r * 32 + lane;
-        const float g = s_group[me];
+        const float g = s_group[0][me];
         int larger = 0;
 #pragma unroll 8
         for (int i = 0; i < kBound; ++i) {
-            const float y = s_group[i];
+            const float y = s_group[0][i];
             larger += y > g || (y == g && i < me);
         }
         const unsigned who = __ballot_sync(0xffffffffu, larger == c1 - 1);

@@ -61,6 +61,19 @@ def test_many_outputs_and_padded_rows(dtype):
     check(draw(rng, 3, 1, 40000), scores_of(rng, 3, 1), k=2, dtype=dtype)
 
 
+@pytest.mark.parametrize("v", [520, 777, 1030, 2049, 9077])
+@pytest.mark.parametrize("k", [16, 31, 32, 64])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_short_segments(v, k, dtype):
+    # rows, and ends of rows, of a few of the scan's steps; also with a block of tokens allowed only
+    rng = np.random.default_rng(v + k)
+    x = draw(rng, 2, 16, v)
+    check(x, scores_of(rng, 2, 16), k=k, dtype=dtype)
+    x[:, :, : v // 3] = -np.inf
+    x[:, :, v // 3 + v // 2:] = -np.inf
+    check(x, scores_of(rng, 2, 16), k=k, dtype=dtype)
+
+
 def test_finished_beams():
     rng = np.random.default_rng(2)
     done = rng.random((6, 4)) < 0.5
