@@ -95,7 +95,8 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(c
     // Every CTA needs the rows' prefix; past kMaxListed rows all write the same values to the
     // scratch.
     int64_t* first = c.rows <= kMaxListed ? s_first : p.first_work;
-    scan_rows<kThreads>(c.rows, first, s_scan, [&](int r) {  // items: column blocks by key/value heads
+    scan_rows<kThreads>(c.rows, first, s_scan, [&](int r) -> int64_t {  // items: column blocks by key/value heads
+        if (r >= c.rows) return 0;
         int64_t begin;
         const int n = row_tokens(c, r, begin);
         return ((int64_t)n * group + kCols - 1) / kCols * c.heads * row_slabs(row_length(c, r));

@@ -87,7 +87,7 @@ __device__ __forceinline__ void scan_rows(int rows, int64_t* first, int64_t* s, 
     int64_t base = 0;
     for (int r0 = 0; r0 < rows; r0 += kThreads) {
         const int r = r0 + tid;
-        const int64_t w = r < rows ? work(r) : 0;
+        const int64_t w = work(r);
         int64_t x = w;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {

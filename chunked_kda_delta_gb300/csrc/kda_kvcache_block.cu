@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
     constexpr uint32_t kLbo = 128, kSbo = kDim * 16;  // K-major core matrices: along the reduction, along rows
     constexpr uint32_t kBoxBytes = kKeys * 128;       // 64 channels of V
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    __shared__ int64_t s_first[kMaxListed + 1], s_scan[kThreads / 32];
+    __shared__ int64_t s_first[kMaxListed + 1], s_scan[kThreads / 32], s_tiles[kThreads / 32];
     __shared__ __align__(16) Meta s_meta[4][kBlocks];
     __shared__ volatile int s_bad;  // a wait ran out
     __shared__ __align__(8) uint64_t s_bar[3];
@@ -163,14 +163,33 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
     }
     follow_stream();
     int64_t* first = c.rows <= kMaxListed ? s_first : p.first_work;
-    for (int r = warp; r < c.rows; r += kThreads / 32) {
+    // Tiles of the rows.  As many rows as warps: a warp each.  More: a thread each, where a row has few
+    // blocks, else its warp for it.
+    constexpr int kFewBlocks = 4;
+    if (c.rows <= kThreads / 32) {
         int64_t begin;
-        const int n = row_tokens(c, r, begin);
-        const int64_t tiles = tiles_before(n, row_length(c, r), group, blocks_of(n, group)) * c.heads;
-        if (lane == 0) first[r] = tiles;
+        const int n = warp < c.rows ? row_tokens(c, warp, begin) : 0, len = warp < c.rows ? row_length(c, warp) : 0;
+        const int64_t tiles = tiles_before(n, len, group, blocks_of(n, group));
+        if (lane == 0) s_tiles[warp] = tiles;
+        __syncthreads();
     }
-    __syncthreads();
-    scan_rows<kThreads>(c.rows, first, s_scan, [&](int r) { return first[r]; });
+    scan_rows<kThreads>(c.rows, first, s_scan, [&](int r) {
+        int64_t tiles = 0;
+        if (c.rows <= kThreads / 32) {
+            if (r < c.rows) tiles = s_tiles[r];
+        } else {
+            int64_t begin;
+            const int n = r < c.rows ? row_tokens(c, r, begin) : 0, len = r < c.rows ? row_length(c, r) : 0, blocks = blocks_of(n, group);
+            for (int x = 0; x < blocks && blocks <= kFewBlocks; ++x) tiles += tiles_of(block_seen(n, len, group, x));
+            for (unsigned many = __ballot_sync(0xffffffffu, blocks > kFewBlocks); many; many &= many - 1) {
+                const int from = __ffs(many) - 1;
+                const int64_t t = tiles_before(__shfl_sync(0xffffffffu, n, from), __shfl_sync(0xffffffffu, len, from), group,
+                                               __shfl_sync(0xffffffffu, blocks, from));
+                if (lane == from) tiles = t;
+            }
+        }
+        return tiles * c.heads;
+    });
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

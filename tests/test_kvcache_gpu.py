@@ -107,6 +107,13 @@ def test_one_long_row_is_split():
     check_attention(rng, 2, 8, 1, 128, 64, [20000, 1], [1, 1], "fp16", cu=False)
 
 
+@pytest.mark.parametrize("counts", [[20] * 700, [1] * 1500, [600] + [3] * 20 + [0, 150, 900], [2, 1100, 0, 70]])
+def test_many_rows_and_rows_of_many_blocks(counts):
+    rng = np.random.default_rng(len(counts))
+    lens = [n + int(rng.integers(0, 40)) for n in counts]
+    check_attention(rng, len(lens), 2, 1, 64, 16, lens, counts, "bf16")
+
+
 def test_large_scores_and_extreme_queries():
     rng = np.random.default_rng(4)
     q = torch.as_tensor(rng.standard_normal((3, 4, 64)))
