@@ -119,6 +119,11 @@ __device__ __forceinline__ int64_t tiles_before(int n, int len, int group, int b
     return x;
 }
 
+// An item that lies in the shares [its own, last] of several CTAs; last < 0: none.
+struct alignas(16) SplitItem {
+    int begin, n, head, block, slot, last, unused[2];  // first token and tokens of its row; slot of its first part
+};
+
 struct Meta {  // scales of 16 keys; k negative where the page is missing
     float k, v;
 };
@@ -212,6 +217,8 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
         phase_o ^= 1;
     };
 
+    // The item that begins in this share and ends in another: none yet.
+    if (tid == 0) reinterpret_cast<SplitItem*>(p.split_items)[blockIdx.x].last = -1;
     for (int64_t w = w_begin; w < w_end;) {
         const int row = row_of(first, c.rows, w);
         int64_t begin;
@@ -517,6 +524,8 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
 
         const bool whole = w == item && item_end <= w_end;
         const int64_t slot = 2 * (int64_t)blockIdx.x + (w == w_begin ? 0 : 1);
+        if (tid == 0 && w == item && item_end > w_end)
+            reinterpret_cast<SplitItem*>(p.split_items)[blockIdx.x] = SplitItem{(int)begin, n, head, block, (int)slot, (int)((item_end - 1) / per), 0, 0};
         const float by = whole ? (l > 0.f ? ref / l : 0.f) : ref;
         T* out = static_cast<T*>(p.out) + (begin + (there ? f / group : 0)) * p.out_stride +
                  (int64_t)(head * group + (there ? f % group : 0)) * kDim;
@@ -561,51 +570,95 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
     if (warp == 0) tmem_dealloc(tmem, kColumns);
 }
 
-// Joins the parts of the items that lie in several CTAs' shares: blockIdx.x counts items,
-// blockIdx.y 16 channels, a thread has one query row.
-template <typename T, int kDim>
-__global__ void __launch_bounds__(kRows) block_join_kernel(const __grid_constant__ AttentionParams p) {
+// Joins the parts of the items that lie in several CTAs' shares: blockIdx.y counts channels, a
+// thread has one query row.  kShares 1: blockIdx.x is the share that the item begins in, at most
+// as many as there are CTAs, however many items there are.  kShares > 1 (few items, of many
+// parts): blockIdx.x counts items, and that many threads have a row's parts in turn.  (One thread
+// after the other through 91 parts took 65 of 73 us for 34 tokens of 3 heads over 5670 keys; a
+// CTA for each of 2560 items and 16 channels 80 of 672 us for 64 rows of 64 tokens, 32 heads.)
+template <typename T, int kDim, int kShares>
+__global__ void __launch_bounds__(kRows * kShares, kShares == 4 ? 2 : 1) block_join_kernel(const __grid_constant__ AttentionParams p) {
+    constexpr int kCh = kShares == 8 ? 4 : kShares == 4 ? 8 : 16, kAhead = kShares == 8 ? 6 : kShares == 4 ? 3 : 1;  // channels, parts under way
+    __shared__ float s_part[kShares > 1 ? kShares - 1 : 1][kCh + 2][kShares > 1 ? kRows : 1];
     const CacheParams& c = p.c;
-    const int group = p.q_heads / c.heads, tid = threadIdx.x, d0 = blockIdx.y * 16;
-    int64_t i = blockIdx.x;
-    int row;
-    const bool there = joined_item(c, group, kRows, i, row);
-    int64_t begin = 0;
-    const int n = there ? row_tokens(c, row, begin) : 0, len = there ? row_length(c, row) : 0, blocks = blocks_of(n, group);
-    const bool ours = blocks > 0 && i < (int64_t)blocks * c.heads;
-    const int head = ours ? (int)(i / blocks) : 0, block = ours ? (int)(i % blocks) : 0;
-    const int64_t before = tiles_before(n, len, group, block);
-    const int tiles = ours ? tiles_of(block_seen(n, len, group, block)) : 0;
-    follow_stream();
-    if (!ours) return;
-    const int64_t per = share_of(p.first_work[c.rows], p.ctas);
-    const int64_t each = (p.first_work[row + 1] - p.first_work[row]) / c.heads;
-    const int64_t w0 = p.first_work[row] + head * each + before, w1 = w0 + tiles;
-    const int64_t u0 = w0 / per, u1 = (w1 - 1) / per;
+    const int group = p.q_heads / c.heads, tid = threadIdx.x % kRows, share = threadIdx.x / kRows, d0 = blockIdx.y * kCh;
+    int64_t begin, u0, u1, slot0;
+    int n, head, block;
+    if constexpr (kShares == 1) {
+        follow_stream();
+        const SplitItem x = reinterpret_cast<const SplitItem*>(p.split_items)[blockIdx.x];
+        if (x.last < 0) return;
+        begin = x.begin, n = x.n, head = x.head, block = x.block, slot0 = x.slot, u0 = blockIdx.x, u1 = x.last;
+    } else {
+        int64_t i = blockIdx.x;
+        int row;
+        const bool there = joined_item(c, group, kRows, i, row);
+        begin = n = 0;
+        if (there) n = row_tokens(c, row, begin);
+        const int len = there ? row_length(c, row) : 0, blocks = blocks_of(n, group);
+        const bool ours = blocks > 0 && i < (int64_t)blocks * c.heads;
+        head = ours ? (int)(i / blocks) : 0, block = ours ? (int)(i % blocks) : 0;
+        const int64_t before = tiles_before(n, len, group, block);
+        const int tiles = ours ? tiles_of(block_seen(n, len, group, block)) : 0;
+        follow_stream();
+        if (!ours) return;
+        const int64_t per = share_of(p.first_work[c.rows], p.ctas);
+        const int64_t each = (p.first_work[row + 1] - p.first_work[row]) / c.heads;
+        const int64_t w0 = p.first_work[row] + head * each + before, w1 = w0 + tiles;
+        u0 = w0 / per, u1 = (w1 - 1) / per, slot0 = 2 * u0 + (u0 * per >= w0 ? 0 : 1);
+        if (u0 == u1) return;
+    }
     const int f = block * kRows + tid;
-    if (u0 == u1 || f >= n * group) return;
-    float top = kNegInf, sum = 0.f, acc[16];
+    const bool mine = f < n * group;
+    float top = kNegInf, sum = 0.f, acc[kCh];
 #pragma unroll
-    for (int d = 0; d < 16; ++d) acc[d] = 0.f;
-    for (int64_t u = u0; u <= u1; ++u) {
-        const int64_t slot = 2 * u + (u * per >= w0 ? 0 : 1);
-        const float mk = p.part_ml[(slot * 2 + 0) * kRows + tid], lk = p.part_ml[(slot * 2 + 1) * kRows + tid];
+    for (int d = 0; d < kCh; ++d) acc[d] = 0.f;
+    auto add = [&](float mk, float lk, const float* o) {
         const float m = fmaxf(top, mk), use = m == kNegInf ? 0.f : m;
         const float a = exp2f(top - use), b = exp2f(mk - use);
         top = m;
         sum = sum * a + lk * b;
 #pragma unroll
-        for (int d = 0; d < 16; ++d) acc[d] = acc[d] * a + p.part_o[(slot * kDim + d0 + d) * kRows + tid] * b;
+        for (int d = 0; d < kCh; ++d) acc[d] = acc[d] * a + o[d] * b;
+    };
+    for (int64_t k = u0 + share; mine && k <= u1; k += kAhead * kShares) {
+        float mk[kAhead], lk[kAhead], o[kAhead][kCh];
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) {
+            const int64_t u = k + x * kShares;
+            if (u > u1) continue;
+            const int64_t slot = u == u0 ? slot0 : 2 * u;
+            mk[x] = p.part_ml[(slot * 2 + 0) * kRows + tid];
+            lk[x] = p.part_ml[(slot * 2 + 1) * kRows + tid];
+#pragma unroll
+            for (int d = 0; d < kCh; ++d) o[x][d] = p.part_o[(slot * kDim + d0 + d) * kRows + tid];
+        }
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x)
+            if (k + x * kShares <= u1) add(mk[x], lk[x], o[x]);
     }
+    if constexpr (kShares > 1) {
+        if (share) {
+            s_part[share - 1][kCh][tid] = top;
+            s_part[share - 1][kCh + 1][tid] = sum;
+#pragma unroll
+            for (int d = 0; d < kCh; ++d) s_part[share - 1][d][tid] = acc[d];
+        }
+        __syncthreads();
+        if (share) return;
+        for (int x = 0; x < kShares - 1; ++x) {
+            float o[kCh];
+#pragma unroll
+            for (int d = 0; d < kCh; ++d) o[d] = s_part[x][d][tid];
+            add(s_part[x][kCh][tid], s_part[x][kCh + 1][tid], o);
+        }
+    }
+    if (!mine) return;
     const float by = sum > 0.f ? 1.f / sum : 0.f;
     T* out = static_cast<T*>(p.out) + (begin + f / group) * p.out_stride + (int64_t)(head * group + f % group) * kDim + d0;
 #pragma unroll
-    for (int d = 0; d < 16; d += 8) {
-        uint32_t u[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) u[k] = Act<T>::pack(acc[d + 2 * k] * by, acc[d + 2 * k + 1] * by);
-        *reinterpret_cast<uint4*>(out + d) = make_uint4(u[0], u[1], u[2], u[3]);
-    }
+    for (int d = 0; d < kCh; d += 4)
+        *reinterpret_cast<uint2*>(out + d) = make_uint2(Act<T>::pack(acc[d] * by, acc[d + 1] * by), Act<T>::pack(acc[d + 2] * by, acc[d + 3] * by));
 }
 
 template <typename T, int kDim>
@@ -614,7 +667,13 @@ cudaError_t launch_dim(const AttentionParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     e = launch_early(block_attention_kernel<T, kDim>, dim3(p.ctas), kThreads, kSmemBytes, stream, 1, p);
     if (e != cudaSuccess) return e;
-    return launch_early(block_join_kernel<T, kDim>, dim3((unsigned)joined_items(p.c, p.q_heads / p.c.heads, kRows), kDim / 16), kRows, 0, stream, 1, p);
+    // As many threads to a row as one wave holds: few items have many parts each.
+    const int64_t items = joined_items(p.c, p.q_heads / p.c.heads, kRows);
+    if (items * (kDim / 4) <= 2 * p.sm_count)
+        return launch_early(block_join_kernel<T, kDim, 8>, dim3((unsigned)items, kDim / 4), kRows * 8, 0, stream, 1, p);
+    if (items * (kDim / 8) <= 4 * p.sm_count)
+        return launch_early(block_join_kernel<T, kDim, 4>, dim3((unsigned)items, kDim / 8), kRows * 4, 0, stream, 1, p);
+    return launch_early(block_join_kernel<T, kDim, 1>, dim3((unsigned)p.ctas, kDim / 16), kRows, 0, stream, 1, p);
 }
 
 }  // namespace

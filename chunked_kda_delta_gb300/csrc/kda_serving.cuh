@@ -131,6 +131,7 @@ struct AttentionParams {
     int32_t q_heads;
     float scale;              // times log2(e)
     // scratch
+    void* split_items;    // scratch of 32 bytes a CTA (items of 128 query rows)
     int64_t* first_work;      // [rows + 1]
     float* part_o;            // [slots][cols * dim], in the layout of the product's fragments
     float* part_ml;           // [slots][cols][2]: maximum and sum

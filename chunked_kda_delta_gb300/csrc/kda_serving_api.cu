@@ -417,10 +417,11 @@ kda_status kda_kvcache_attention(const kda_kvcache* cache, const void* q, int32_
         p.ctas = kda::attention_ctas(cache->head_dim, cols, f16, di->sm_count);
         const size_t parts = (cols == kda::kBlockRows ? (size_t)2 * p.ctas : kda::attention_slots(p.ctas)) * cols;
         char* ws = nullptr;
-        if ((st = scratch(dev, stream, parts * (cache->head_dim + 2) * 4 + ((size_t)cache->rows + 1) * 8, &ws)) != KDA_OK) return st;
+        if ((st = scratch(dev, stream, parts * (cache->head_dim + 2) * 4 + (size_t)p.ctas * 32 + ((size_t)cache->rows + 1) * 8, &ws)) != KDA_OK) return st;
         p.part_o = reinterpret_cast<float*>(ws);
         p.part_ml = p.part_o + parts * cache->head_dim;
-        p.first_work = reinterpret_cast<int64_t*>(p.part_ml + parts * 2);
+        p.split_items = p.part_ml + parts * 2;
+        p.first_work = reinterpret_cast<int64_t*>(p.part_ml + parts * 2 + (size_t)p.ctas * 8);
         p.q = q;
         p.out = out;
         p.q_stride = q_stride;

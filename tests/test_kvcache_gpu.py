@@ -107,6 +107,16 @@ def test_one_long_row_is_split():
     check_attention(rng, 2, 8, 1, 128, 64, [20000, 1], [1, 1], "fp16", cu=False)
 
 
+@pytest.mark.parametrize("rows,hkv,group,d,n,length", [
+    (1, 1, 3, 128, 34, 5670),  # one item of many parts, and more of fewer
+    (2, 2, 7, 64, 7, 9000), (6, 3, 5, 128, 8, 3001), (12, 4, 4, 64, 20, 1945), (3, 8, 16, 64, 9, 700),
+    (1, 1, 5, 64, 1, 40001), (1, 1, 12, 128, 1, 20001), (5, 8, 2, 128, 2, 3333), (9, 8, 1, 64, 1, 2500)])
+def test_few_items_of_many_parts(rows, hkv, group, d, n, length):
+    rng = np.random.default_rng(length)
+    lens = [length - 7 * i for i in range(rows)]
+    check_attention(rng, rows, hkv * group, hkv, d, 32, lens, [n] * rows, "fp16", cu=n > 1)
+
+
 @pytest.mark.parametrize("counts", [[20] * 700, [1] * 1500, [600] + [3] * 20 + [0, 150, 900], [2, 1100, 0, 70]])
 def test_many_rows_and_rows_of_many_blocks(counts):
     rng = np.random.default_rng(len(counts))
