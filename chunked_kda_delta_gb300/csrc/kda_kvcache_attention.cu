@@ -23,15 +23,15 @@
 // enters as its ratio to the largest one met, so weights stay in [0, 1].  Running maximum,
 // sums, outputs and the joined parts are fp32.
 //
-// Work split: warps work alone.  The items' cached tokens, cut into slabs of 32, are numbered
+// Work split: warps work alone.  The items' cached tokens, cut into slabs, are numbered
 // through all items; every resident warp takes an equal contiguous share, however long the rows
 // are.  An item inside one share is written at once; the parts of the others, in the layout of
 // the product's fragments, are joined by a second launch.  (With four warps sharing each tile
 // and joining in shared memory at every item's end the loads paused there: 147 us instead of
 // 133 for 64 rows of up to 8192 tokens, 8 heads.  Asking L2 for codes two to eight slabs ahead
 // made it 1 to 35% slower, slabs of 16 keys with four CTAs an SM 5%, two CTAs without spills
-// 10%.)  Bound by HBM: that call takes 127 us, 0.83 of its bytes at the copy rate (718 MB), the join
-// and its tail with it; 4 rows of up to 131072 tokens, 4 heads, 71 us, 0.75; one row of 1000
+// 10%.)  Bound by HBM: that call takes 126 us, 0.84 of its bytes at the copy rate (718 MB), the join
+// and its tail with it; 4 rows of up to 131072 tokens, 4 heads, 68 us, 0.78; one row of 1000
 // tokens 8 us, two launches' latency.
 #include "kda_kvcache_attention.cuh"
 
@@ -40,7 +40,11 @@ namespace {
 
 constexpr int kThreads = 128, kWarps = 4;
 constexpr int kMaxListed = 1024;  // rows whose prefix fits in shared memory
-constexpr int kKeys = 32, kBlk = kKeys / 16;  // keys of a slab, and blocks of 16 in it
+// Keys of a slab: 4 KB of codes of K, so that as many bytes are under way for head_dim 64 as for
+// 128 (64 keys against 32 there: 85 rows of up to 7582 tokens, 32 heads over 2, 51 against 65 us; one
+// row of 130878, 9 over 3, 26 against 34).
+template <int kDim>
+constexpr int kSlabKeys = 4096 / kDim;
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
@@ -54,7 +58,17 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ int row_slabs(int len) { return len > kKeys ? (len + kKeys - 1) / kKeys : 1; }
+template <int kDim>
+__device__ __forceinline__ int row_slabs(int len) {
+    constexpr int kKeys = kSlabKeys<kDim>;
+    return len > kKeys ? (len + kKeys - 1) / kKeys : 1;
+}
+// 2^x by the hardware's instruction (results below 2^-126 are 0).
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 // Codes of 16 keys, widened, against the query rows: acc += K Q^T.  q(step, nt) gives the two
 // registers of a reduction step.
@@ -78,7 +92,7 @@ __device__ __forceinline__ void product_k(float (&acc)[kNT][4], const uint4 (&k)
 
 template <typename T, int kDim, int kNT>
 __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(const __grid_constant__ AttentionParams p) {
-    constexpr int kCols = 8 * kNT;
+    constexpr int kCols = 8 * kNT, kKeys = kSlabKeys<kDim>, kBlk = kKeys / 16;  // (blocks of 16 keys)
     constexpr int kHalves = kDim / 64;   // 16-byte loads of a key by a thread
     constexpr int kSteps = kDim / 16;    // reduction steps of S^T
     constexpr int kMT = kDim / 16;       // 16-channel tiles of O^T
@@ -99,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(c
         if (r >= c.rows) return 0;
         int64_t begin;
         const int n = row_tokens(c, r, begin);
-        return ((int64_t)n * group + kCols - 1) / kCols * c.heads * row_slabs(row_length(c, r));
+        return ((int64_t)n * group + kCols - 1) / kCols * c.heads * row_slabs<kDim>(row_length(c, r));
     });
     __syncthreads();
     if (blockIdx.x == 0 && c.rows <= kMaxListed)
@@ -112,7 +126,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(c
     for (int64_t w = w_begin; w < w_end;) {
         const int row = row_of(first, c.rows, w);
         int64_t begin;
-        const int n = row_tokens(c, row, begin), len = row_length(c, row), slabs = row_slabs(len);
+        const int n = row_tokens(c, row, begin), len = row_length(c, row), slabs = row_slabs<kDim>(len);
         const int64_t i_row = (w - first[row]) / slabs, item = first[row] + i_row * slabs, item_end = item + slabs;
         const int head = (int)(i_row % c.heads), block = (int)(i_row / c.heads);
         const int slab0 = (int)(w - item);
@@ -314,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(c
                     for (int s = 4; s <= 16; s <<= 1) top[col] = fmaxf(top[col], __shfl_xor_sync(0xffffffffu, top[col], s));
                     const float m_new = fmaxf(m[nt][col], top[col]);
                     const float m_use = m_new == kNegInf ? 0.f : m_new;
-                    fix[col] = exp2f(m[nt][col] - m_use);
+                    fix[col] = exp2_fast(m[nt][col] - m_use);
                     m[nt][col] = m_new;
                     l[nt][col] *= fix[col];
                     top[col] = m_use;
@@ -325,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(c
                     float e[4];
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        e[x] = exp2f(sc[i][nt][x] - top[x & 1]);
+                        e[x] = exp2_fast(sc[i][nt][x] - top[x & 1]);
                         l[nt][x & 1] += e[x];
                         e[x] *= wv;
                     }
@@ -396,13 +410,13 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(c
 
 // Joins the parts of the items that lie in several warps' shares.  blockIdx.x counts items,
 // blockIdx.y column tiles; a warp has 16 channels of 8 columns, in the fragments' layout.
-// kSplit (items of many parts): blockIdx.z is the channel tile, and the warps share the parts.
-constexpr int kJoinSplit = 8;  // warps that share the parts
-
-template <typename T, int kDim, int kNT, bool kSplit>
-__global__ void __launch_bounds__(kSplit ? kJoinSplit * 32 : kDim * 2) attention_join_kernel(const __grid_constant__ AttentionParams p) {
+// kShares > 1 (items of many parts): blockIdx.z is the channel tile, and that many warps share the
+// parts.
+template <typename T, int kDim, int kNT, int kShares>
+__global__ void __launch_bounds__(kShares > 1 ? kShares * 32 : kDim * 2) attention_join_kernel(const __grid_constant__ AttentionParams p) {
     constexpr int kCols = 8 * kNT, kMT = kDim / 16, kVWords = kDim / 32;
-    __shared__ float4 s_o[kSplit ? kJoinSplit : 1][32], s_ml[kSplit ? kJoinSplit : 1][32];
+    constexpr bool kSplit = kShares > 1;
+    __shared__ float4 s_o[kShares][32], s_ml[kShares][32];
     const CacheParams& c = p.c;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int nt = blockIdx.y, j = kSplit ? blockIdx.z : warp;
@@ -412,7 +426,7 @@ __global__ void __launch_bounds__(kSplit ? kJoinSplit * 32 : kDim * 2) attention
     const bool there = joined_item(c, group, kCols, i, row);
     int64_t begin = 0;
     const int n = there ? row_tokens(c, row, begin) : 0;
-    const int slabs = there ? row_slabs(row_length(c, row)) : 0;
+    const int slabs = there ? row_slabs<kDim>(row_length(c, row)) : 0;
     follow_stream();
     if (!there) return;
     const int64_t all = p.first_work[c.rows], w_row = p.first_work[row], w_next = p.first_work[row + 1];
@@ -437,7 +451,7 @@ __global__ void __launch_bounds__(kSplit ? kJoinSplit * 32 : kDim * 2) attention
         }
     };
     constexpr int kAhead = 8;
-    const int64_t step = kSplit ? kJoinSplit : 1;
+    const int64_t step = kShares;
     for (int64_t k = u0 + (kSplit ? warp : 0); k <= u1; k += kAhead * step) {
         float4 ml[kAhead], o[kAhead];
 #pragma unroll
@@ -457,7 +471,7 @@ __global__ void __launch_bounds__(kSplit ? kJoinSplit * 32 : kDim * 2) attention
         s_ml[warp][lane] = make_float4(top[0], sum[0], top[1], sum[1]);
         __syncthreads();
         if (warp) return;
-        for (int x = 1; x < kJoinSplit; ++x) add(s_ml[x][lane], s_o[x][lane]);
+        for (int x = 1; x < kShares; ++x) add(s_ml[x][lane], s_o[x][lane]);
     }
 #pragma unroll
     for (int col = 0; col < 2; ++col) {
@@ -477,10 +491,14 @@ cudaError_t launch_one(const AttentionParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const int64_t group = p.q_heads / c.heads;
     const int64_t items = joined_items(c, group, kCols);
-    // Fewer items than SMs leave SMs idle and have many parts each.
-    const bool split = items * kNT < p.sm_count;
-    return launch_early(split ? attention_join_kernel<T, kDim, kNT, true> : attention_join_kernel<T, kDim, kNT, false>,
-                        dim3((unsigned)items, kNT, split ? kDim / 16 : 1), split ? kJoinSplit * 32 : kDim * 2, 0, stream, 1, p);
+    // As many warps to a part of an item as a wave or two hold: few items have many parts each (2 rows
+    // of up to 24086 tokens: 20 us with 16, 29 with 8; 34 rows of 135: 17 us with one, 28 with 16).
+    const int64_t tiles = items * kNT * (kDim / 16);
+    if (tiles <= 2ll * p.sm_count)
+        return launch_early(attention_join_kernel<T, kDim, kNT, 16>, dim3((unsigned)items, kNT, kDim / 16), 512, 0, stream, 1, p);
+    if (tiles <= 5ll * p.sm_count)
+        return launch_early(attention_join_kernel<T, kDim, kNT, 4>, dim3((unsigned)items, kNT, kDim / 16), 128, 0, stream, 1, p);
+    return launch_early(attention_join_kernel<T, kDim, kNT, 1>, dim3((unsigned)items, kNT), kDim * 2, 0, stream, 1, p);
 }
 
 // CTAs an SM holds; the same on every device the library runs on.
