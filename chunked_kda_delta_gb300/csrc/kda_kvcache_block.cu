@@ -325,14 +325,12 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
             // This warp's 16 keys of each tile lie in one page.  Load number i of a lane: key
             // 8 (i % 2) + lane % 8, channels 16 (4 (i / 2) + lane / 8).
             const int mine = warp - kSoft / 32;
-            auto entry_at = [&](int tile) {
-                const int key = tile * kKeys + mine * 16;
-                return tile >= tile1 || key >= seen_max ? -1 : table[key >> page_shift];
-            };
+            auto needed = [&](int tile) { return tile < tile1 && tile * kKeys + mine * 16 < seen_max; };
+            auto entry_at = [&](int tile) { return needed(tile) ? table[(tile * kKeys + mine * 16) >> page_shift] : -1; };
             // (Looked at a tile after it was read: the wait for the table would hold up the loop.)
-            auto checked = [&](int32_t x) {
-                if (x < c.pages) return x;
-                if (lane == 0) report(c.status, kStatusBadIndex);
+            auto checked = [&](int32_t x, int tile) {
+                if (x >= 0 && x < c.pages) return x;
+                if (lane == 0 && needed(tile)) report(c.status, kStatusBadIndex);
                 return -1;
             };
             auto meta_of = [&](int32_t page) {
@@ -376,8 +374,8 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
 
             // Pages, scales and codes are read a tile or two ahead.
             int32_t page0 = entry_at(tile0), page1 = entry_at(tile0 + 1), page2 = entry_at(tile0 + 2);
-            page0 = checked(page0);
-            page1 = checked(page1);
+            page0 = checked(page0, tile0);
+            page1 = checked(page1, tile0 + 1);
             Meta meta1 = meta_of(page1);  // of tile + 1
             uint4 kr[kLoads], vr[kLoads];
             if (tile0 < tile1) {
@@ -402,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
                     tc_fence_after();
                     issue_s(tile + 1);
                 }
-                page2 = checked(page2);
+                page2 = checked(page2, tile + 2);
                 load(kr, c.k_codes, tile + 2, page2, 16);
 #pragma unroll
                 for (int i = 0; i < kLoads; ++i) {

@@ -102,6 +102,23 @@ def test_many_tokens_equal_single_tokens(d, page):
     assert K.kda_get_device_status() == 0
 
 
+@pytest.mark.parametrize("d,page,group,dtype", [(128, 16, 8, "bf16"), (128, 128, 5, "fp16"), (64, 32, 8, "bf16"), (64, 64, 7, "fp16")])
+@pytest.mark.parametrize("missing", [False, True])
+def test_pieces_of_prompts(d, page, group, dtype, missing):
+    # large enough for the kernel of 128 query rows an item
+    rng = np.random.default_rng(d + page)
+    counts, lens = [200, 0, 301, 1, 77], [200, 40, 700, 900, 78]
+
+    def drop(tab):
+        tab = tab.copy()
+        tab[2, 1] = tab[2, 300 // page] = tab[0, 0] = tab[3, 800 // page] = -1
+        return tab
+
+    K.kda_get_device_status()
+    check_attention(rng, 5, 4 * group, 4, d, page, lens, counts, dtype, tables=drop if missing else None)
+    assert K.kda_get_device_status() == (1 if missing else 0)
+
+
 def test_one_long_row_is_split():
     rng = np.random.default_rng(3)
     check_attention(rng, 2, 8, 1, 128, 64, [20000, 1], [1, 1], "fp16", cu=False)
