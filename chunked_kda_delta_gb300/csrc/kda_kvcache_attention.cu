@@ -528,15 +528,23 @@ int resident_cols(int cols) {
 
 }  // namespace
 
-// Query rows of an item: 8 or 16 where they hold one row's (token, head) pairs, else 128 on
-// tcgen05.  Items of 32 rows here, against tcgen05, with 24 or 32 pairs a row and 4 key/value
-// heads: 64 rows of 4096 tokens 87 against 67 us (head_dim 64) and 129 against 108 (128), 16 rows
-// of 4096 tokens 36 against 31 and 46 against 43, only 4 rows of 1000 tokens 15 against 22 and
-// 20 against 25.  With 16 pairs and 64 rows of 4096 tokens items of 16 take 52 and 66 us.
-constexpr int kFewRows = 16;
-int attention_cols(int64_t tokens, int32_t rows, int32_t group) {
-    const int64_t each = (tokens + rows - 1) / rows * group;
-    return each <= 8 ? 8 : each <= kFewRows ? 16 : kBlockRows;
+// Query rows of an item: 8 where they hold a row's (token, head) pairs, 16 up to kFewRows pairs or
+// where the call is small, else 128 on tcgen05.  Items of 16 against items of 128, us for rows,
+// key/value heads and tokens cached at most (a third of it and more): 32 pairs, 16 rows, 4 heads, 2000:
+// 20 against 24 (head_dim 64), 24 against 31 (128); 64, 4, 500: 22 / 22, 32 / 35; 1, 8, 30000: 28 / 28,
+// 40 / 47.  48 pairs, 64, 4, 500: 24 / 23, 36 / 35; 1, 8, 30000: 40 / 28, 50 / 47.  Small
+// calls, with two warps for an item of 16 and at most 256 keys of an item for a warp: 128 pairs, 4, 8,
+// 500: 12 / 15, 19 / 21; 96 pairs, 16, 4, 500: 16 / 18, 23 / 27; 128 pairs, 1, 1, 30000: 22 / 22, 25 / 28; with
+// more items than that 64 pairs, 111, 2, 40: 14 / 11, 25 / 16.  (Of the cached tokens the host knows what
+// the tables have places for.)
+constexpr int kFewRows = 32, kFewKeys = 256;
+int attention_cols(const CacheParams& c, int32_t group, int sm_count) {
+    const int64_t each = (c.tokens + c.rows - 1) / c.rows * group;
+    if (each <= 8) return 8;
+    const int64_t items = (c.tokens * group / 16 + c.rows) * c.heads, keys = (int64_t)c.width * c.page_tokens;
+    const int64_t warps = 2ll * kWarps * sm_count;
+    const bool small = items <= warps / 2 && items * keys <= kFewKeys * warps;
+    return each <= kFewRows || small ? 16 : kBlockRows;
 }
 
 size_t attention_slots(int ctas) { return (size_t)2 * ctas * kWarps; }

@@ -138,7 +138,7 @@ struct AttentionParams {
     int32_t ctas, sm_count;
 };
 size_t attention_slots(int ctas);
-int attention_cols(int64_t tokens, int32_t rows, int32_t group);
+int attention_cols(const CacheParams& c, int32_t group, int sm_count);
 int attention_ctas(int32_t dim, int cols, bool f16, int sm_count);
 cudaError_t launch_attention(const AttentionParams& p, int cols, bool f16, cudaStream_t stream);
 // Items of 128 query rows on tcgen05 (kda_kvcache_block.cu): two CTAs an SM, two parts each.

@@ -410,9 +410,9 @@ kda_status kda_kvcache_attention(const kda_kvcache* cache, const void* q, int32_
         if ((st = current_device(&dev, &di)) != KDA_OK) return st;
         if (num_tokens == 0) return KDA_OK;
         const bool f16 = act_dtype == KDA_ACT_F16;
-        const int cols = kda::attention_cols(num_tokens, cache->rows, group);
         kda::AttentionParams p{};
         p.c = cache_params(cache, num_tokens, lens, cu_tokens, di->status);
+        const int cols = kda::attention_cols(p.c, group, di->sm_count);
         p.sm_count = di->sm_count;
         p.ctas = kda::attention_ctas(cache->head_dim, cols, f16, di->sm_count);
         const size_t parts = (cols == kda::kBlockRows ? (size_t)2 * p.ctas : kda::attention_slots(p.ctas)) * cols;
