@@ -19,9 +19,9 @@
 //
 // q is scaled by a power of two per row so that its largest magnitude is in [2^14, 2^15) and
 // becomes fp16 without loss (bf16 has fewer bits; what falls below fp16's range is 2^-38 of the
-// largest).  Softmax weights are fp16 relative to the running maximum; each page's v scale
-// enters as its ratio to the largest one met, so weights stay in [0, 1].  Running maximum,
-// sums, outputs and the joined parts are fp32.
+// largest).  Weights times their page's v scale are fp16 relative to the running maximum of
+// that product, so they stay in [0, 1]; the sum of the weights divides the scale out again by
+// blocks of 16 keys.  Running maximum, sums, outputs and the joined parts are fp32.
 //
 // Work split: warps work alone.  The items' cached tokens, cut into slabs, are numbered
 // through all items; every resident warp takes an equal contiguous share, however long the rows
@@ -63,13 +63,6 @@ __device__ __forceinline__ int row_slabs(int len) {
     constexpr int kKeys = kSlabKeys<kDim>;
     return len > kKeys ? (len + kKeys - 1) / kKeys : 1;
 }
-// 2^x by the hardware's instruction (results below 2^-126 are 0).
-__device__ __forceinline__ float exp2_fast(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // Codes of 16 keys, widened, against the query rows: acc += K Q^T.  q(step, nt) gives the two
 // registers of a reduction step.
 template <int kHalves, int kNT, typename Q>
@@ -202,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(c
                 factor[nt][i] = __shfl_sync(0xffffffffu, q_scale[nt], (2 * t + i) * 4);
             }
 
-        float o[kNT][kMT][4], m[kNT][2], l[kNT][2], ref = 0.f;
+        float o[kNT][kMT][4], m[kNT][2], l[kNT][2];
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
             m[nt][0] = m[nt][1] = kNegInf;
@@ -212,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(c
         }
 
         auto scale_of = [&](const float* scales, int32_t page) { return page < 0 ? 0.f : scales[(int64_t)page * c.heads + head]; };
-        float k_scales = scale_of(c.k_scale, pages), v_scales = scale_of(c.v_scale, pages);
+        float k_scales = scale_of(c.k_scale, pages), v_logs = scale_log2(scale_of(c.v_scale, pages));
         int b0 = slab0 * kBlk;  // block of lane 0
 
         uint4 kr[kBlk][2][kHalves];  // [16 keys][key g, g + 8][channel half]
@@ -268,13 +261,13 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(c
         }
         if (slab1 - slab0 > kBatch) pages_next = page_at(b0 + 32 + lane);
         for (int slab = slab0; slab < slab1; ++slab) {
-            float ks[kBlk], vs[kBlk];
+            float ks[kBlk], lv[kBlk];
             bool missing = false;
 #pragma unroll
             for (int i = 0; i < kBlk; ++i) {
                 const int from = slab * kBlk + i - b0;
                 ks[i] = __shfl_sync(0xffffffffu, k_scales, from);
-                vs[i] = __shfl_sync(0xffffffffu, v_scales, from);
+                lv[i] = __shfl_sync(0xffffffffu, v_logs, from);
                 missing |= __shfl_sync(0xffffffffu, pages, from) < 0;
             }
             const int32_t pages_now = pages;
@@ -291,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(c
                 if ((slab + 1) * kBlk - b0 == 32) {
                     pages = pages_next;
                     k_scales = scale_of(c.k_scale, pages);
-                    v_scales = scale_of(c.v_scale, pages);
+                    v_logs = scale_log2(scale_of(c.v_scale, pages));
                     b0 += 32;
                     if ((b0 + 32) / kBlk < slab1) pages_next = page_at(b0 + 32 + lane);
                 }
@@ -300,11 +293,6 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(c
 
             const int key0 = slab * kKeys;
             const bool edge = key0 + kKeys > seen_min || missing;
-            float ref_new = ref;
-#pragma unroll
-            for (int i = 0; i < kBlk; ++i) ref_new = fmaxf(ref_new, vs[i]);
-            const float ref_inv = ref_new > 0.f ? 1.f / ref_new : 0.f, shrink = ref * ref_inv;
-            ref = ref_new;
             uint32_t pf[kBlk][kNT][2];
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt) {
@@ -315,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(c
                     const bool gone = edge && __shfl_sync(0xffffffffu, pages_now, slab * kBlk + i - b_now) < 0;
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        float y = sc[i][nt][x] * fk[x & 1];
+                        float y = fmaf(sc[i][nt][x], fk[x & 1], lv[i]);
                         if (edge && (gone || key0 + 16 * i + g + 8 * (x >> 1) >= seen[nt][x & 1])) y = kNegInf;
                         sc[i][nt][x] = y;
                         top[x & 1] = fmaxf(top[x & 1], y);
@@ -335,25 +323,23 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(c
                 }
 #pragma unroll
                 for (int i = 0; i < kBlk; ++i) {
-                    const float wv = vs[i] * ref_inv;
+                    const float iv = exp2_fast(-lv[i]);
                     float e[4];
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
                         e[x] = exp2_fast(sc[i][nt][x] - top[x & 1]);
-                        l[nt][x & 1] += e[x];
-                        e[x] *= wv;
+                        l[nt][x & 1] += e[x] * iv;
                     }
                     pf[i][nt][0] = transpose8x8(pack_half2(e[0], e[1]));
                     pf[i][nt][1] = transpose8x8(pack_half2(e[2], e[3]));
                 }
-                const float f0 = fix[0] * shrink, f1 = fix[1] * shrink;
-                if (__any_sync(0xffffffffu, f0 != 1.f || f1 != 1.f)) {
+                if (__any_sync(0xffffffffu, fix[0] != 1.f || fix[1] != 1.f)) {
 #pragma unroll
                     for (int j = 0; j < kMT; ++j) {
-                        o[nt][j][0] *= f0;
-                        o[nt][j][1] *= f1;
-                        o[nt][j][2] *= f0;
-                        o[nt][j][3] *= f1;
+                        o[nt][j][0] *= fix[0];
+                        o[nt][j][1] *= fix[1];
+                        o[nt][j][2] *= fix[0];
+                        o[nt][j][3] *= fix[1];
                     }
                 }
             }
@@ -389,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(c
                 for (int col = 0; col < 2; ++col) {
                     const int f = row0 + nt * 8 + 2 * t + col;
                     if (f >= rows_all) continue;
-                    const float by = l[nt][col] > 0.f ? ref / l[nt][col] : 0.f;
+                    const float by = l[nt][col] > 0.f ? 1.f / l[nt][col] : 0.f;
                     T* out = static_cast<T*>(p.out) + (begin + f / group) * p.out_stride + (int64_t)(head * group + f % group) * kDim + kVWords * 4 * g;
 #pragma unroll
                     for (int j = 0; j < kMT; ++j)
@@ -399,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(c
                 float4* part = reinterpret_cast<float4*>(p.part_o) + (slot * kNT + nt) * kMT * 32 + lane;
 #pragma unroll
                 for (int j = 0; j < kMT; ++j)
-                    part[32 * j] = make_float4(o[nt][j][0] * ref, o[nt][j][1] * ref, o[nt][j][2] * ref, o[nt][j][3] * ref);
+                    part[32 * j] = make_float4(o[nt][j][0], o[nt][j][1], o[nt][j][2], o[nt][j][3]);
                 if (g == 0)
                     reinterpret_cast<float4*>(p.part_ml)[(slot * kNT + nt) * 4 + t] = make_float4(m[nt][0], l[nt][0], m[nt][1], l[nt][1]);
             }

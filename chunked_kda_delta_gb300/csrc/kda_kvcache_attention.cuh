@@ -71,6 +71,18 @@ __device__ __forceinline__ int row_tokens(const CacheParams& c, int r, int64_t& 
     if (r == c.rows - 1 && end != c.tokens) report(c.status, kStatusBadSeqlens);
     return (int)(end - begin);
 }
+// log2 of a page's v scale.  Softmax weights carry the scale of their v in the exponent, and what is
+// largest of weight and scale together is the reference: so a weight's rounding to fp16 is relative
+// to the row's largest contributions, whatever the scales.  Below 2^-100 (0: its codes are 0) it does
+// not matter.
+__device__ __forceinline__ float scale_log2(float v) { return log2f(fmaxf(v, 0x1p-100f)); }
+// 2^x by the hardware's instruction (results below 2^-126 are 0).
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Cached tokens of row r that its table has places for.
 __device__ __forceinline__ int row_length(const CacheParams& c, int r) {
     const int len = c.lens[r];

@@ -15,10 +15,9 @@
 // everything, two threads a row, took 4300 cycles a tile: 1000 of them issuing, the rest
 // waiting for each other at three barriers; 159 us instead of 88 for 8 pieces of up to 512
 // tokens, 16 heads of 64 over 4, 4096 cached.)
-// O is rescaled only when a row's maximum has grown by more than 2^8 (or a page's v scale by
-// more than 2^4) over the one in use: weights stay below 2^12 in fp16 and the sums are the
-// same.  The v scale enters the exponent, weights p vs / ref, and leaves the sum again by blocks
-// of 16 keys.  The bound is the softmax's instructions, about four a score.
+// O is rescaled only when a row's maximum has grown by more than 2^8 over the one in use: weights
+// stay below 2^8 in fp16 and the sums are the same.  The v scale enters the exponent, also for the
+// maximum, and leaves the sum again by blocks of 16 keys.  The bound is the softmax's instructions, about four a score.
 //
 // Work split as in kda_kvcache_attention.cu, by tiles that are seen: the CTAs (two an SM) take
 // equal contiguous shares of all tiles of all items, and the parts are joined by a second launch.
@@ -40,12 +39,6 @@ constexpr uint32_t kColS = 0, kColO = 128, kColumns = 256;  // tensor memory: S 
 constexpr int64_t kWaitLimit = 1ll << 20;
 // Two CTAs an SM and no third: the tensor memory is for two.
 constexpr size_t kSmemBytes = 80 * 1024;
-
-__device__ __forceinline__ float exp2_fast(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 // Two floats side by side: one instruction for both.
 __device__ __forceinline__ uint64_t pair(float a, float b) {
@@ -124,7 +117,7 @@ struct alignas(16) SplitItem {
     int begin, n, head, block, slot, last, unused[2];  // first token and tokens of its row; slot of its first part
 };
 
-struct Meta {  // scales of 16 keys; k negative where the page is missing
+struct Meta {  // scales of 16 keys, of v in shared memory its log2; k negative where the page is missing
     float k, v;
 };
 
@@ -320,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
             commit_one(bar_o);
         };
 
-        float m = kNegInf, l = 0.f, ref = 0.f, ref_inv = 0.f;
+        float m = kNegInf, l = 0.f;
         if (!soft) {
             // This warp's 16 keys of each tile lie in one page.  Load number i of a lane: key
             // 8 (i % 2) + lane % 8, channels 16 (4 (i / 2) + lane / 8).
@@ -364,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
                     *reinterpret_cast<uint4*>(dst + kLbo) = hi;
                 }
                 if (lane == 0) {
-                    s_meta[tile & 3][mine] = meta;
+                    s_meta[tile & 3][mine] = Meta{meta.k, scale_log2(meta.v)};
                     mbar_arrive(bar_of(tile - tile0));
                 }
                 fence_proxy_async_smem();
@@ -433,12 +426,10 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
                 tmem_ld32(t_s, sr);
                 tmem_ld32(t_s + 32, sr + 32);
                 Meta meta[kBlocks];
-                float top_v = 0.f;
                 bool missing = false;
 #pragma unroll
                 for (int x = 0; x < kBlocks; ++x) {
                     meta[x] = s_meta[tile & 3][x];
-                    top_v = fmaxf(top_v, meta[x].v);
                     missing |= meta[x].k < 0.f;
                 }
                 tmem_wait_ld_regs<kKeys>(sr);
@@ -459,27 +450,19 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
                         z = max3(z, __uint_as_float(sr[16 * x + i + 2]), __uint_as_float(sr[16 * x + i + 3]));
                     }
                     y = fmaxf(max3(y, z, __uint_as_float(sr[16 * x + 14])), __uint_as_float(sr[16 * x + 15]));
-                    top = fmaxf(top, y == kNegInf ? kNegInf : y * (meta[x].k * factor));  // (a scale of 0 makes scores 0)
+                    top = fmaxf(top, y == kNegInf ? kNegInf : fmaf(y, meta[x].k * factor, meta[x].v));  // (a scale of 0 makes scores 0)
                 }
-                // References of the weights: this row's maximum, the pages' largest v scale.
+                // The reference of the weights.
                 const float m_new = top > m + kGrowth || m == kNegInf ? fmaxf(m, top) : m;
                 const float m_use = m_new == kNegInf ? 0.f : m_new;
                 const float fix = m == kNegInf ? (m_new == kNegInf ? 1.f : 0.f) : exp2_fast(m - m_use);
-                float fix_o = fix;
-                if (top_v > 16.f * ref) {
-                    ref_inv = 1.f / top_v;
-                    fix_o *= ref * ref_inv;
-                    ref = top_v;
-                }
                 m = m_new;
                 l *= fix;
 #pragma unroll
                 for (int x = 0; x < kBlocks; ++x) {
-                    // Weight times wv = vs / ref, 1 where vs is 0 (its codes were not loaded).  A
-                    // factor of 0 must not make masked scores NaN.
+                    // (A factor of 0 must not make masked scores NaN.)
                     const float k = meta[x].k * factor > 0.f ? meta[x].k * factor : 0x1p-126f;
-                    const float wv = meta[x].v > 0.f ? meta[x].v * ref_inv : 1.f;
-                    const float bias = __log2f(wv) - m_use;
+                    const float bias = meta[x].v - m_use;
                     const uint64_t k2 = pair(k, k), bias2 = pair(bias, bias);
                     uint64_t acc[2] = {0, 0};  // (+0, +0)
 #pragma unroll
@@ -493,19 +476,19 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
                     }
                     float sum[2];
                     unpair(add2(acc[0], acc[1]), sum[0], sum[1]);
-                    l += (sum[0] + sum[1]) * __fdividef(1.f, wv);
+                    l += (sum[0] + sum[1]) * exp2_fast(-meta[x].v);
                 }
                 if (tile > tile0) {  // O += P V of the tile before is done
                     wait_o();
                     tc_fence_after();
-                    if (__any_sync(0xffffffffu, fix_o != 1.f)) {
+                    if (__any_sync(0xffffffffu, fix != 1.f)) {
 #pragma unroll
                         for (int q = 0; q < kDim; q += 16) {
                             uint32_t o[16];
                             tmem_ld16(tmem + kColO + lanes + q, o);
                             tmem_wait_ld_regs<16>(o);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fix_o);
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fix);
                             tmem_st8(tmem + kColO + lanes + q, *reinterpret_cast<uint32_t(*)[8]>(o));
                             tmem_st8(tmem + kColO + lanes + q + 8, *reinterpret_cast<uint32_t(*)[8]>(o + 8));
                         }
@@ -524,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
         const int64_t slot = 2 * (int64_t)blockIdx.x + (w == w_begin ? 0 : 1);
         if (tid == 0 && w == item && item_end > w_end)
             reinterpret_cast<SplitItem*>(p.split_items)[blockIdx.x] = SplitItem{(int)begin, n, head, block, (int)slot, (int)((item_end - 1) / per), 0, 0};
-        const float by = whole ? (l > 0.f ? ref / l : 0.f) : ref;
+        const float by = l > 0.f ? 1.f / l : 0.f;
         T* out = static_cast<T*>(p.out) + (begin + (there ? f / group : 0)) * p.out_stride +
                  (int64_t)(head * group + (there ? f % group : 0)) * kDim;
         if (!whole && soft) {
@@ -554,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
                 }
             } else {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) p.part_o[(slot * kDim + q + i) * kRows + tid] = __uint_as_float(o[i]) * by;
+                for (int i = 0; i < 16; ++i) p.part_o[(slot * kDim + q + i) * kRows + tid] = __uint_as_float(o[i]);
             }
         }
         tc_fence_before();

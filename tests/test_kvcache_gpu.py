@@ -119,6 +119,39 @@ def test_pieces_of_prompts(d, page, group, dtype, missing):
     assert K.kda_get_device_status() == (1 if missing else 0)
 
 
+@pytest.mark.parametrize("d,hq", [(64, 16), (128, 24)])
+@pytest.mark.parametrize("n", [1, 300])
+def test_scales_and_scores_far_apart(d, hq, n):
+    # references of the weights that grow along the keys: rows' maxima by far more than 2^8, v's scales
+    # by orders of magnitude, scales of zero; for single tokens and for pieces of prompts.  A weight p vs
+    # that leaves fp16's normal range is off by up to 2^-25 of the row's largest one.
+    rng = np.random.default_rng(1000 * n + d)
+    counts, lens = [n, n], [640, 999]
+    kc, vc, ks, vs, tab = make_cache(rng, 2, 4, 16, d, lens)
+    ks *= rng.uniform(0, 3, ks.shape).astype(np.float32)
+    vs *= (10.0 ** rng.integers(-6, 6, vs.shape)).astype(np.float32)
+    vs[tab[0, 0]] = vs[tab[1, 50]] = 0
+    ks[tab[1, 3]] = 0
+    q = torch.as_tensor(rng.standard_normal((2 * n, hq, d)) * 3).to(torch.bfloat16)
+    want, weight = ref.attention(q.double().numpy(), kc, vc, ks, vs, tab, lens, counts, 16, 0.125)
+    got = K.kda_kvcache_attention(q.cuda(), *gpu_cache(kc, vc, ks, vs, tab), torch.tensor(lens, dtype=torch.int32).cuda(),
+                                  cu_tokens=cu_of(counts), scale=0.125).double().cpu().numpy()
+    below = np.zeros_like(want)
+    for r in range(2):
+        ids = tab[r, : -(-lens[r] // 16)]
+        k, v = (ref.E4M3[c[ids]].transpose(1, 0, 2, 3).reshape(4, -1, d)[:, : lens[r]] for c in (kc, vc))
+        sk, sv = (np.repeat(x[ids].T.astype(np.float64), 16, 1)[:, : lens[r]] for x in (ks, vs))
+        for i in range(n):
+            p = lens[r] - n + i + 1
+            for h in range(hq):
+                g = h * 4 // hq
+                z = 0.125 * (k[g, :p] @ q[r * n + i, h].double().numpy()) * sk[g, :p]
+                w = np.exp(z - z.max())
+                below[r * n + i, h] = 2.0 ** -25 * (w * sv[g, :p]).max() / w.sum() * np.abs(v[g, :p]).sum(0)
+    assert np.isfinite(got).all()
+    assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -10 * weight + below + 1e-6).all()
+
+
 def test_one_long_row_is_split():
     rng = np.random.default_rng(3)
     check_attention(rng, 2, 8, 1, 128, 64, [20000, 1], [1, 1], "fp16", cu=False)
