@@ -5,7 +5,7 @@
 // makes one call of the C ABI in include/kda.h on the given or the current stream; all of the
 // computation is in that call's kernels.  A decoding step makes these calls many times
 // for a few microseconds of GPU work each: with the same checks in Python and ctypes calls in a
-// row took 13 to 34 us each, most of it in the interpreter; here 6 to 18 (GB300).
+// row took 13 to 34 us each, most of it in the interpreter; here 4 to 9, or what the GPU takes.
 #include <Python.h>
 
 #include <ATen/EmptyTensor.h>

@@ -9,7 +9,7 @@
 // (k + 1)-th largest of the groups' maxima is not above the segment's (k + 1)-th largest value.
 // (Groups of neighbouring lanes of one warp are empty in short segments, the last of most
 // rows: without a bound all of their values are candidates, too many for the buffer, and the
-// rounds that are left then took 40 us for 16 beams of 1326 or 9077 logits instead of 9.)  Only the steps of lanes
+// rounds that are left then took 40 us for 16 beams of 1326 or 9077 logits instead of 10.)  Only the steps of lanes
 // whose noted maximum reaches that bound are read again, a few dozen bytes each and little
 // more than k + 1 of them, and their values that reach it are the candidates.  (Keeping sorted
 // lists while streaming, with a bound that rises, took 12 us more on 256 rows of 131072: some

@@ -11,9 +11,9 @@
 // (IBM J. Res. Dev. 34, 1990): q = rn(x r), then rn(q + rn(x - q s) r) is the correctly rounded
 // x / s wherever no intermediate leaves the normal range and s's fraction is not all
 // ones -- three operations a value instead of a full division (86 us for 30.7k tokens of 8
-// heads with divisions, where instructions and not bytes were the bound; now 35, 0.80 of its bytes
-// at the copy rate, with 69% of the issue slots taken).  Other scales, and blocks with values that
-// are not finite, take the division.  One token of 256 rows, 8 heads: 4.8 us, a launch and a chain of
+// heads with divisions, where instructions and not bytes were the bound; now 34, 0.81 of its bytes
+// at the copy rate, with 71% of the issue slots taken).  Other scales, and blocks with values that
+// are not finite, take the division.  One token of 256 rows, 8 heads: 5.1 us, a launch and a chain of
 // dependent loads.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

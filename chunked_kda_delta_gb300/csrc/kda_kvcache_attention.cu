@@ -1,5 +1,6 @@
 // kda_kvcache_attention.cu -- causal attention over the 8-bit paged cache, for one or a few
-// new tokens a row (up to 16 query rows for a key/value head; kda_kvcache_block.cu takes more).
+// new tokens a row (up to 32 query rows for a key/value head, and small calls with more;
+// kda_kvcache_block.cu takes the others).
 //
 // Query rows (token, query head of a group) that share a key/value head go through the cache
 // together: an item is kCols = 8 kNT such rows of one (row, key/value head), so the codes are
@@ -30,8 +31,8 @@
 // and joining in shared memory at every item's end the loads paused there: 147 us instead of
 // 133 for 64 rows of up to 8192 tokens, 8 heads.  Asking L2 for codes two to eight slabs ahead
 // made it 1 to 35% slower, slabs of 16 keys with four CTAs an SM 5%, two CTAs without spills
-// 10%.)  Bound by HBM: that call takes 126 us, 0.84 of its bytes at the copy rate (718 MB), the join
-// and its tail with it; 4 rows of up to 131072 tokens, 4 heads, 68 us, 0.78; one row of 1000
+// 10%.)  Bound by HBM: that call takes 125 us, 0.85 of its bytes at the copy rate (718 MB), the join
+// and its tail with it; 4 rows of up to 131072 tokens, 4 heads, 67 us, 0.78; one row of 1000
 // tokens 8 us, two launches' latency.
 #include "kda_kvcache_attention.cuh"
 

@@ -11,13 +11,17 @@
 // Four warps do the softmax, four read and widen codes (each the tile's 16 keys of one page), the
 // first of which issues the matrix instructions as well (a ninth warp for that left 96 registers
 // a thread and spills); two CTAs an SM.  S(j + 1) is computed and V(j) widened while the softmax
-// of tile j runs.  (One kind of warps for
-// everything, two threads a row, took 4300 cycles a tile: 1000 of them issuing, the rest
-// waiting for each other at three barriers; 159 us instead of 88 for 8 pieces of up to 512
-// tokens, 16 heads of 64 over 4, 4096 cached.)
+// of tile j runs.  (One kind of warps for everything, two threads a row, took 4300 cycles a tile:
+// 1000 of them issuing, the rest waiting for each other at three barriers; 159 us instead of 87 for 8 pieces of up to 512
+// tokens, 16 heads of 64 over 4, 4096 cached.  Eight widening warps: 102; two softmax groups: 105
+// and 108.)
 // O is rescaled only when a row's maximum has grown by more than 2^8 over the one in use: weights
 // stay below 2^8 in fp16 and the sums are the same.  The v scale enters the exponent, also for the
-// maximum, and leaves the sum again by blocks of 16 keys.  The bound is the softmax's instructions, about four a score.
+// maximum, and leaves the sum again by blocks of 16 keys.
+//
+// Bound by issue and latency: a tile takes each of an SM's two CTAs 2700 cycles (head_dim 128: 4700),
+// nearly all of them work of both kinds of warps, 55% of the issue slots and 21% of the tensor
+// cores' cycles.  The call above takes 87 us, 397 TFLOP/s; with heads of 128 151 us, 458.
 //
 // Work split as in kda_kvcache_attention.cu, by tiles that are seen: the CTAs (two an SM) take
 // equal contiguous shares of all tiles of all items, and the parts are joined by a second launch.

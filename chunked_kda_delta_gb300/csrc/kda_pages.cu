@@ -12,10 +12,10 @@
 // memory.  Free pages are handed out lowest first to entries in row-major order, from prefix
 // sums over contiguous ranges, so the result does not depend on the order in which CTAs or
 // atomics run (the atomics add whole numbers and take minima).  A fork of 128 rows of a cache takes
-// 14.7 us with its copies (10 MB); with one CTA up to 16384 entries it was 57.
+// 14.3 us with its copies (10 MB); with one CTA up to 16384 entries it was 57.
 //
 // The copies are bound by HBM: a fork that copies states of 64 KiB (402 MB read and written) takes
-// 72 us, 54 of them the copies (0.83 of the copy rate with the plan), compaction of a cache 56 us
+// 70 us, 54 of them the copies (0.84 of the copy rate with the plan), compaction of a cache 55 us
 // (292 MB, 0.77).
 #include <cooperative_groups.h>
 #include <limits.h>

@@ -3,9 +3,9 @@ beam selection (``include/kda.h``).
 
 Thin wrappers of the extension ``_build/_kda_serving.so``, which checks the tensors, allocates what
 is returned and calls the C ABI, asynchronously on the given (or current) stream; every step runs
-in the library's CUDA kernels and there is no fallback.  Calls in a row, each of them bound by the
-host: appending one token to 256 rows 6.2 us, a selection of 4 from 4 beams 10.3, a fork of a
-cache's tables 18.4 (GB300); with this marshalling in Python and ctypes 13.0, 25.3 and 33.9.
+in the library's CUDA kernels and there is no fallback.  Calls in a row: appending one token to 256
+rows 5.2 us, a selection of 4 from 4 beams 8.2, a fork of a cache's tables 14.7 (GB300); with this
+marshalling in Python and ctypes, where the host was the bound, 13.0, 25.3 and 33.9.
 What only a kernel can see (page numbers out of range, too few free pages, values that are not
 finite) goes to the device status word: :func:`~.kda.kda_get_device_status`.
 """
