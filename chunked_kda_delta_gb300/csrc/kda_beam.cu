@@ -22,9 +22,11 @@
 // by counting larger keys needs no sort and ties go to the lowest index.
 //
 // Sums are relative to 2^c with whole c, so exp2(x log2 e - c) takes one fused multiply-add and
-// the reference is exact.  Logits of 1e30 and more (the type's lowest value as a mask) have
-// a sum of their own, relative to their maximum; steps with such logits, NaN or
-// infinities take a slower path.
+// the reference is exact.  c is made from the rounded product, which for |x| below 2^30 is off by up to
+// 2^6: terms stay below 2^65.  Logits of 2^30 and more (large numbers and the type's lowest value as
+// masks) have a sum of their own, relative to their maximum; steps with such logits, NaN
+// or infinities take a slower path.  One of 2^30 and more is at least 64 away from the largest of
+// the others: the lower of the two sums does not count.
 //
 // Ranking by totals, not logits: within a row larger logits give totals that are not
 // smaller, but rounding can make totals equal whose logits differ, and then the lower index
@@ -46,7 +48,7 @@ constexpr int kLoads = 4;     // 16-byte loads of a lane and step
 constexpr int kMaxSteps = 16; // of a warp
 constexpr float kNegInf = -INFINITY;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kHuge = 1e30f;
+constexpr float kHuge = 0x1p30f;
 
 // 2^x by the hardware's instruction (results below 2^-126 are 0, which sums of a largest
 // term near 1 do not notice).
@@ -561,9 +563,10 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamParam
             huge += __shfl_xor_sync(0xffffffffu, huge, o);
         }
         // Huge logits matter alone, or where they are positive.  With no finite logit at all
-        // there are no candidates either.
+        // there are no candidates either.  (The scan's rounded factor is divided out again, not
+        // log2 e: they differ by 1.3e-8 of a logit, 13 for one of 1e9.)
         if (lane == 0)
-            lse[w] = h > 0.f || c == kNegInf ? h + logf(huge) : (float)(((double)c + log2f(sum)) * 0.6931471805599453);
+            lse[w] = h > 0.f || c == kNegInf ? h + logf(huge) : (float)(((double)c + log2f(sum)) * (1.0 / (double)kLog2e));
     }
     __syncthreads();
 

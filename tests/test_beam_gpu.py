@@ -150,3 +150,33 @@ def test_selection_feeds_the_fork():
     tables = torch.arange(b * w, device="cuda", dtype=torch.int32).view(-1, 1)
     nt, nr = K.kda_pages_fork(tables, torch.ones(b * w, dtype=torch.int32, device="cuda"), parents.view(-1), pools=[pool])
     assert torch.equal(pool[nt[:, 0].long()], before[parents.view(-1).long()]) and (nr == 1).all()
+
+
+LARGE = [1e9, 1e10, 1e12, 1e20, 1e29]
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("size", LARGE)
+def test_masks_of_large_numbers(size, dtype):
+    # as additive masks have them: over whole loads of most lanes, in the last row over all of it (its
+    # totals are then its score: fp32 does not hold the logarithm of the count beside such numbers)
+    rng = np.random.default_rng(9)
+    x = draw(rng, 2, 3, 9000)
+    x[:, :, 40:8000] = -size
+    x[1, 2] = -size
+    check(x, scores_of(rng, 2, 3), k=7, dtype=dtype)
+    x[:, :, 9:] = -size  # fewer others than places
+    check(x, scores_of(rng, 2, 3), k=40, dtype=dtype)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("size", LARGE)
+def test_large_logits(size, dtype):
+    rng = np.random.default_rng(10)
+    x = draw(rng, 2, 2, 9000)
+    x[0, 0, [70, 4000]] = size, size * 1.5
+    x[0, 1, 8999] = size
+    x[1, 0, 500:] = size
+    x[1, 1, 3:] = -size
+    x[1, 1, 3000] = -size * 0.5
+    check(x, scores_of(rng, 2, 2), k=9, dtype=dtype)
