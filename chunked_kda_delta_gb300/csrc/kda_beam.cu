@@ -30,8 +30,10 @@
 //
 // Ranking by totals, not logits: within a row larger logits give totals that are not
 // smaller, but rounding can make totals equal whose logits differ, and then the lower index
-// wins.  The (k + 1)-th key of a segment bounds what the segment left out; if the next
-// smaller logit would still reach the k-th best total, beam_join reads that segment again.
+// wins.  The (k + 1)-th key of a segment, its edge, bounds what the segment left out: the edge's
+// logit at higher indexes, and smaller logits anywhere.  If the edge's logit at the next index, or the
+// next smaller logit at any, would come before the k-th best total, beam_join reads that
+// segment again.
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -608,9 +610,9 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamParam
             const int w = (list0 + tid) / p.segs;
             const uint64_t edge = done[w] ? 0 : list0 == 0 ? edge0 : cand[(list0 + tid) * c1 + p.k];
             if (edge) {  // else nothing was left out
-                const uint64_t could = total_key(w, next_below<T>(key_value(edge)), 0);
-                // Whatever its index, it may come before the last.
-                if (could && (could | 0xffffffffu) > best[p.k - 1]) again[atomicAdd(&agains, 1)] = list0 + tid;
+                const uint64_t last = best[p.k - 1], same = total_key(w, key_value(edge), key_index(edge) + 1);
+                const uint64_t could = total_key(w, next_below<T>(key_value(edge)), 0);  // whatever its index
+                if (same > last || (could && (could | 0xffffffffu) > last)) again[atomicAdd(&agains, 1)] = list0 + tid;
             }
         }
         __syncthreads();

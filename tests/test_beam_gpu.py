@@ -180,3 +180,27 @@ def test_large_logits(size, dtype):
     x[1, 1, 3:] = -size
     x[1, 1, 3000] = -size * 0.5
     check(x, scores_of(rng, 2, 2), k=9, dtype=dtype)
+
+
+@pytest.mark.parametrize("dtype,score", [("bf16", -1e6), ("fp16", -1e5)])
+def test_equal_totals_of_logits_a_step_apart(dtype, score):
+    # two tokens a step of the type above two of lower index, all four totals equal in fp32 and the
+    # next smaller logit's below them: the two of lower index win, the second of which a segment that
+    # keeps three candidates left out.  (Values are searched whose totals are no closer than a tenth of
+    # the scores' spacing to where fp32 rounds the other way.)
+    gap = float(np.spacing(np.float32(-score)))
+    step = {"bf16": 2.0 ** -5, "fp16": 2.0 ** -8}[dtype]  # of the type in [4, 8)
+    rng = np.random.default_rng(11)
+    found = 0
+    for low in np.arange(4 + step, 8 - 2 * step, step):
+        x = draw(rng, 1, 1, 4000) / 4
+        x[0, 0, [500, 600]], x[0, 0, [800, 900]] = low, low + step
+        lse = np.log(np.exp(x[0, 0]).sum())
+        t = (score + np.array([low + step, low, low - step]) - lse) / gap
+        if np.abs(t - np.round(t)).max() > 0.4 or len(set(np.round(t[:2]))) > 1 or round(t[2]) == round(t[1]):
+            continue
+        found += 1
+        want = ref.beam(x, np.array([[score]], np.float32), 2)
+        assert want[1].tolist() == [[500, 600]]
+        check(x, np.array([[score]], np.float32), k=2, dtype=dtype)
+    assert found > 5
