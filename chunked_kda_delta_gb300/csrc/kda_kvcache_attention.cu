@@ -206,7 +206,9 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(c
         }
 
         auto scale_of = [&](const float* scales, int32_t page) { return page < 0 ? 0.f : scales[(int64_t)page * c.heads + head]; };
-        float k_scales = scale_of(c.k_scale, pages), v_logs = scale_log2(scale_of(c.v_scale, pages));
+        auto log_of = [&](int32_t page) { return page < 0 ? 0.f : log2f(scale_of(c.v_scale, page)); };
+        float k_scales = scale_of(c.k_scale, pages), v_logs = log_of(pages);
+        float least = kScaleLeast;  // that a log2 of v's scale counts as
         int b0 = slab0 * kBlk;  // block of lane 0
 
         uint4 kr[kBlk][2][kHalves];  // [16 keys][key g, g + 8][channel half]
@@ -270,6 +272,13 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(c
                 ks[i] = __shfl_sync(0xffffffffu, k_scales, from);
                 lv[i] = __shfl_sync(0xffffffffu, v_logs, from);
                 missing |= __shfl_sync(0xffffffffu, pages, from) < 0;
+                least = fmaxf(least, lv[i] - kScaleSpan);
+            }
+            bool low = false;
+#pragma unroll
+            for (int i = 0; i < kBlk; ++i) {
+                low |= lv[i] < least;
+                lv[i] = fmaxf(lv[i], least);
             }
             const int32_t pages_now = pages;
             const int b_now = b0;
@@ -285,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(c
                 if ((slab + 1) * kBlk - b0 == 32) {
                     pages = pages_next;
                     k_scales = scale_of(c.k_scale, pages);
-                    v_logs = scale_log2(scale_of(c.v_scale, pages));
+                    v_logs = log_of(pages);
                     b0 += 32;
                     if ((b0 + 32) / kBlk < slab1) pages_next = page_at(b0 + 32 + lane);
                 }
@@ -310,18 +319,18 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(c
                         top[x & 1] = fmaxf(top[x & 1], y);
                     }
                 }
-                float fix[2];
+                float down[2];  // log2 of what sums and outputs are rescaled by
 #pragma unroll
                 for (int col = 0; col < 2; ++col) {
 #pragma unroll
                     for (int s = 4; s <= 16; s <<= 1) top[col] = fmaxf(top[col], __shfl_xor_sync(0xffffffffu, top[col], s));
                     const float m_new = fmaxf(m[nt][col], top[col]);
                     const float m_use = m_new == kNegInf ? 0.f : m_new;
-                    fix[col] = exp2_fast(m[nt][col] - m_use);
+                    down[col] = m[nt][col] - m_use;
                     m[nt][col] = m_new;
-                    l[nt][col] *= fix[col];
                     top[col] = m_use;
                 }
+                float add[2] = {0.f, 0.f};
 #pragma unroll
                 for (int i = 0; i < kBlk; ++i) {
                     const float iv = exp2_fast(-lv[i]);
@@ -329,18 +338,36 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(c
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
                         e[x] = exp2_fast(sc[i][nt][x] - top[x & 1]);
-                        l[nt][x & 1] += e[x] * iv;
+                        add[x & 1] += e[x] * iv;
                     }
                     pf[i][nt][0] = transpose8x8(pack_half2(e[0], e[1]));
                     pf[i][nt][1] = transpose8x8(pack_half2(e[2], e[3]));
                 }
-                if (__any_sync(0xffffffffu, fix[0] != 1.f || fix[1] != 1.f)) {
+                if (__any_sync(0xffffffffu, down[0] != 0.f || down[1] != 0.f)) {
+                    const float half[2] = {exp2_fast(0.5f * down[0]), exp2_fast(0.5f * down[1])};
+                    const float fix[2] = {half[0] * half[0], half[1] * half[1]};
+                    l[nt][0] = rescaled(l[nt][0], half[0]);
+                    l[nt][1] = rescaled(l[nt][1], half[1]);
 #pragma unroll
                     for (int j = 0; j < kMT; ++j) {
                         o[nt][j][0] *= fix[0];
                         o[nt][j][1] *= fix[1];
                         o[nt][j][2] *= fix[0];
                         o[nt][j][3] *= fix[1];
+                    }
+                }
+                l[nt][0] += add[0];
+                l[nt][1] += add[1];
+            }
+            if (low) {
+#pragma unroll
+                for (int i = 0; i < kBlk; ++i) {
+                    const int32_t page = __shfl_sync(0xffffffffu, pages_now, slab * kBlk + i - b_now);
+                    const float by = exp2_fast(fminf(log_of(page) - lv[i], 0.f));
+#pragma unroll
+                    for (int nt = 0; nt < kNT; ++nt) {
+                        pf[i][nt][0] = brought_down(pf[i][nt][0], by);
+                        pf[i][nt][1] = brought_down(pf[i][nt][1], by);
                     }
                 }
             }
@@ -430,9 +457,9 @@ __global__ void __launch_bounds__(kShares > 1 ? kShares * 32 : kDim * 2) attenti
 #pragma unroll
         for (int col = 0; col < 2; ++col) {
             const float m = fmaxf(top[col], mk[col]), use = m == kNegInf ? 0.f : m;
-            const float a = exp2f(top[col] - use), b = exp2f(mk[col] - use);
+            const float ha = exp2_fast(0.5f * (top[col] - use)), hb = exp2_fast(0.5f * (mk[col] - use)), a = ha * ha, b = hb * hb;
             top[col] = m;
-            sum[col] = sum[col] * a + lk[col] * b;
+            sum[col] = rescaled(sum[col], ha) + rescaled(lk[col], hb);
             acc[col] = acc[col] * a + ok[col] * b;
             acc[2 + col] = acc[2 + col] * a + ok[2 + col] * b;
         }

@@ -71,11 +71,22 @@ __device__ __forceinline__ int row_tokens(const CacheParams& c, int r, int64_t& 
     if (r == c.rows - 1 && end != c.tokens) report(c.status, kStatusBadSeqlens);
     return (int)(end - begin);
 }
-// log2 of a page's v scale.  Softmax weights carry the scale of their v in the exponent, and what is
-// largest of weight and scale together is the reference: so a weight's rounding to fp16 is relative
-// to the row's largest contributions, whatever the scales.  Below 2^-100 (0: its codes are 0) it does
-// not matter.
-__device__ __forceinline__ float scale_log2(float v) { return log2f(fmaxf(v, 0x1p-100f)); }
+// Softmax weights carry the scale of their v in the exponent, and what is largest of weight and scale
+// together, m, is the reference: so a weight's rounding to fp16 is relative to the row's largest
+// contributions, whatever the scales.  The sum of the weights takes the scale out again, and there a
+// block counts whose contributions are nothing: 2^(s + log2 v - m) must not fall out of fp32 where
+// 2^s matters.  So in m and in the sum no block's log2 v counts as less than the largest met so far less
+// kScaleSpan (m is at most max s + that largest, and 2^-126 is 36 bits below max s then), nor as less
+// than kScaleLeast, which holds sums of 2^31 weights in fp32.  The weights for the product are
+// brought down again to what the scale is.
+constexpr float kScaleSpan = 90.f, kScaleLeast = -80.f;
+__device__ __forceinline__ uint32_t brought_down(uint32_t half2, float by) {
+    const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&half2), __float2half2_rn(by));
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+// l 2^d for d <= 0 in two steps, h = 2^(d / 2): a sum of small scales is as large as 2^125, and 2^d alone
+// may lie below fp32's range.
+__device__ __forceinline__ float rescaled(float l, float h) { return l * h * h; }
 // 2^x by the hardware's instruction (results below 2^-126 are 0).
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;

@@ -121,7 +121,7 @@ struct alignas(16) SplitItem {
     int begin, n, head, block, slot, last, unused[2];  // first token and tokens of its row; slot of its first part
 };
 
-struct Meta {  // scales of 16 keys, of v in shared memory its log2; k negative where the page is missing
+struct Meta {  // scales of 16 keys, of v in shared memory its log2 (-inf for 0); k negative where the page is missing
     float k, v;
 };
 
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
             };
             auto meta_of = [&](int32_t page) {
                 const int64_t at = (int64_t)max(page, 0) * c.heads + head;
-                return page < 0 ? Meta{-1.f, 0.f} : Meta{c.k_scale[at], c.v_scale[at]};
+                return page < 0 ? Meta{-1.f, 1.f} : Meta{c.k_scale[at], c.v_scale[at]};
             };
             // What no row sees, and V of a scale of 0, is to leave no trace: zero.
             auto load = [&](uint4 (&raw)[kLoads], const uint8_t* codes, int tile, int32_t page, int keys) {
@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
                     *reinterpret_cast<uint4*>(dst + kLbo) = hi;
                 }
                 if (lane == 0) {
-                    s_meta[tile & 3][mine] = Meta{meta.k, scale_log2(meta.v)};
+                    s_meta[tile & 3][mine] = Meta{meta.k, log2f(meta.v)};
                     mbar_arrive(bar_of(tile - tile0));
                 }
                 fence_proxy_async_smem();
@@ -422,6 +422,7 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
             }
             if (tile0 < tile1) wait_o();
         } else {
+            float least = kScaleLeast;  // that a log2 of v's scale counts as
             for (int tile = tile0; tile < tile1; ++tile) {
                 wait_s(tile - tile0);
                 tc_fence_after();
@@ -430,11 +431,17 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
                 tmem_ld32(t_s, sr);
                 tmem_ld32(t_s + 32, sr + 32);
                 Meta meta[kBlocks];
-                bool missing = false;
+                bool missing = false, low = false;
 #pragma unroll
                 for (int x = 0; x < kBlocks; ++x) {
                     meta[x] = s_meta[tile & 3][x];
                     missing |= meta[x].k < 0.f;
+                    least = fmaxf(least, meta[x].v - kScaleSpan);
+                }
+#pragma unroll
+                for (int x = 0; x < kBlocks; ++x) {
+                    low |= meta[x].v < least;
+                    meta[x].v = fmaxf(meta[x].v, least);
                 }
                 tmem_wait_ld_regs<kKeys>(sr);
                 const int key0 = tile * kKeys;
@@ -459,9 +466,9 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
                 // The reference of the weights.
                 const float m_new = top > m + kGrowth || m == kNegInf ? fmaxf(m, top) : m;
                 const float m_use = m_new == kNegInf ? 0.f : m_new;
-                const float fix = m == kNegInf ? (m_new == kNegInf ? 1.f : 0.f) : exp2_fast(m - m_use);
+                const float half = m == kNegInf ? (m_new == kNegInf ? 1.f : 0.f) : exp2_fast(0.5f * (m - m_use)), fix = half * half;
                 m = m_new;
-                l *= fix;
+                l = rescaled(l, half);
 #pragma unroll
                 for (int x = 0; x < kBlocks; ++x) {
                     // (A factor of 0 must not make masked scores NaN.)
@@ -481,6 +488,14 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
                     float sum[2];
                     unpair(add2(acc[0], acc[1]), sum[0], sum[1]);
                     l += (sum[0] + sum[1]) * exp2_fast(-meta[x].v);
+                }
+                if (low) {
+#pragma unroll
+                    for (int x = 0; x < kBlocks; ++x) {
+                        const float by = exp2_fast(fminf(s_meta[tile & 3][x].v - least, 0.f));
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) sr[8 * x + i] = brought_down(sr[8 * x + i], by);
+                    }
                 }
                 if (tile > tile0) {  // O += P V of the tile before is done
                     wait_o();
@@ -600,9 +615,9 @@ __global__ void __launch_bounds__(kRows * kShares, kShares == 4 ? 2 : 1) block_j
     for (int d = 0; d < kCh; ++d) acc[d] = 0.f;
     auto add = [&](float mk, float lk, const float* o) {
         const float m = fmaxf(top, mk), use = m == kNegInf ? 0.f : m;
-        const float a = exp2f(top - use), b = exp2f(mk - use);
+        const float ha = exp2_fast(0.5f * (top - use)), hb = exp2_fast(0.5f * (mk - use)), a = ha * ha, b = hb * hb;
         top = m;
-        sum = sum * a + lk * b;
+        sum = rescaled(sum, ha) + rescaled(lk, hb);
 #pragma unroll
         for (int d = 0; d < kCh; ++d) acc[d] = acc[d] * a + o[d] * b;
     };

@@ -397,7 +397,8 @@ kda_status kda_kvcache_append(const kda_kvcache* cache, const void* k, const voi
  *   cu_tokens     device int32 [rows + 1] or NULL: one token for each row, num_tokens = rows
  *   scale         finite
  * Codes at positions below lens[r] must be finite (the append writes no others); what a page
- * holds past them is never used.  Scales of pages in use are finite and not negative.  Positions
+ * holds past them is never used.  Scales of pages in use are not negative, v's at most 2^120 (the
+ * append writes none above).  A page whose v scale is 0 adds nothing but its weights to the sum.  Positions
  * whose page is missing are skipped and recorded as KDA_ERR_INVALID_ARGUMENT. */
 kda_status kda_kvcache_attention(const kda_kvcache* cache, const void* q, int32_t num_q_heads,
                                  int32_t act_dtype, int64_t q_stride, int64_t num_tokens,

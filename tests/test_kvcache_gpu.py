@@ -399,3 +399,33 @@ def test_append_then_attend_in_a_graph():
     first = out.clone()
     step()
     assert torch.equal(out, first)
+
+
+@pytest.mark.parametrize("order", [1, -1])
+@pytest.mark.parametrize("small,large", [(0, 2.0 ** 30), (0, 2.0 ** 110), (2.0 ** -70, 2.0 ** 60), (2.0 ** -20, 2.0 ** 110)])
+@pytest.mark.parametrize("hq,d,n,length", [(4, 64, 1, 64), (16, 128, 1, 5000), (16, 64, 100, 128), (32, 128, 100, 3000)])
+def test_scales_of_values_any_distance_apart(hq, d, n, length, small, large, order):
+    # equal scores, half of the pages with a small or zero scale of v: those keep their half of the
+    # weights.  Weights are fp16 and their pages' contributions no closer than 2^-90 of the largest
+    # scale's (2^-80 here, of 448: far below the bound of the large ones).  Outputs of 448 * 2^110 are finite in bf16.
+    rng = np.random.default_rng(length + d)
+    kc, vc, ks, vs, tab = make_cache(rng, 1, 4, 16, d, [length])
+    first = np.arange(tab.shape[1]) < tab.shape[1] // 2
+    vs[tab[0]] = np.where(first == (order > 0), small, large).astype(np.float32)[:, None]
+    q = torch.zeros(n, hq, d, dtype=torch.bfloat16)
+    want, weight = ref.attention(q.double().numpy(), kc, vc, ks, vs, tab, [length], [n], 16, 0.125)
+    got = K.kda_kvcache_attention(q.cuda(), *gpu_cache(kc, vc, ks, vs, tab), torch.tensor([length], dtype=torch.int32).cuda(),
+                                  cu_tokens=cu_of([n]), scale=0.125).double().cpu().numpy()
+    assert np.isfinite(got).all()
+    assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -10 * weight + 1e-6).all()
+
+
+@pytest.mark.parametrize("hq,n", [(4, 1), (8, 100)])
+def test_codes_of_a_scale_of_zero_are_zero(hq, n):
+    # what infinities in an otherwise empty page leave behind
+    rng = np.random.default_rng(17)
+    kc, vc, ks, vs, tab = make_cache(rng, 1, 1, 16, 64, [200])
+    vs[:] = 0
+    q = torch.as_tensor(rng.standard_normal((n, hq, 64))).to(torch.bfloat16)
+    got = K.kda_kvcache_attention(q.cuda(), *gpu_cache(kc, vc, ks, vs, tab), torch.tensor([200], dtype=torch.int32).cuda(), cu_tokens=cu_of([n]))
+    assert (got == 0).all()
