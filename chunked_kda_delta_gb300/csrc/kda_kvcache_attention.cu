@@ -21,8 +21,9 @@
 // q is scaled by a power of two per row so that its largest magnitude is in [2^14, 2^15) and
 // becomes fp16 without loss (bf16 has fewer bits; what falls below fp16's range is 2^-38 of the
 // largest).  Weights times their page's v scale are fp16 relative to the running maximum of
-// that product, so they stay in [0, 1]; the sum of the weights divides the scale out again by
-// blocks of 16 keys.  Running maximum, sums, outputs and the joined parts are fp32.
+// that product, which becomes 2^14, so they use fp16's whole range: a long row's weights may all be
+// 2^-20 of one key's and less and hold a large part of the sum together.  The sum of the weights divides
+// the scale out again by blocks of 16 keys.  Running maximum, sums, outputs and the joined parts are fp32.
 //
 // Work split: warps work alone.  The items' cached tokens, cut into slabs, are numbered
 // through all items; every resident warp takes an equal contiguous share, however long the rows
@@ -40,6 +41,7 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 128, kWarps = 4;
+constexpr float kLift = 14.f;     // log2 of the largest weight: fp16 is normal down to 2^-28 of it
 constexpr int kMaxListed = 1024;  // rows whose prefix fits in shared memory
 // Keys of a slab: 4 KB of codes of K, so that as many bytes are under way for head_dim 64 as for
 // 128 (64 keys against 32 there: 85 rows of up to 7582 tokens, 32 heads over 2, 51 against 65 us; one
@@ -328,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(c
                     const float m_use = m_new == kNegInf ? 0.f : m_new;
                     down[col] = m[nt][col] - m_use;
                     m[nt][col] = m_new;
-                    top[col] = m_use;
+                    top[col] = m_use - kLift;
                 }
                 float add[2] = {0.f, 0.f};
 #pragma unroll

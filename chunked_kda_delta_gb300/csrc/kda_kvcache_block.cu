@@ -15,8 +15,9 @@
 // 1000 of them issuing, the rest waiting for each other at three barriers; 159 us instead of 87 for 8 pieces of up to 512
 // tokens, 16 heads of 64 over 4, 4096 cached.  Eight widening warps: 102; two softmax groups: 105
 // and 108.)
-// O is rescaled only when a row's maximum has grown by more than 2^8 over the one in use: weights
-// stay below 2^8 in fp16 and the sums are the same.  The v scale enters the exponent, also for the
+// O is rescaled only when a row's maximum has grown by more than 2^8 over the one in use (a published
+// method), whose weight is 2^7: weights stay below 2^15 in fp16, which is normal down to 2^-21 of the
+// largest, and the sums are the same.  The v scale enters the exponent, also for the
 // maximum, and leaves the sum again by blocks of 16 keys.
 //
 // Bound by issue and latency: a tile takes each of an SM's two CTAs 2700 cycles (head_dim 128: 4700),
@@ -38,7 +39,7 @@ constexpr int kRows = kBlockRows, kKeys = 64, kBlocks = kKeys / 16;
 constexpr int kSoft = 128, kWiden = 128;          // threads of the softmax, of the widening
 constexpr int kThreads = kSoft + kWiden;
 constexpr int kMaxListed = 512;           // rows whose prefix fits in shared memory
-constexpr float kGrowth = 8.f;            // log2 of how far a maximum may grow
+constexpr float kGrowth = 8.f, kLift = 7.f; // log2 of how far a maximum may grow, of the weight at it
 constexpr uint32_t kColS = 0, kColO = 128, kColumns = 256;  // tensor memory: S and P twice, O
 constexpr int64_t kWaitLimit = 1ll << 20;
 // Two CTAs an SM and no third: the tensor memory is for two.
@@ -473,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
                 for (int x = 0; x < kBlocks; ++x) {
                     // (A factor of 0 must not make masked scores NaN.)
                     const float k = meta[x].k * factor > 0.f ? meta[x].k * factor : 0x1p-126f;
-                    const float bias = meta[x].v - m_use;
+                    const float bias = meta[x].v - m_use + kLift;
                     const uint64_t k2 = pair(k, k), bias2 = pair(bias, bias);
                     uint64_t acc[2] = {0, 0};  // (+0, +0)
 #pragma unroll

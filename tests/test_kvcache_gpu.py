@@ -429,3 +429,30 @@ def test_codes_of_a_scale_of_zero_are_zero(hq, n):
     q = torch.as_tensor(rng.standard_normal((n, hq, 64))).to(torch.bfloat16)
     got = K.kda_kvcache_attention(q.cuda(), *gpu_cache(kc, vc, ks, vs, tab), torch.tensor([200], dtype=torch.int32).cuda(), cu_tokens=cu_of([n]))
     assert (got == 0).all()
+
+
+@pytest.mark.parametrize("away", [13.0, 16.0, 18.0])
+@pytest.mark.parametrize("hq,n,rows", [(1, 1, 1), (4, 1, 1200), (12, 1, 1200), (4, 64, 300)])
+def test_many_small_weights_beside_a_large_one(hq, n, rows, away):
+    # A first key whose score lies `away` above all others and whose value is zero; 2^17 keys of equal
+    # scores and values v.  With M of them seen, o = v M e^-away / (1 + M e^-away).  Bound: fp16 weights
+    # (2^-11, of a weight below fp16's normal range up to 2^-32 of the largest), scores in fp32 (2^-18
+    # of the weights), one rounding to bf16 (2^-9).  Enough rows that a part is most of one.
+    d, page, length = 64, 128, 2 ** 17
+    pages = length // page
+    code = {1.0: 0x38, 2.0: 0x40}
+    kc, vc = np.zeros((2, 1, page, d), np.uint8), np.full((2, 1, page, d), code[1.0], np.uint8)
+    vc[..., 1::2] = code[2.0] | 0x80
+    kc[0, 0, 0, 0], vc[0, 0, 0] = code[1.0], 0
+    ks, vs = np.full((2, 1), away, np.float32), np.full((2, 1), 0.5, np.float32)
+    tab = np.array([[0] + [1] * (pages - 1)] * rows)
+    q = torch.zeros(rows * n, hq, d)
+    q[..., 0] = 1
+    got = K.kda_kvcache_attention(q.bfloat16().cuda(), *gpu_cache(kc, vc, ks, vs, tab), torch.full((rows,), length, dtype=torch.int32).cuda(),
+                                  cu_tokens=cu_of([n] * rows), scale=1.0).double().cpu().numpy()
+    m = (length - n + np.tile(np.arange(n), rows))[:, None, None].astype(np.float64)  # others that a token sees
+    v = np.where(np.arange(d) % 2, -1.0, 0.5)
+    w = np.exp(-away)
+    want = v * m * w / (1 + m * w)
+    allowed = (2.0 ** -8 + 2.0 ** -10) * np.abs(want) + 2.0 ** -32 * m * np.abs(v) / (1 + m * w)
+    assert (np.abs(got - want) <= allowed).all(), np.max(np.abs(got - want) / allowed)
