@@ -538,8 +538,8 @@ def kda_decode_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch
     _check_result("out", out, _out_shape(q, v), torch.bfloat16, "cuda")
     if stream is None:
         stream = torch.cuda.current_stream(q.device)
-    elif not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), q.device)
+    elif not isinstance(stream, torch.cuda.Stream):  # 0 and 1 are handles of the default stream
+        stream = torch.cuda.ExternalStream(int(stream), q.device) if int(stream) > 1 else torch.cuda.default_stream(q.device)
     if out is None:
         with torch.cuda.stream(stream):  # memory that work of this stream alone may still use
             out = torch.empty(_out_shape(q, v), dtype=q.dtype, device=q.device)

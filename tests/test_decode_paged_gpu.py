@@ -55,3 +55,23 @@ def test_refusals():
         K.kda_decode_paged(*x, pool.transpose(2, 3), at)
     with pytest.raises(K.KdaError):  # grouped query heads would race on the state
         K.kda_decode_paged(*tokens(2, 1, 2, 4, 6), pool, at)
+
+
+@pytest.mark.parametrize("handle", [0, 1])
+def test_handles_of_the_default_stream(handle):
+    # the call comes after work that is pending there
+    x = tokens(3, 1, 2, 2, 8)
+    state = torch.randn(3, 2, 128, 128, device="cuda") * 0.1
+    at = torch.tensor([2, 0, 1], dtype=torch.int32, device="cuda")
+    want_pool = state.clone()
+    want = K.kda_decode_paged(*x, want_pool, at)
+    pool = torch.zeros_like(state)
+    busy = torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.default_stream()):
+        for _ in range(8):
+            busy = busy @ busy * 1e-3
+        pool.copy_(state)
+    got = K.kda_decode_paged(*x, pool, at, stream=handle)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(pool, want_pool)
