@@ -57,11 +57,12 @@ __device__ int32_t g_status_word = 0;
 constexpr int kMaxDevices = 64;
 constexpr int64_t kDefaultWaitLimit = 1ll << 22;
 constexpr size_t kMaxWorkspaces = 8;
-constexpr size_t kMaxServingWorkspaces = 32;  // streams with their own serving scratch
 constexpr int kMaxHostPieces = 64;  // pieces kda_prefill_host may stream a call in
 
 std::mutex g_mutex;
 DeviceInfo g_devices[kMaxDevices];
+cudaMemPool_t g_pools[kMaxDevices] = {};  // serving scratch of callers without an allocator of theirs
+thread_local kda_scratch_allocator t_allocator = {};
 
 }  // namespace
 
@@ -125,6 +126,60 @@ kda_status current_device(int* dev, DeviceInfo** out) {
     return device_info(*dev, out);
 }
 
+// ---------------------------------------------------------------------------
+// Scratch of a serving call: of no other call's until the stream is past this one's launches,
+// whichever threads and graphs make them.  The pool keeps what it was given back.
+static kda_status scratch_pool(int dev, cudaMemPool_t* out) {
+    std::lock_guard<std::mutex> lock(g_mutex);
+    if (!g_pools[dev]) {
+        cudaMemPoolProps props = {};
+        props.allocType = cudaMemAllocationTypePinned;
+        props.location.type = cudaMemLocationTypeDevice;
+        props.location.id = dev;
+        // (No part of a capture that another thread may have under way.)
+        cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+        cudaThreadExchangeStreamCaptureMode(&mode);
+        cudaMemPool_t pool = nullptr;
+        cudaError_t e = cudaMemPoolCreate(&pool, &props);
+        uint64_t keep = ~0ull;
+        if (e == cudaSuccess) e = cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep);
+        cudaThreadExchangeStreamCaptureMode(&mode);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaMemPoolCreate");
+        g_pools[dev] = pool;
+    }
+    *out = g_pools[dev];
+    return KDA_OK;
+}
+
+kda_status Scratch::take(int dev, void* stream, size_t bytes) {
+    from_ = t_allocator;
+    stream_ = stream;
+    bytes_ = bytes;
+    void* p = nullptr;
+    if (from_.allocate) {
+        p = from_.allocate(from_.context, bytes, stream);
+        if (!p) return fail(KDA_ERR_OUT_OF_MEMORY, "the scratch allocator has no %zu bytes", bytes);
+    } else {
+        cudaMemPool_t pool = nullptr;
+        const kda_status st = scratch_pool(dev, &pool);
+        if (st != KDA_OK) return st;
+        const cudaError_t e = cudaMallocFromPoolAsync(&p, bytes, pool, (cudaStream_t)stream);
+        if (e != cudaSuccess) {
+            cudaGetLastError();
+            return fail(e == cudaErrorMemoryAllocation ? KDA_ERR_OUT_OF_MEMORY : KDA_ERR_CUDA,
+                        "cudaMallocFromPoolAsync(%zu) for scratch failed: %s", bytes, cudaGetErrorString(e));
+        }
+    }
+    base = static_cast<char*>(p);
+    return KDA_OK;
+}
+
+Scratch::~Scratch() {
+    if (!base) return;
+    if (from_.allocate) from_.release(from_.context, base, bytes_, stream_);
+    else if (cudaFreeAsync(base, (cudaStream_t)stream_) != cudaSuccess) cudaGetLastError();
+}
+
 }  // namespace host
 }  // namespace kda
 
@@ -132,8 +187,9 @@ namespace {
 
 // ---------------------------------------------------------------------------
 // Workspaces: one device buffer per (device, stream), grown on demand, at most
-// kMaxWorkspaces alive (least recently used evicted).  Serving scratch counts by itself, up
-// to kMaxServingWorkspaces.
+// kMaxWorkspaces alive (least recently used evicted).
+enum WorkspaceKind { kWsSegment = 0, kWsHostArena = 1 };
+
 struct Workspace {
     int device;
     void* stream;
@@ -143,13 +199,7 @@ struct Workspace {
     unsigned long long last_use;
 };
 std::vector<Workspace> g_workspaces;
-std::vector<Workspace> g_retired;  // outgrown serving scratch: captured graphs may still use it
 unsigned long long g_use_clock = 0;
-
-}  // namespace
-
-namespace kda {
-namespace host {
 
 kda_status get_workspace(int dev, cudaStream_t stream, int kind, size_t bytes, void** out) {
     *out = nullptr;
@@ -170,27 +220,15 @@ kda_status get_workspace(int dev, cudaStream_t stream, int kind, size_t bytes, v
     for (size_t i = 0; i < g_workspaces.size(); ++i)
         if (g_workspaces[i].device == dev && g_workspaces[i].stream == (void*)stream &&
             g_workspaces[i].kind == kind) {
-            if (kind == kWsServing) {
-                g_retired.push_back(g_workspaces[i]);
-            } else {
-                cudaStreamSynchronize(stream);
-                cudaFree(g_workspaces[i].ptr);
-            }
+            cudaStreamSynchronize(stream);
+            cudaFree(g_workspaces[i].ptr);
             g_workspaces.erase(g_workspaces.begin() + i);
             break;
         }
-    const bool serving = kind == kWsServing;
-    size_t alive = 0, lru = 0;
-    unsigned long long oldest = ~0ull;
-    for (size_t i = 0; i < g_workspaces.size(); ++i)
-        if ((g_workspaces[i].kind == kWsServing) == serving) {
-            ++alive;
-            if (g_workspaces[i].last_use < oldest) {
-                oldest = g_workspaces[i].last_use;
-                lru = i;
-            }
-        }
-    if (alive >= (serving ? kMaxServingWorkspaces : kMaxWorkspaces)) {
+    if (g_workspaces.size() >= kMaxWorkspaces) {
+        size_t lru = 0;
+        for (size_t i = 1; i < g_workspaces.size(); ++i)
+            if (g_workspaces[i].last_use < g_workspaces[lru].last_use) lru = i;
         int cur;
         cudaGetDevice(&cur);
         cudaSetDevice(g_workspaces[lru].device);
@@ -210,11 +248,6 @@ kda_status get_workspace(int dev, cudaStream_t stream, int kind, size_t bytes, v
     *out = p;
     return KDA_OK;
 }
-
-}  // namespace host
-}  // namespace kda
-
-namespace {
 
 // ---------------------------------------------------------------------------
 // TMA descriptors.  cuTensorMapEncodeTiled is reached through the runtime's
@@ -1242,16 +1275,12 @@ kda_status kda_release_workspaces(int32_t device) {
             ++i;
         }
     }
-    for (size_t i = 0; i < g_retired.size();) {
-        if (device < 0 || g_retired[i].device == device) {
-            cudaSetDevice(g_retired[i].device);
+    for (int d = 0; d < kMaxDevices; ++d)
+        if (g_pools[d] && (device < 0 || device == d)) {
+            cudaSetDevice(d);
             cudaDeviceSynchronize();
-            cudaFree(g_retired[i].ptr);
-            g_retired.erase(g_retired.begin() + i);
-        } else {
-            ++i;
+            cudaMemPoolTrimTo(g_pools[d], 0);
         }
-    }
     for (size_t i = 0; i < g_pipes.size();) {
         if (device < 0 || g_pipes[i]->device == device) {
             destroy_pipe(*g_pipes[i]);
@@ -1261,6 +1290,15 @@ kda_status kda_release_workspaces(int32_t device) {
         }
     }
     cudaSetDevice(cur);
+    return KDA_OK;
+}
+
+kda_status kda_set_scratch_allocator(const kda_scratch_allocator* allocator, kda_scratch_allocator* previous) {
+    const kda_scratch_allocator next = allocator ? *allocator : kda_scratch_allocator{};
+    if ((next.allocate == nullptr) != (next.release == nullptr))
+        return fail(KDA_ERR_INVALID_ARGUMENT, "allocate and release come together");
+    if (previous) *previous = t_allocator;
+    t_allocator = next;
     return KDA_OK;
 }
 

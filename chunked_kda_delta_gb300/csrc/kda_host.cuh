@@ -25,10 +25,22 @@ kda_status device_info(int dev, DeviceInfo** out);
 // The current device and its cached properties.
 kda_status current_device(int* dev, DeviceInfo** out);
 
-// Scratch of the cache, page and beam calls (kWsServing) is one buffer per (device, stream)
-// that those calls share in stream order.  Grown buffers are kept until the release.
-enum WorkspaceKind { kWsSegment = 0, kWsHostArena = 1, kWsServing = 2 };
-kda_status get_workspace(int dev, cudaStream_t stream, int kind, size_t bytes, void** out);
+// Scratch of one cache, page or beam call, from the thread's allocator or the library's pool: taken in
+// the order of the stream, and given back in it when the object goes, after the call's last launch.
+class Scratch {
+public:
+    Scratch() = default;
+    Scratch(const Scratch&) = delete;
+    Scratch& operator=(const Scratch&) = delete;
+    ~Scratch();
+    kda_status take(int dev, void* stream, size_t bytes);
+    char* base = nullptr;
+
+private:
+    kda_scratch_allocator from_ = {};
+    void* stream_ = nullptr;
+    size_t bytes_ = 0;
+};
 
 struct Range {
     const void* p;

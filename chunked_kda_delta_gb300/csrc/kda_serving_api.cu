@@ -15,19 +15,6 @@ using namespace kda::host;
 
 namespace {
 
-constexpr size_t kMinScratch = (size_t)4 << 20;
-
-// Scratch of one call: at least kMinScratch and a power of two, so that calls of different
-// sizes rarely make it grow.
-kda_status scratch(int dev, void* stream, size_t bytes, char** out) {
-    size_t size = kMinScratch;
-    while (size < bytes) size <<= 1;
-    void* p = nullptr;
-    const kda_status st = get_workspace(dev, (cudaStream_t)stream, kWsServing, size, &p);
-    *out = static_cast<char*>(p);
-    return st;
-}
-
 // Runs an entry's body: nothing throws across the ABI.
 template <typename F>
 kda_status guarded(F body) {
@@ -138,9 +125,9 @@ kda_status run_plan(kda::PagePlan p, int mode, bool compact, const kda::PoolSet&
     const size_t entries = (size_t)p.rows * p.width;
     if (entries == 0 && p.pages == 0 && !compact) return KDA_OK;
     const size_t pairs = compact ? (size_t)p.pages : mode == kda::kPagesFork ? entries : 0;
-    char* ws = nullptr;
-    if ((st = scratch(dev, stream, (64 + 3 * (size_t)p.pages + 2 * pairs) * 4, &ws)) != KDA_OK) return st;
-    int32_t* at = reinterpret_cast<int32_t*>(ws);
+    Scratch ws;
+    if ((st = ws.take(dev, stream, (64 + 3 * (size_t)p.pages + 2 * pairs) * 4)) != KDA_OK) return st;
+    int32_t* at = reinterpret_cast<int32_t*>(ws.base);
     p.copies = at;
     p.held = at + 64;
     p.first = p.held + p.pages;
@@ -416,9 +403,9 @@ kda_status kda_kvcache_attention(const kda_kvcache* cache, const void* q, int32_
         p.sm_count = di->sm_count;
         p.ctas = kda::attention_ctas(cache->head_dim, cols, f16, di->sm_count);
         const size_t parts = (cols == kda::kBlockRows ? (size_t)2 * p.ctas : kda::attention_slots(p.ctas)) * cols;
-        char* ws = nullptr;
-        if ((st = scratch(dev, stream, parts * (cache->head_dim + 2) * 4 + (size_t)p.ctas * 32 + ((size_t)cache->rows + 1) * 8, &ws)) != KDA_OK) return st;
-        p.part_o = reinterpret_cast<float*>(ws);
+        Scratch ws;
+        if ((st = ws.take(dev, stream, parts * (cache->head_dim + 2) * 4 + (size_t)p.ctas * 32 + ((size_t)cache->rows + 1) * 8)) != KDA_OK) return st;
+        p.part_o = reinterpret_cast<float*>(ws.base);
         p.part_ml = p.part_o + parts * cache->head_dim;
         p.split_items = p.part_ml + parts * 2;
         p.first_work = reinterpret_cast<int64_t*>(p.part_ml + parts * 2 + (size_t)p.ctas * 8);
@@ -488,10 +475,10 @@ kda_status kda_beam_select(int32_t batch, int32_t beams, int32_t vocab, int32_t 
         p.segs = (int32_t)(((int64_t)vocab + (even ? 0 : 16 / elem - 1) + p.seg_len - 1) / p.seg_len);
         if (rows * p.segs > 0x7fffffffll) return fail(KDA_ERR_INVALID_ARGUMENT, "batch * beams * vocab is too large");
         const size_t pb = (size_t)rows * p.segs * 16, cb = (size_t)rows * p.segs * (num_out + 1) * 8;
-        char* ws = nullptr;
-        if ((st = scratch(dev, stream, cb + pb, &ws)) != KDA_OK) return st;
-        p.part = reinterpret_cast<float4*>(ws);
-        p.cand = reinterpret_cast<uint64_t*>(ws + pb);
+        Scratch ws;
+        if ((st = ws.take(dev, stream, cb + pb)) != KDA_OK) return st;
+        p.part = reinterpret_cast<float4*>(ws.base);
+        p.cand = reinterpret_cast<uint64_t*>(ws.base + pb);
         const cudaError_t e = kda::launch_beam(p, (cudaStream_t)stream);
         return e == cudaSuccess ? KDA_OK : cuda_fail(e, "beam selection launch");
     });

@@ -35,7 +35,7 @@ EXPORTED_SYMBOLS = (
     "kda_last_error_message", "kda_version", "kda_prefill_segment_noalloc", "kda_plan",
     "kda_plan_varlen", "kda_decode", "kda_decode_paged", "kda_pages_alloc", "kda_pages_free",
     "kda_pages_fork", "kda_pages_compact", "kda_pages_copy", "kda_kvcache_append",
-    "kda_kvcache_attention", "kda_beam_select",
+    "kda_kvcache_attention", "kda_beam_select", "kda_set_scratch_allocator",
 )
 
 STATE_F32 = 0
@@ -79,6 +79,12 @@ class KdaKvCache(ctypes.Structure):
                 ("pages", ctypes.c_int32), ("page_tokens", ctypes.c_int32),
                 ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("tables", ctypes.c_void_p), ("rows", ctypes.c_int32), ("width", ctypes.c_int32)]
+
+
+class KdaScratchAllocator(ctypes.Structure):
+    _fields_ = [("allocate", ctypes.CFUNCTYPE(ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p)),
+                ("release", ctypes.CFUNCTYPE(None, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p)),
+                ("context", ctypes.c_void_p)]
 
 
 _lib = None
@@ -133,6 +139,8 @@ def load_library(path: Optional[str] = None, build_if_missing: bool = False) -> 
                                               vp]
         lib.kda_beam_select.argtypes = [i32, i32, i32, i32, vp, i32, i64, vp, vp, i32, vp, vp, vp,
                                         vp, vp]
+        lib.kda_set_scratch_allocator.argtypes = [ctypes.POINTER(KdaScratchAllocator),
+                                                  ctypes.POINTER(KdaScratchAllocator)]
         lib.kda_get_device_status.argtypes = [vp, ctypes.POINTER(ctypes.c_int32)]
         lib.kda_release_workspaces.argtypes = [ctypes.c_int32]
         lib.kda_status_string.argtypes = [ctypes.c_int]
@@ -145,7 +153,7 @@ def load_library(path: Optional[str] = None, build_if_missing: bool = False) -> 
                   lib.kda_release_workspaces, lib.kda_decode_paged, lib.kda_pages_alloc,
                   lib.kda_pages_free, lib.kda_pages_fork, lib.kda_pages_compact,
                   lib.kda_pages_copy, lib.kda_kvcache_append, lib.kda_kvcache_attention,
-                  lib.kda_beam_select):
+                  lib.kda_beam_select, lib.kda_set_scratch_allocator):
             f.restype = ctypes.c_int
         if path is None:
             _lib = lib

@@ -6,6 +6,9 @@ is returned and calls the C ABI, asynchronously on the given (or current) stream
 in the library's CUDA kernels and there is no fallback.  Calls in a row: appending one token to 256
 rows 5.2 us, a selection of 4 from 4 beams 8.2, a fork of a cache's tables 14.7 (GB300); with this
 marshalling in Python and ctypes, where the host was the bound, 13.0, 25.3 and 33.9.
+Results and scratch are torch's memory of the call's stream: inside ``torch.cuda.graph`` they belong to
+the graph, and no call is needed before it.  (A capture begun without torch has to keep to the C
+ABI: torch does not hold memory for it.)
 What only a kernel can see (page numbers out of range, too few free pages, values that are not
 finite) goes to the device status word: :func:`~.kda.kda_get_device_status`.
 """

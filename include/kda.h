@@ -34,8 +34,8 @@
  * 16-byte aligned; beta 2-byte aligned; cu_seqlens 4-byte aligned.
  *
  * Ownership: the caller owns every tensor.  The library owns only its
- * workspaces (device scratch, per device and stream, bounded in number) and
- * releases them in kda_release_workspaces().  No caller pointer is retained
+ * workspaces (device scratch, per device and stream, bounded in number) and the
+ * pool of the serving calls' scratch, and releases them in kda_release_workspaces().  No caller pointer is retained
  * after a call returns.
  *
  * Errors: every entry point returns a kda_status; nothing throws across the
@@ -434,6 +434,25 @@ kda_status kda_beam_select(int32_t batch, int32_t beams, int32_t vocab, int32_t 
                            float* new_scores, int32_t* tokens, int32_t* parents,
                            uint8_t* new_done, void* stream);
 
+/* Scratch of the page, cache and beam calls (kda_pages_*, kda_kvcache_*, kda_beam_select).  Each call
+ * takes its own, in the order of its stream, and gives it back after its last launch: calls share
+ * none, whichever threads, streams and captured graphs they come from, and a capture needs no call before it.  By
+ * default it comes from a memory pool of the library (cudaMallocFromPoolAsync; inside a capture it
+ * becomes an allocation of that graph).  kda_set_scratch_allocator puts an allocator in the pool's place for
+ * the calls that this host thread makes from then on (NULL, or all members NULL: the pool again);
+ * what was set before goes to *previous unless that is NULL.
+ *   allocate  device memory of the current device, 16-byte aligned, that work put on `stream` from
+ *             now on may use; NULL: none (the call returns KDA_ERR_OUT_OF_MEMORY).  Must not throw
+ *   release   called once for each, when all work that uses it has been put on `stream`
+ *   context   passed to both
+ * Errors: KDA_ERR_INVALID_ARGUMENT (one of the two functions alone). */
+typedef struct kda_scratch_allocator {
+    void* (*allocate)(void* context, size_t bytes, void* stream);
+    void (*release)(void* context, void* scratch, size_t bytes, void* stream);
+    void* context;
+} kda_scratch_allocator;
+kda_status kda_set_scratch_allocator(const kda_scratch_allocator* allocator, kda_scratch_allocator* previous);
+
 /* Bytes of device workspace a call with this shape and these options uses
  * (0 for serial mode).  The segment pipeline's scratch (per-segment summaries,
  * transitions and carries: cuLA PR #103, review of the CP driver's _get_scratch, which
@@ -492,9 +511,8 @@ kda_status kda_get_device_status(void* stream, int32_t* code);
  * pages' scratch cache raced across streams because its key lacked the stream (cuLA PR
  * #103, review of _get_scratch) and their per-stream workspace maps grew without bound
  * (flashinfer PR #4313, review of kda_prefill.py, which asks for a bound or an eviction
- * path); this call is the explicit release.  The scratch of the cache, page and beam calls
- * is one more buffer per (device, stream), for at most 32 of them; where a larger call grows
- * it, the smaller buffer lives on until this call, so graphs captured on it stay valid. */
+ * path); this call is the explicit release.  The pool that the page, cache and beam calls take
+ * their scratch from gives back to the device what no call or graph holds. */
 kda_status kda_release_workspaces(int32_t device);
 
 /* Static description of a status code.  The pages' bindings fail with a message per

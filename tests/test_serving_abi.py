@@ -7,7 +7,7 @@ import torch
 
 import chunked_kda_delta_gb300 as K
 from chunked_kda_delta_gb300 import build as kbuild
-from chunked_kda_delta_gb300.kda import KdaKvCache, KdaPageShape, KdaPool, KdaShape
+from chunked_kda_delta_gb300.kda import KdaKvCache, KdaPageShape, KdaPool, KdaScratchAllocator, KdaShape
 
 # Calls that pass validation go on with made-up addresses: they must not reach a GPU.
 pytestmark = pytest.mark.skipif(torch.cuda.is_available(), reason="made-up device addresses")
@@ -162,3 +162,14 @@ def test_binding_refuses_cpu_tensors_and_wrong_types():
     c = torch.zeros(4, 1, 16, 64, dtype=torch.uint8)
     with pytest.raises(ValueError):
         K.kda_kvcache_attention(torch.zeros(1, 1, 64), c, c, torch.zeros(4, 1), torch.zeros(4, 1), t[:1], r[:1])
+
+
+def test_scratch_allocator_rules(lib):
+    fields = KdaScratchAllocator._fields_
+    one = KdaScratchAllocator(fields[0][1](lambda c, n, s: None), fields[1][1](), 5)
+    assert lib.kda_set_scratch_allocator(ctypes.byref(one), None) == INVALID
+    both = KdaScratchAllocator(fields[0][1](lambda c, n, s: None), fields[1][1](lambda c, p, n, s: None), 5)
+    before = KdaScratchAllocator()
+    assert lib.kda_set_scratch_allocator(ctypes.byref(both), ctypes.byref(before)) == 0 and not before.context
+    assert lib.kda_set_scratch_allocator(None, ctypes.byref(before)) == 0 and before.context == 5
+    assert lib.kda_set_scratch_allocator(None, None) == 0

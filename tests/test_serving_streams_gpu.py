@@ -1,11 +1,15 @@
 """The serving operators on a stream that is not the current one: given as a torch stream or as a
 raw handle, with results whose memory no pending work of the current stream still writes."""
+import ctypes
+from concurrent.futures import ThreadPoolExecutor
+
 import numpy as np
 import pytest
 import torch
 
 import chunked_kda_delta_gb300 as K
 from chunked_kda_delta_gb300.inputs import custom, make_inputs
+from chunked_kda_delta_gb300.kda import KdaScratchAllocator
 
 pytestmark = pytest.mark.gpu
 
@@ -135,3 +139,146 @@ def test_chains_of_calls_without_waits():
     for _ in range(5):
         assert all(torch.equal(a, b) for a, b in zip(run(lambda: None), want))
     assert K.kda_get_device_status() == 0
+
+
+def graph_of(call):
+    """A graph of the call, captured on torch's own capture stream with no call before it there."""
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        out = call(None)
+    return g, out
+
+
+def attend_and_beam(seed):
+    """Calls whose launches hand results on through scratch: parts of attention, candidates, copies."""
+    gen = torch.Generator("cuda").manual_seed(seed)
+    draw = lambda *s: torch.randn(*s, device="cuda", generator=gen)  # noqa: E731
+    x, scores = draw(2, 4, 50000), draw(2, 4)
+    codes = [draw(64, 2, 64, 64).to(torch.float8_e4m3fn) for _ in range(2)]
+    scales = [torch.rand(64, 2, device="cuda", generator=gen) + 0.5 for _ in range(2)]
+    tables = torch.randperm(64, device="cuda", generator=gen).to(torch.int32).view(2, 32)
+    q1, q2 = draw(2, 16, 64).bfloat16(), draw(140, 16, 64).bfloat16()
+    lens, cu = i32([2048, 1999]), i32([0, 70, 140])
+    pool, refs, two = draw(64, 1000), torch.ones(64, dtype=torch.int32, device="cuda"), i32([1, 1])
+    more = torch.cat([refs, torch.zeros(64, dtype=torch.int32, device="cuda")])
+    big = torch.cat([pool, torch.zeros_like(pool)])
+
+    def call(s):
+        copy = big.clone()
+        return [K.kda_kvcache_attention(q1, *codes, *scales, tables, lens, stream=s),
+                K.kda_kvcache_attention(q2, *codes, *scales, tables, lens, cu_tokens=cu, stream=s),
+                *K.kda_beam_select(x, scores, stream=s),
+                *K.kda_pages_fork(tables, more, two, pools=[copy], stream=s), copy]
+    return call
+
+
+def test_capture_without_a_call_before_it():
+    call = attend_and_beam(1)
+    g, out = graph_of(call)
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, call(None)))
+
+
+def test_graphs_of_one_capture_stream_share_no_scratch():
+    # replayed side by side on two streams, with calls on a third and on the capture stream's handle
+    calls_ = [attend_and_beam(s) for s in (2, 3, 4)]
+    want = [[t.clone() for t in c(None)] for c in calls_]
+    graphs = [graph_of(c) for c in calls_[:2]]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for _ in range(50):
+        for (g, _), s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        with torch.cuda.stream(streams[2]):
+            got = calls_[2](None)
+    torch.cuda.synchronize()
+    for (_, out), w in zip(graphs, want):
+        assert all(torch.equal(a, b) for a, b in zip(out, w))
+    assert all(torch.equal(a, b) for a, b in zip(got, want[2]))
+
+
+def test_graphs_outlive_calls_on_many_streams():
+    call, other = attend_and_beam(5), attend_and_beam(6)
+    want = [t.clone() for t in call(None)]
+    g, out = graph_of(call)
+    wide = torch.cuda.Stream(priority=-1)
+    streams = [torch.cuda.Stream() for _ in range(40)] + [torch.cuda.Stream(priority=-1) for _ in range(40)] + [wide]
+    handles = {s.cuda_stream for s in streams}
+    assert len(handles) > 33
+    keep = [other(s) for s in streams]
+    torch.cuda.synchronize()
+    fill = torch.full((64 << 20,), 0xFF, dtype=torch.uint8, device="cuda")
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, want)) and (fill == 0xFF).all()
+    assert all(torch.equal(a, b) for k in keep for a, b in zip(k, keep[0]))
+
+
+def beam_call(lib, x, scores, out, stream):
+    P = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    b, w, v = x.shape
+    return lib.kda_beam_select(b, w, v, w, P(x), 0, v, P(scores), None, -1, P(out[0]), P(out[1]), P(out[2]), None, ctypes.c_void_p(stream))
+
+
+def beam_out(b, w):
+    return torch.empty(b, w, device="cuda"), *(torch.empty(b, w, dtype=torch.int32, device="cuda") for _ in range(2))
+
+
+def test_threads_on_one_stream_share_no_scratch():
+    # through the C ABI, whose calls run at the same time: the launches of two calls in any order
+    lib = K.load_library()
+    gen = torch.Generator("cuda").manual_seed(7)
+    xs, scores = torch.randn(4, 1, 4, 20000, device="cuda", generator=gen), torch.zeros(1, 4, device="cuda")
+    want = [K.kda_beam_select(x, scores) for x in xs]
+    outs = [[beam_out(1, 4) for _ in range(300)] for _ in xs]
+    stream = torch.cuda.Stream().cuda_stream
+    torch.cuda.synchronize()
+
+    def work(i):
+        for o in outs[i]:
+            assert beam_call(lib, xs[i], scores, o, stream) == 0
+
+    with ThreadPoolExecutor(len(xs)) as pool:
+        list(pool.map(work, range(len(xs))))
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert all(torch.equal(a, b) for x in o for a, b in zip(x, w))
+
+
+def test_scratch_of_a_callers_allocator():
+    lib = K.load_library()
+    x, scores = torch.randn(1, 4, 20000, device="cuda"), torch.zeros(1, 4, device="cuda")
+    want, out = K.kda_beam_select(x, scores), beam_out(1, 4)
+    stream = torch.cuda.current_stream().cuda_stream
+    held, log = {}, []
+
+    def allocate(context, size, s):
+        if context == 7:
+            return None
+        t = torch.empty(size, dtype=torch.uint8, device="cuda")
+        held[t.data_ptr()] = t
+        log.append((size, s or 0))
+        return t.data_ptr()
+
+    def release(context, p, size, s):
+        assert held.pop(p).numel() == size and log[-1] == (size, s or 0)
+
+    a = KdaScratchAllocator(KdaScratchAllocator._fields_[0][1](allocate), KdaScratchAllocator._fields_[1][1](release), 0)
+    before = KdaScratchAllocator()
+    assert lib.kda_set_scratch_allocator(ctypes.byref(a), None) == 0
+    try:
+        assert beam_call(lib, x, scores, out, stream) == 0
+        assert len(log) == 1 and not held and log[0][1] == stream
+        assert all(torch.equal(p, q) for p, q in zip(K.kda_beam_select(x, scores), want))  # (torch's, and back)
+        a.context = 7
+        lib.kda_set_scratch_allocator(ctypes.byref(a), None)
+        assert beam_call(lib, x, scores, out, stream) == 4 and b"scratch" in lib.kda_last_error_message()
+    finally:
+        assert lib.kda_set_scratch_allocator(None, ctypes.byref(before)) == 0
+    assert before.context == 7
+    assert beam_call(lib, x, scores, out, stream) == 0
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(out, want))
