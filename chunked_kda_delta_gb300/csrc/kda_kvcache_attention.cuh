@@ -4,6 +4,7 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <limits.h>
 #include <math.h>
 
 #include "kda_serving.cuh"
@@ -94,10 +95,12 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-// Cached tokens of row r that its table has places for.
+// Cached tokens of row r that its table has places for, and key numbers: those of the tiles, pages and scales
+// that are looked at ahead fit in 31 bits too.
+constexpr int kMaxLength = INT_MAX - 4095;
 __device__ __forceinline__ int row_length(const CacheParams& c, int r) {
     const int len = c.lens[r];
-    const int64_t room = (int64_t)c.width * c.page_tokens;
+    const int64_t room = min((int64_t)c.width * c.page_tokens, (int64_t)kMaxLength);
     if (len < 0 || len > room) report(c.status, kStatusBadIndex);
     return len < 0 ? 0 : len > room ? (int)room : len;
 }

@@ -393,7 +393,8 @@ kda_status kda_kvcache_append(const kda_kvcache* cache, const void* k, const voi
  * the codes.
  *   q, out        device [num_tokens][num_q_heads][head_dim] of act_dtype, token strides in
  *                 elements (multiples of 8), 16-byte aligned; out must not overlap any input
- *   lens          device int32 [rows]
+ *   lens          device int32 [rows]; more than the table has places for, or than 2^31 - 4096, is
+ *                 recorded as KDA_ERR_INVALID_ARGUMENT and taken as that
  *   cu_tokens     device int32 [rows + 1] or NULL: one token for each row, num_tokens = rows
  *   scale         finite
  * Codes at positions below lens[r] must be finite (the append writes no others); what a page

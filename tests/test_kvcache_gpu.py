@@ -456,3 +456,24 @@ def test_many_small_weights_beside_a_large_one(hq, n, rows, away):
     want = v * m * w / (1 + m * w)
     allowed = (2.0 ** -8 + 2.0 ** -10) * np.abs(want) + 2.0 ** -32 * m * np.abs(v) / (1 + m * w)
     assert (np.abs(got - want) <= allowed).all(), np.max(np.abs(got - want) / allowed)
+
+
+@pytest.mark.parametrize("hq,n,parts", [(1, 1, 1824), (16, 1, 1216), (4, 40, 304)])
+def test_rows_of_almost_two_to_the_31_tokens(hq, n, parts):
+    # one page throughout, so every key of it is seen equally often but for the last few.  A length past
+    # the limit is recorded and taken as it.  Sums and outputs are fp32, a part's in steps of 16 keys: 2^-24
+    # of a sum for each step.
+    rng = np.random.default_rng(18)
+    kc, vc, ks, vs, _ = make_cache(rng, 1, 1, 128, 64, [128], spare=0)
+    cache = gpu_cache(kc, vc, ks, vs, np.zeros((1, 1)))
+    table = torch.zeros(1, 1 << 24, dtype=torch.int32, device="cuda")
+    q = torch.as_tensor(rng.standard_normal((n, hq, 64))).to(torch.bfloat16)
+    want, weight = ref.attention(q.double().numpy().reshape(1, n * hq, 64), kc, vc, ks, vs, np.zeros((1, 1), int), [128], [1], 128, 0.125)
+    want, weight = want.reshape(n, hq, 64), weight.reshape(n, hq, 64)
+    sums = 2 * 2.0 ** -24 * 2 ** 31 / 16 / parts
+    K.kda_get_device_status()
+    for length, status in ((2 ** 31 - 4096, 0), (2 ** 31 - 1, 1)):
+        ln = torch.tensor([length], dtype=torch.int32, device="cuda")
+        got = K.kda_kvcache_attention(q.cuda(), *cache[:4], table, ln, cu_tokens=cu_of([n]), scale=0.125).double().cpu().numpy()
+        assert K.kda_get_device_status() == status
+        assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + (2.0 ** -10 + sums) * weight + 1e-6).all()
