@@ -32,9 +32,11 @@
 // and joining in shared memory at every item's end the loads paused there: 147 us instead of
 // 133 for 64 rows of up to 8192 tokens, 8 heads.  Asking L2 for codes two to eight slabs ahead
 // made it 1 to 35% slower, slabs of 16 keys with four CTAs an SM 5%, two CTAs without spills
-// 10%.)  Bound by HBM: that call takes 125 us, 0.85 of its bytes at the copy rate (718 MB), the join
-// and its tail with it; 4 rows of up to 131072 tokens, 4 heads, 67 us, 0.78; one row of 1000
-// tokens 8 us, two launches' latency.
+// 10%.)  Bound by HBM: that call takes 127 us, 0.83 of its bytes at the copy rate (718 MB), the join
+// and its tail with it; 4 rows of up to 131072 tokens, 4 heads, 68 us, 0.78; one row of 1000
+// tokens 8 us, two launches' latency.  16 columns, and head_dim 64, are bound by latency: the codes under
+// way are in registers, of which 16 columns leave eight warps an SM (85 rows of up to 7582 tokens, 32 heads
+// of 64 over 2: 51 us, 0.32 of its bytes; 64 rows of up to 8192, 64 heads of 64 over 8: 79 us, 0.67).
 #include "kda_kvcache_attention.cuh"
 
 namespace kda {
@@ -552,7 +554,8 @@ int resident_cols(int cols) {
 // calls, with two warps for an item of 16 and at most 256 keys of an item for a warp: 128 pairs, 4, 8,
 // 500: 12 / 15, 19 / 21; 96 pairs, 16, 4, 500: 16 / 18, 23 / 27; 128 pairs, 1, 1, 30000: 22 / 22, 25 / 28; with
 // more items than that 64 pairs, 111, 2, 40: 14 / 11, 25 / 16.  (Of the cached tokens the host knows what
-// the tables have places for.)
+// the tables have places for: where those are 32768 and more, calls like these small ones take the second
+// figure.)
 constexpr int kFewRows = 32, kFewKeys = 256;
 int attention_cols(const CacheParams& c, int32_t group, int sm_count) {
     const int64_t each = (c.tokens + c.rows - 1) / c.rows * group;

@@ -12,7 +12,7 @@
 // first of which issues the matrix instructions as well (a ninth warp for that left 96 registers
 // a thread and spills); two CTAs an SM.  S(j + 1) is computed and V(j) widened while the softmax
 // of tile j runs.  (One kind of warps for everything, two threads a row, took 4300 cycles a tile:
-// 1000 of them issuing, the rest waiting for each other at three barriers; 159 us instead of 87 for 8 pieces of up to 512
+// 1000 of them issuing, the rest waiting for each other at three barriers; 159 us instead of 88 for 8 pieces of up to 512
 // tokens, 16 heads of 64 over 4, 4096 cached.  Eight widening warps: 102; two softmax groups: 105
 // and 108.)
 // O is rescaled only when a row's maximum has grown by more than 2^8 over the one in use (a published
@@ -22,7 +22,7 @@
 //
 // Bound by issue and latency: a tile takes each of an SM's two CTAs 2700 cycles (head_dim 128: 4700),
 // nearly all of them work of both kinds of warps, 55% of the issue slots and 21% of the tensor
-// cores' cycles.  The call above takes 87 us, 397 TFLOP/s; with heads of 128 151 us, 458.
+// cores' cycles.  The call above takes 88 us, 393 TFLOP/s; with heads of 128 151 us, 456.
 //
 // Work split as in kda_kvcache_attention.cu, by tiles that are seen: the CTAs (two an SM) take
 // equal contiguous shares of all tiles of all items, and the parts are joined by a second launch.

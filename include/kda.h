@@ -369,7 +369,7 @@ typedef struct kda_kvcache {
  * cu_tokens[r] .. cu_tokens[r + 1] - 1 of k and v at positions lens[r], lens[r] + 1, ...
  * Per touched page and head, with a the largest finite magnitude among its new values: a page
  * whose first token is among them gets scale a / 448 (whatever it held before); an open
- * page keeps its scale s where a <= 448 s, and otherwise takes a / 448, its older codes
+ * page keeps its scale s where a / 448 <= s, and otherwise takes a / 448, its older codes
  * rounded again for it.  Quotients are IEEE fp32, codes rounded to nearest even.
  * Infinities are stored as +-448, NaN as 0; both record KDA_ERR_NONFINITE.
  *   k, v          device [num_tokens][num_kv_heads][head_dim], token stride in elements (a
@@ -390,7 +390,8 @@ kda_status kda_kvcache_append(const kda_kvcache* cache, const void* k, const voi
  *     o = sum_j softmax_j(scale * q . k_j) v_j,
  * zero where it sees none.  Query head h reads key/value head h / (num_q_heads /
  * num_kv_heads).  Sums are fp32; the softmax weights are rounded to fp16 for the product with
- * the codes.
+ * the codes: by 2^-11 of themselves, or, of weights times v scales below 2^-21 of the row's largest, by up
+ * to 2^-32 of that.
  *   q, out        device [num_tokens][num_q_heads][head_dim] of act_dtype, token strides in
  *                 elements (multiples of 8), 16-byte aligned; out must not overlap any input
  *   lens          device int32 [rows]; more than the table has places for, or than 2^31 - 4096, is
