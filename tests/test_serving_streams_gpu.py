@@ -282,3 +282,25 @@ def test_scratch_of_a_callers_allocator():
     assert beam_call(lib, x, scores, out, stream) == 0
     torch.cuda.synchronize()
     assert all(torch.equal(p, q) for p, q in zip(out, want))
+
+
+def test_per_thread_default_streams_share_no_scratch():
+    # one handle for the streams of all threads
+    lib = K.load_library()
+    gen = torch.Generator("cuda").manual_seed(8)
+    xs, scores = torch.randn(4, 1, 4, 20000, device="cuda", generator=gen), torch.zeros(1, 4, device="cuda")
+    want = [K.kda_beam_select(x, scores) for x in xs]
+    outs = [[beam_out(1, 4) for _ in range(300)] for _ in xs]
+    torch.cuda.synchronize()
+
+    def work(i):
+        for o in outs[i]:
+            assert beam_call(lib, xs[i], scores, o, 2) == 0
+
+    with ThreadPoolExecutor(len(xs)) as pool:
+        list(pool.map(work, range(len(xs))))
+    got = K.kda_beam_select(xs[0], scores, stream=2)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert all(torch.equal(a, b) for x in o for a, b in zip(x, w))
+    assert all(torch.equal(a, b) for a, b in zip(got, want[0]))
