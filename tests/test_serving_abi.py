@@ -7,7 +7,8 @@ import torch
 
 import chunked_kda_delta_gb300 as K
 from chunked_kda_delta_gb300 import build as kbuild
-from chunked_kda_delta_gb300.kda import KdaKvCache, KdaPageShape, KdaPool, KdaScratchAllocator, KdaShape
+from chunked_kda_delta_gb300.kda import KdaKvCache, KdaPageShape, KdaPool, KdaShape
+from chunked_kda_delta_gb300.kda import KdaScratchAllocator
 
 # Calls that pass validation go on with made-up addresses: they must not reach a GPU.
 pytestmark = pytest.mark.skipif(torch.cuda.is_available(), reason="made-up device addresses")
