@@ -32,6 +32,7 @@ from .serving import (  # noqa: F401
     kda_pages_compact,
     kda_pages_copy,
     kda_kvcache_append,
+    kda_kvcache_append_rotary,
     kda_kvcache_attention,
     kda_beam_select,
 )

@@ -378,6 +378,42 @@ PyObject* kvcache_append(PyObject* const* a) {
     Py_RETURN_NONE;
 }
 
+// (q, k, v, rotary, k_codes, v_codes, k_scale, v_scale, tables, lens, cu_tokens, positions, interleaved, out, stream)
+PyObject* kvcache_append_rotary(PyObject* const* a) {
+    const Cache x = cache_of(a + 4);
+    const Tensor& q = tensor(a[0], "q");
+    const Tensor& k = tensor(a[1], "k");
+    const Tensor& v = tensor(a[2], "v");
+    if (k.scalar_type() != v.scalar_type() || k.sizes() != v.sizes()) refuse("k and v must have the same type and shape");
+    const int32_t type = act_type(q, "q", x.device);
+    if (k.scalar_type() != q.scalar_type()) refuse("q and k must have the same type");
+    act_type(k, "k", x.device);
+    act_type(v, "v", x.device);
+    const int64_t qs = act_stride(q, "q", -1, x.c.head_dim), ks = act_stride(k, "k", x.c.num_kv_heads, x.c.head_dim),
+                  vs = act_stride(v, "v", x.c.num_kv_heads, x.c.head_dim);
+    if (q.size(1) > INT32_MAX) refuse("q has too many heads");
+    if (q.size(0) != k.size(0)) refuse("q and k must have the same tokens");
+    const Tensor& table = tensor(a[3], "rotary");
+    if (table.dim() != 2 || table.size(1) > INT32_MAX) refuse("rotary must be [positions, rotary_dim]");
+    vector(a[3], "rotary", {ScalarType::Float}, table.sizes(), x.device);
+    const int32_t* positions = given(a[11]) ? ptr<int32_t>(vector(a[11], "positions", {ScalarType::Int}, {q.size(0)}, x.device)) : nullptr;
+    const int interleaved = PyObject_IsTrue(a[12]);
+    if (interleaved < 0) throw python_error();
+    Place on(x.device, a[14]);
+    Tensor out;
+    if (given(a[13])) {
+        out = tensor(a[13], "out");
+        if (out.scalar_type() != q.scalar_type() || out.sizes() != q.sizes()) refuse("out must have q's type and shape");
+        act_type(out, "out", x.device);
+    } else {
+        out = on.empty(q.sizes(), q.scalar_type());
+    }
+    const int64_t os = act_stride(out, "out", q.size(1), x.c.head_dim);
+    check(kda_kvcache_append_rotary(&x.c, q.data_ptr(), k.data_ptr(), v.data_ptr(), (int32_t)q.size(1), type, qs, ks, vs, q.size(0), x.lens, x.cu,
+                                    ptr<float>(table), table.size(0), (int32_t)table.size(1), interleaved, positions, out.data_ptr(), os, on.stream));
+    return THPVariable_Wrap(out);
+}
+
 // (q, k_codes, v_codes, k_scale, v_scale, tables, lens, cu_tokens, scale, out, stream)
 PyObject* kvcache_attention(PyObject* const* a) {
     const Cache x = cache_of(a + 1);
@@ -468,6 +504,7 @@ PyMethodDef methods[] = {
     method<pages_compact, 7>("pages_compact"),
     method<pages_copy, 5>("pages_copy"),
     method<kvcache_append, 10>("kvcache_append"),
+    method<kvcache_append_rotary, 15>("kvcache_append_rotary"),
     method<kvcache_attention, 11>("kvcache_attention"),
     method<beam_select, 6>("beam_select"),
     PyMethodDef{nullptr, nullptr, 0, nullptr},

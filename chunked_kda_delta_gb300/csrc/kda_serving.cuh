@@ -122,6 +122,19 @@ struct AppendParams {
     int64_t stride[2];
 };
 cudaError_t launch_append(const AppendParams& p, bool f16, cudaStream_t stream);
+// With the positions' rotation (kda_kvcache_rotary.cu).
+struct RotaryParams : AppendParams {
+    const void* q;
+    void* q_out;              // may be q, at q's stride
+    int64_t q_stride, out_stride;
+    int32_t q_heads;
+    const float* table;       // [num_positions][rot]: cosines, then sines
+    const int32_t* positions; // [tokens] or nullptr: places in the cache
+    int64_t num_positions;
+    int32_t rot;              // multiple of 16
+    bool interleaved;
+};
+cudaError_t launch_rotary_append(const RotaryParams& p, bool f16, cudaStream_t stream);
 
 struct AttentionParams {
     CacheParams c;

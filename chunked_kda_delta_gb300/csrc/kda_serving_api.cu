@@ -1,6 +1,7 @@
 // kda_serving_api.cu -- the C ABI of the serving operators: page operations, the 8-bit
 // key/value cache and beam selection.  Validation, scratch layout and launches; the kernels
-// live in kda_pages.cu, kda_kvcache_append.cu, kda_kvcache_attention.cu and kda_beam.cu.
+// live in kda_pages.cu, kda_kvcache_append.cu, kda_kvcache_rotary.cu, kda_kvcache_attention.cu and
+// kda_beam.cu.
 #include <math.h>
 
 #include <exception>
@@ -175,6 +176,17 @@ kda::PagePlan plan_of(const kda_page_shape* s, const int32_t* tables, const int3
 
 // Bytes a strided [n][inner] activation spans.
 size_t span(int64_t n, int64_t stride, int64_t inner) { return n > 0 ? (size_t)((n - 1) * stride + inner) * 2 : 0; }
+
+// Strided activations [n][inner] that share memory.  Those of one stride, heads of a fused projection
+// for instance, may lie between each other.
+bool strided_overlap(const void* a, int64_t a_stride, int64_t a_inner, const void* b, int64_t b_stride, int64_t b_inner, int64_t n) {
+    if (!overlaps({a, span(n, a_stride, a_inner)}, {b, span(n, b_stride, b_inner)})) return false;
+    if (a_stride != b_stride) return true;
+    const int64_t step = a_stride * 2;
+    int64_t d = ((int64_t)(uintptr_t)b - (int64_t)(uintptr_t)a) % step;  // b's rows start here within a's
+    if (d < 0) d += step;
+    return d < a_inner * 2 || d + b_inner * 2 > step;
+}
 
 kda_status check_cache(const kda_kvcache* c, int64_t num_tokens, const int32_t* lens, const int32_t* cu) {
     if (!c) return fail(KDA_ERR_INVALID_ARGUMENT, "cache is NULL");
@@ -362,6 +374,73 @@ kda_status kda_kvcache_append(const kda_kvcache* cache, const void* k, const voi
         p.stride[1] = v_stride;
         const cudaError_t e = kda::launch_append(p, act_dtype == KDA_ACT_F16, (cudaStream_t)stream);
         return e == cudaSuccess ? KDA_OK : cuda_fail(e, "cache append launch");
+    });
+}
+
+kda_status kda_kvcache_append_rotary(const kda_kvcache* cache, const void* q, const void* k, const void* v,
+                                     int32_t num_q_heads, int32_t act_dtype, int64_t q_stride,
+                                     int64_t k_stride, int64_t v_stride, int64_t num_tokens,
+                                     const int32_t* lens, const int32_t* cu_tokens, const float* rotary,
+                                     int64_t num_positions, int32_t rotary_dim, int32_t interleaved,
+                                     const int32_t* positions, void* q_out, int64_t out_stride,
+                                     void* stream) {
+    return guarded([&] {
+        kda_status st = check_cache(cache, num_tokens, lens, cu_tokens);
+        if (st != KDA_OK) return st;
+        if (act_dtype != KDA_ACT_BF16 && act_dtype != KDA_ACT_F16)
+            return fail(KDA_ERR_INVALID_ARGUMENT, "unknown act_dtype %d", act_dtype);
+        if (num_q_heads < 1 || num_q_heads > (1 << 16))
+            return fail(KDA_ERR_INVALID_ARGUMENT, "num_q_heads must be in [1, 2^16] (got %d)", num_q_heads);
+        if (rotary_dim < 16 || rotary_dim % 16 != 0 || rotary_dim > cache->head_dim)
+            return fail(KDA_ERR_INVALID_ARGUMENT, "rotary_dim must be a multiple of 16 in [16, head_dim] (got %d)", rotary_dim);
+        if (num_positions < 0 || num_positions > (int64_t)1 << 31)
+            return fail(KDA_ERR_INVALID_ARGUMENT, "num_positions must be in [0, 2^31] (got %lld)", (long long)num_positions);
+        const int64_t inner = (int64_t)cache->num_kv_heads * cache->head_dim, q_inner = (int64_t)num_q_heads * cache->head_dim;
+        if ((st = check_act("q", q, num_tokens, q_stride, q_inner)) || (st = check_act("k", k, num_tokens, k_stride, inner)) ||
+            (st = check_act("v", v, num_tokens, v_stride, inner)) || (st = check_act("q_out", q_out, num_tokens, out_stride, q_inner)))
+            return st;
+        const size_t table = (size_t)num_positions * rotary_dim * 4;
+        if ((st = check_pointer("rotary", rotary, table, 16))) return st;
+        if (positions && !aligned(positions, 4)) return fail(KDA_ERR_INVALID_ARGUMENT, "positions is not 4-byte aligned");
+        const size_t blocks = (size_t)cache->pages * cache->num_kv_heads, codes = blocks * cache->page_tokens * cache->head_dim;
+        const Range out_r{q_out, span(num_tokens, out_stride, q_inner)};
+        const Buffer tables{"tables", {cache->tables, (size_t)cache->rows * cache->width * 4}}, lens_b{"lens", {lens, (size_t)cache->rows * 4}},
+            cu_b{"cu_tokens", {cu_tokens, ((size_t)cache->rows + 1) * 4}}, rotary_b{"rotary", {rotary, table}},
+            positions_b{"positions", {positions, (size_t)num_tokens * 4}};
+        if ((st = check_overlap({{"k_codes", {cache->k_codes, codes}}, {"v_codes", {cache->v_codes, codes}},
+                                 {"k_scale", {cache->k_scale, blocks * 4}}, {"v_scale", {cache->v_scale, blocks * 4}}},
+                                {{"q", {q, span(num_tokens, q_stride, q_inner)}}, {"k", {k, span(num_tokens, k_stride, inner)}},
+                                 {"v", {v, span(num_tokens, v_stride, inner)}}, {"q_out", out_r}, tables, lens_b, cu_b, rotary_b, positions_b})) ||
+            (st = check_overlap({{"q_out", out_r}}, {tables, lens_b, cu_b, rotary_b, positions_b})))
+            return st;
+        if (strided_overlap(q_out, out_stride, q_inner, k, k_stride, inner, num_tokens)) return fail(KDA_ERR_ALIASING, "q_out overlaps k");
+        if (strided_overlap(q_out, out_stride, q_inner, v, v_stride, inner, num_tokens)) return fail(KDA_ERR_ALIASING, "q_out overlaps v");
+        if ((q_out != q || out_stride != q_stride) && strided_overlap(q_out, out_stride, q_inner, q, q_stride, q_inner, num_tokens))
+            return fail(KDA_ERR_ALIASING, "q_out overlaps q");
+        const int64_t units = cu_tokens ? num_tokens / cache->page_tokens + 2ll * cache->rows : 0;
+        if (units > 0x7fffffff || 2 * num_tokens * cache->num_kv_heads > 0x7fffffffll * 2 || num_tokens * num_q_heads > 0x7fffffffll * 4)
+            return fail(KDA_ERR_INVALID_ARGUMENT, "too many tokens for one launch");
+        int dev = 0;
+        DeviceInfo* di = nullptr;
+        if ((st = current_device(&dev, &di)) != KDA_OK) return st;
+        kda::RotaryParams p{};
+        p.c = cache_params(cache, num_tokens, lens, cu_tokens, di->status);
+        p.x[0] = k;
+        p.x[1] = v;
+        p.stride[0] = k_stride;
+        p.stride[1] = v_stride;
+        p.q = q;
+        p.q_out = q_out;
+        p.q_stride = q_stride;
+        p.out_stride = out_stride;
+        p.q_heads = num_q_heads;
+        p.table = rotary;
+        p.positions = positions;
+        p.num_positions = num_positions;
+        p.rot = rotary_dim;
+        p.interleaved = interleaved != 0;
+        const cudaError_t e = kda::launch_rotary_append(p, act_dtype == KDA_ACT_F16, (cudaStream_t)stream);
+        return e == cudaSuccess ? KDA_OK : cuda_fail(e, "rotary append launch");
     });
 }
 

@@ -131,6 +131,25 @@ def kda_kvcache_append(k: torch.Tensor, v: torch.Tensor, k_codes: torch.Tensor,
                                         cu_tokens, _handle(stream))
 
 
+def kda_kvcache_append_rotary(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, rotary: torch.Tensor,
+                              k_codes: torch.Tensor, v_codes: torch.Tensor, k_scale: torch.Tensor,
+                              v_scale: torch.Tensor, tables: torch.Tensor, lens: torch.Tensor,
+                              cu_tokens: Optional[torch.Tensor] = None,
+                              positions: Optional[torch.Tensor] = None, interleaved: bool = False,
+                              out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """:func:`kda_kvcache_append` with the rotation of positions on the way; returns the rotated q.
+
+    q: ``[tokens, q_heads, head_dim]`` of k's type; ``rotary``: fp32 ``[positions, rotary_dim]``, a
+    position's ``rotary_dim / 2`` cosines and then as many sines (any scaling of angles is in there);
+    rotary_dim: a multiple of 16 up to head_dim, channels past it stay as they are.  Pairs lie
+    rotary_dim / 2 apart, or side by side with ``interleaved``.  ``positions`` (int32 ``[tokens]``):
+    each token's row of ``rotary``; without it its place in the cache.  ``out`` may be q itself, and
+    may have a token stride of its own.
+    """
+    return (_ext or _binding()).kvcache_append_rotary(q, k, v, rotary, k_codes, v_codes, k_scale, v_scale, tables, lens,
+                                                      cu_tokens, positions, interleaved, out, _handle(stream))
+
+
 def kda_kvcache_attention(q: torch.Tensor, k_codes: torch.Tensor, v_codes: torch.Tensor,
                           k_scale: torch.Tensor, v_scale: torch.Tensor, tables: torch.Tensor,
                           lens: torch.Tensor, cu_tokens: Optional[torch.Tensor] = None,

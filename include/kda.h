@@ -384,6 +384,31 @@ kda_status kda_kvcache_append(const kda_kvcache* cache, const void* k, const voi
                               int64_t num_tokens, const int32_t* lens, const int32_t* cu_tokens,
                               void* stream);
 
+/* kda_kvcache_append_rotary -- kda_kvcache_append with the rotation of positions on the way, and the
+ * rotated queries.  In every head of q and k the pairs of the first rotary_dim channels turn by
+ * their token's angles, of which row x of `rotary` has the cosines and then the sines:
+ *     a' = a cos - b sin,  b' = b cos + a sin
+ * with pair i (i, i + rotary_dim / 2), or with interleaved (2 i, 2 i + 1); the other channels stay.
+ * fp32 with an error of at most 2 units in the last place of the result.  Rotated keys are quantised
+ * from these fp32 values by the append's rules; queries are rounded once to act_dtype.
+ *   q, q_out       device [num_tokens][num_q_heads][head_dim] of act_dtype, token strides in elements
+ *                  (multiples of 8), 16-byte aligned.  q_out may be q (with its stride); else it
+ *                  must not overlap any input or the cache
+ *   rotary         device fp32 [num_positions][rotary_dim], 16-byte aligned
+ *   rotary_dim     multiple of 16, at most head_dim
+ *   positions      device int32 [num_tokens]: each token's row of `rotary`; NULL: its place in the
+ *                  cache.  Tokens with a position outside of the table are not turned, and recorded as
+ *                  KDA_ERR_INVALID_ARGUMENT
+ * Tokens without a page are dropped and recorded, their queries turned all the same.  Everything else as
+ * kda_kvcache_append. */
+kda_status kda_kvcache_append_rotary(const kda_kvcache* cache, const void* q, const void* k, const void* v,
+                                     int32_t num_q_heads, int32_t act_dtype, int64_t q_stride,
+                                     int64_t k_stride, int64_t v_stride, int64_t num_tokens,
+                                     const int32_t* lens, const int32_t* cu_tokens, const float* rotary,
+                                     int64_t num_positions, int32_t rotary_dim, int32_t interleaved,
+                                     const int32_t* positions, void* q_out, int64_t out_stride,
+                                     void* stream);
+
 /* kda_kvcache_attention -- causal attention of new tokens over the cache.  Row r has lens[r]
  * tokens in the cache, its query tokens cu_tokens[r] .. cu_tokens[r + 1] - 1 among them as the
  * last ones: token i of n sits at position p = lens[r] - n + i and sees keys 0 .. p,

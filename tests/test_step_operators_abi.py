@@ -1,0 +1,63 @@
+"""Host-side refusals of a decoding step's operators: bad arguments are rejected with the documented
+status before any device work."""
+import ctypes
+
+import pytest
+import torch
+
+import chunked_kda_delta_gb300 as K
+from chunked_kda_delta_gb300 import build as kbuild
+from chunked_kda_delta_gb300.kda import KdaKvCache
+
+# Calls that pass validation go on with made-up addresses: they must not reach a GPU.
+pytestmark = pytest.mark.skipif(torch.cuda.is_available(), reason="made-up device addresses")
+
+INVALID, ALIAS = 1, 2
+P = lambda x: None if x is None else ctypes.c_void_p(x)  # noqa: E731
+
+
+@pytest.fixture(scope="module")
+def lib():
+    kbuild.build()
+    return K.load_library()
+
+
+def cache(**over):
+    a = dict(k=0x10000000, v=0x20000000, ks=0x30000000, vs=0x40000000, pages=8, page=16, heads=2, dim=64, tables=0x50000000, rows=3, width=4)
+    a.update(over)
+    return KdaKvCache(a["k"], a["v"], a["ks"], a["vs"], a["pages"], a["page"], a["heads"], a["dim"], a["tables"], a["rows"], a["width"])
+
+
+def rotary(lib, c=None, q=0x60000000, k=0x61000000, v=0x62000000, hq=4, act=0, qs=256, ks=128, vs=128, n=3, lens=0x70000000, cu=None,
+           table=0x71000000, positions=100, rot=64, inter=0, at=None, out=0x72000000, os=256):
+    return lib.kda_kvcache_append_rotary(ctypes.byref(c or cache()), P(q), P(k), P(v), hq, act, qs, ks, vs, n, P(lens), P(cu), P(table), positions,
+                                         rot, inter, P(at), P(out), os, None)
+
+
+def test_rotary_rules(lib):
+    assert rotary(lib) not in (INVALID, ALIAS)
+    for bad in (dict(page=24), dict(dim=96), dict(heads=0), dict(pages=-1), dict(rows=-1), dict(width=0), dict(k=None), dict(v=0x20000008),
+                dict(ks=None), dict(vs=0x40000002), dict(tables=None)):
+        assert rotary(lib, c=cache(**bad)) == INVALID, bad
+    for bad in (dict(act=2), dict(hq=0), dict(hq=1 << 17), dict(n=4), dict(n=-1, cu=0x73000000), dict(cu=0x73000002), dict(lens=None), dict(q=None),
+                dict(q=0x60000008), dict(qs=128), dict(qs=260), dict(ks=64), dict(vs=132), dict(k=None), dict(v=0x62000002), dict(out=None),
+                dict(out=0x72000008), dict(os=128), dict(table=None), dict(table=0x71000004), dict(rot=0), dict(rot=24), dict(rot=80), dict(rot=-16),
+                dict(positions=-1), dict(positions=1 << 40), dict(at=0x73000002)):
+        assert rotary(lib, **bad) == INVALID, bad
+    assert rotary(lib, hq=5, qs=320, os=320) not in (INVALID, ALIAS)       # any number of query heads
+    assert rotary(lib, table=None, positions=0) not in (INVALID, ALIAS)
+
+
+def test_rotary_overlaps(lib):
+    assert rotary(lib, out=0x60000000) not in (INVALID, ALIAS)              # in place
+    assert rotary(lib, out=0x60000000, os=264) == ALIAS                     # at another stride
+    for bad in (dict(out=0x60000010), dict(out=0x61000000), dict(out=0x62000010), dict(out=0x10000000), dict(out=0x30000000), dict(out=0x50000000),
+                dict(out=0x70000000), dict(out=0x71000000), dict(at=0x73000000, out=0x73000000), dict(k=0x10000000), dict(q=0x20000000),
+                dict(table=0x10000000), dict(at=0x30000000)):
+        assert rotary(lib, **bad) == ALIAS, bad
+    # heads of one fused projection [tokens][q 4, k 2, v 2]: q in place between its neighbours
+    fused = dict(q=0x60000000, k=0x60000000 + 512, v=0x60000000 + 768, qs=512, ks=512, vs=512, os=512)
+    assert rotary(lib, out=0x60000000, **fused) not in (INVALID, ALIAS)
+    assert rotary(lib, out=0x60000000 + 128, **fused) == ALIAS
+    assert rotary(lib, out=0x60000000 - 128, **fused) == ALIAS
+    assert rotary(lib, out=0x60000000 - 512, **dict(fused, os=1024)) == ALIAS
