@@ -34,5 +34,6 @@ from .serving import (  # noqa: F401
     kda_kvcache_append,
     kda_kvcache_append_rotary,
     kda_kvcache_attention,
+    kda_logits_penalize,
     kda_beam_select,
 )

@@ -1,5 +1,5 @@
 // serving_binding.cpp -- argument marshalling of the serving operators (page operations, 8-bit
-// key/value cache, beam selection) as a CPython extension on torch tensors.
+// key/value cache, penalties on logits, beam selection) as a CPython extension on torch tensors.
 //
 // Every function checks its tensors (type, layout, shape, device), allocates what it returns, and
 // makes one call of the C ABI in include/kda.h on the given or the current stream; all of the
@@ -441,6 +441,94 @@ PyObject* kvcache_attention(PyObject* const* a) {
     return THPVariable_Wrap(out);
 }
 
+// ---- logits ----------------------------------------------------------------------------
+// Rows of logits [..., vocab] at one stride.
+struct Rows {
+    IntArrayRef lead;
+    int64_t n, vocab, stride;
+};
+Rows rows_of(const Tensor& x, const char* name) {
+    const int64_t dims = x.dim();
+    Rows r{x.sizes().slice(0, dims - 1), 1, x.size(dims - 1), 0};
+    for (int64_t d : r.lead) r.n *= d;
+    r.stride = r.vocab;
+    if (!r.n) return r;
+    bool ok = r.vocab <= 1 || x.stride(dims - 1) == 1, first = true;
+    int64_t next = 0;  // stride of the dimension before
+    for (int64_t d = dims - 2; d >= 0; --d) {
+        if (x.size(d) == 1) continue;
+        if (first) next = r.stride = x.stride(d);
+        ok &= x.stride(d) == next;
+        next *= x.size(d);
+        first = false;
+    }
+    if (!ok) refuse(std::string(name) + " must have contiguous rows at one stride");
+    return r;
+}
+// A contiguous tensor [..., (width)] with logits' leading dimensions, which may be one; its width.
+const Tensor* per_row(PyObject* o, const char* name, ScalarType type, const Rows& rows, bool wide, int64_t& width, const at::Device& device) {
+    if (!given(o)) return nullptr;
+    const Tensor& t = tensor(o, name);
+    const int64_t lead = t.dim() - (wide ? 1 : 0);
+    bool ok = t.device() == device && t.is_contiguous() && t.scalar_type() == type;
+    ok = ok && (lead == 1 ? t.size(0) == rows.n : lead == (int64_t)rows.lead.size() && t.sizes().slice(0, lead) == rows.lead);
+    if (!ok)
+        refuse(std::string(name) + " must be a contiguous " + c10::toString(type) + " tensor on " + device.str() + " with logits' " +
+               std::to_string(rows.n) + " rows" + (wide ? " in its leading dimensions" : ""));
+    if (wide) width = t.size(t.dim() - 1);
+    return &t;
+}
+
+// (logits, history, lens, prompt_lens, repetition, presence, frequency, bias_tokens, bias, mask, out, stream)
+PyObject* logits_penalize(PyObject* const* a) {
+    const Tensor& x = tensor(a[0], "logits");
+    const ScalarType type = x.scalar_type();
+    if (!x.is_cuda() || x.dim() < 1 || (type != ScalarType::Float && type != ScalarType::BFloat16 && type != ScalarType::Half))
+        refuse("logits must be fp32, bf16 or fp16 [..., vocab] on cuda");
+    const at::Device device = x.device();
+    const Rows rows = rows_of(x, "logits");
+    if (rows.n > INT32_MAX || rows.vocab > INT32_MAX) refuse("logits are too large");
+    int64_t width = 0, biases = 0, values = 0, words = 0, none = 0;
+    const Tensor* history = per_row(a[1], "history", ScalarType::Int, rows, true, width, device);
+    const Tensor* lens = per_row(a[2], "lens", ScalarType::Int, rows, false, none, device);
+    const Tensor* prompt = per_row(a[3], "prompt_lens", ScalarType::Int, rows, false, none, device);
+    const Tensor* repetition = per_row(a[4], "repetition", ScalarType::Float, rows, false, none, device);
+    const Tensor* presence = per_row(a[5], "presence", ScalarType::Float, rows, false, none, device);
+    const Tensor* frequency = per_row(a[6], "frequency", ScalarType::Float, rows, false, none, device);
+    const Tensor* bias_tokens = per_row(a[7], "bias_tokens", ScalarType::Int, rows, true, biases, device);
+    const Tensor* bias = per_row(a[8], "bias", ScalarType::Float, rows, true, values, device);
+    const Tensor* mask = per_row(a[9], "mask", ScalarType::Int, rows, true, words, device);
+    if (!history && (lens || prompt || repetition || presence || frequency)) refuse("lengths and penalties need a history");
+    if (!bias_tokens != !bias || biases != values) refuse("bias_tokens and bias must have the same shape");
+    if (width > INT32_MAX || biases > INT32_MAX) refuse("history or bias is too wide");
+    if (mask && words < (rows.vocab + 31) / 32) refuse("mask must have " + std::to_string((rows.vocab + 31) / 32) + " words a row");
+    Place on(device, a[11]);
+    Tensor out;
+    int64_t stride = rows.vocab;
+    if (given(a[10])) {
+        out = tensor(a[10], "out");
+        if (out.scalar_type() != type || out.sizes() != x.sizes() || out.device() != device) refuse("out must have logits' type, shape and device");
+        stride = rows_of(out, "out").stride;
+    } else if (rows.n && rows.stride != rows.vocab) {
+        // Padded rows give padded rows: each starts on 16 bytes.
+        const int64_t each = 16 / (int64_t)x.element_size();
+        stride = (rows.vocab + each - 1) / each * each;
+        std::vector<int64_t> shape(rows.lead.begin(), rows.lead.end());
+        shape.push_back(stride);
+        out = on.empty(shape, type).narrow((int64_t)shape.size() - 1, 0, rows.vocab);
+    } else {
+        out = on.empty(x.sizes(), type);
+    }
+    auto ints = [](const Tensor* t) { return t ? ptr<int32_t>(*t) : nullptr; };
+    auto floats = [](const Tensor* t) { return t ? ptr<float>(*t) : nullptr; };
+    const kda_logits_rules rules{ints(history), ints(lens), ints(prompt), floats(repetition), floats(presence), floats(frequency), ints(bias_tokens),
+                                 floats(bias), ints(mask), words, (int32_t)width, (int32_t)biases};
+    check(kda_logits_penalize(&rules, rows.n, (int32_t)rows.vocab, x.data_ptr(),
+                              type == ScalarType::Float ? KDA_LOGITS_F32 : type == ScalarType::BFloat16 ? KDA_LOGITS_BF16 : KDA_LOGITS_F16, rows.stride,
+                              out.data_ptr(), stride, on.stream));
+    return THPVariable_Wrap(out);
+}
+
 // ---- beam selection --------------------------------------------------------------------
 // (logits, scores, num_out, done, eos, stream)
 PyObject* beam_select(PyObject* const* a) {
@@ -506,6 +594,7 @@ PyMethodDef methods[] = {
     method<kvcache_append, 10>("kvcache_append"),
     method<kvcache_append_rotary, 15>("kvcache_append_rotary"),
     method<kvcache_attention, 11>("kvcache_attention"),
+    method<logits_penalize, 12>("logits_penalize"),
     method<beam_select, 6>("beam_select"),
     PyMethodDef{nullptr, nullptr, 0, nullptr},
 };

@@ -179,4 +179,29 @@ struct BeamParams {
 int beam_seg_len(int64_t rows, int32_t vocab, int elem, int sm_count);
 cudaError_t launch_beam(const BeamParams& p, cudaStream_t stream);
 
+// ---- penalties, biases and masks on logits ----------------------------------------------
+struct LogitsParams {
+    const void* logits;
+    void* out;
+    int64_t stride, out_stride;
+    int64_t rows;
+    int32_t vocab;
+    const int32_t* history;   // [rows][width]
+    int32_t width;
+    const int32_t* lens;      // [rows] or nullptr
+    const int32_t* prompt_lens;
+    const float* repetition;  // [rows] or nullptr, as the next two
+    const float* presence;
+    const float* frequency;
+    const int32_t* bias_tokens;  // [rows][num_bias]
+    const float* bias;
+    int32_t num_bias;
+    const uint32_t* mask;     // [rows][mask_stride] or nullptr
+    int64_t mask_stride;
+    int32_t* status;
+    int32_t sm_count;
+    int32_t segs;             // set by the launch
+};
+cudaError_t launch_penalize(LogitsParams p, int dtype, cudaStream_t stream);
+
 }  // namespace kda

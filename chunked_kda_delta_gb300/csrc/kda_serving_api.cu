@@ -1,7 +1,7 @@
 // kda_serving_api.cu -- the C ABI of the serving operators: page operations, the 8-bit
-// key/value cache and beam selection.  Validation, scratch layout and launches; the kernels
-// live in kda_pages.cu, kda_kvcache_append.cu, kda_kvcache_rotary.cu, kda_kvcache_attention.cu and
-// kda_beam.cu.
+// key/value cache, penalties on logits and beam selection.  Validation, scratch layout and launches; the kernels
+// live in kda_pages.cu, kda_kvcache_append.cu, kda_kvcache_rotary.cu, kda_kvcache_attention.cu, kda_logits.cu
+// and kda_beam.cu.
 #include <math.h>
 
 #include <exception>
@@ -496,6 +496,77 @@ kda_status kda_kvcache_attention(const kda_kvcache* cache, const void* q, int32_
         p.scale = scale * 1.4426950408889634f;
         const cudaError_t e = kda::launch_attention(p, cols, f16, (cudaStream_t)stream);
         return e == cudaSuccess ? KDA_OK : cuda_fail(e, "cache attention launch");
+    });
+}
+
+kda_status kda_logits_penalize(const kda_logits_rules* rules, int64_t rows, int32_t vocab,
+                               const void* logits, int32_t logits_dtype, int64_t logits_stride,
+                               void* out, int64_t out_stride, void* stream) {
+    return guarded([&] {
+        if (!rules) return fail(KDA_ERR_INVALID_ARGUMENT, "rules is NULL");
+        const kda_logits_rules& r = *rules;
+        if (rows < 0 || rows > (1 << 30) || vocab < 1 || vocab > (1 << 30))
+            return fail(KDA_ERR_INVALID_ARGUMENT, "rows must be in [0, 2^30], vocab in [1, 2^30] (got %lld, %d)", (long long)rows, vocab);
+        if (logits_dtype != KDA_LOGITS_F32 && logits_dtype != KDA_LOGITS_BF16 && logits_dtype != KDA_LOGITS_F16)
+            return fail(KDA_ERR_INVALID_ARGUMENT, "unknown logits_dtype %d", logits_dtype);
+        for (const int64_t s : {logits_stride, out_stride})
+            if (s < vocab || s > (int64_t)1 << 32)
+                return fail(KDA_ERR_INVALID_ARGUMENT, "logits_stride and out_stride must be at least vocab (got %lld)", (long long)s);
+        if (r.history_width < 0 || r.history_width > (1 << 30) || r.num_bias < 0 || r.num_bias > (1 << 30))
+            return fail(KDA_ERR_INVALID_ARGUMENT, "history_width and num_bias must be in [0, 2^30] (got %d, %d)", r.history_width, r.num_bias);
+        const int64_t words = ((int64_t)vocab + 31) / 32;
+        if (r.mask && (r.mask_stride < words || r.mask_stride > (int64_t)1 << 32))
+            return fail(KDA_ERR_INVALID_ARGUMENT, "mask_stride must be at least %lld (got %lld)", (long long)words, (long long)r.mask_stride);
+        const size_t elem = logits_dtype == KDA_LOGITS_F32 ? 4 : 2, n = (size_t)rows;
+        auto bytes = [&](int64_t stride) { return rows > 0 ? (size_t)((rows - 1) * stride + vocab) * elem : 0; };
+        const size_t lb = bytes(logits_stride), ob = bytes(out_stride);
+        const size_t hb = n * r.history_width * 4, bb = n * r.num_bias * 4;
+        const size_t mb = r.mask && rows > 0 ? (size_t)((rows - 1) * r.mask_stride + words) * 4 : 0;
+        kda_status st;
+        if ((st = check_pointer("logits", logits, lb, elem)) || (st = check_pointer("out", out, ob, elem)) ||
+            (st = check_pointer("history", r.history, hb, 4)) || (st = check_pointer("bias_tokens", r.bias_tokens, bb, 4)) ||
+            (st = check_pointer("bias", r.bias, bb, 4)) || (st = check_pointer("mask", r.mask, mb, 4)))
+            return st;
+        const Buffer per_row[] = {{"lens", {r.lens, n * 4}}, {"prompt_lens", {r.prompt_lens, n * 4}}, {"repetition", {r.repetition, n * 4}},
+                                  {"presence", {r.presence, n * 4}}, {"frequency", {r.frequency, n * 4}}};
+        for (const Buffer& b : per_row)
+            if (b.r.p && !aligned(b.r.p, 4)) return fail(KDA_ERR_INVALID_ARGUMENT, "%s is not 4-byte aligned", b.name);
+        const Buffer out_b{"out", {out, ob}};
+        if ((st = check_overlap({out_b}, {{"history", {r.history, hb}}, {"bias_tokens", {r.bias_tokens, bb}}, {"bias", {r.bias, bb}}, {"mask", {r.mask, mb}},
+                                          per_row[0], per_row[1], per_row[2], per_row[3], per_row[4]})) != KDA_OK)
+            return st;
+        if ((out != logits || out_stride != logits_stride) && (st = check_overlap({out_b}, {{"logits", {logits, lb}}})) != KDA_OK) return st;
+        int dev = 0;
+        DeviceInfo* di = nullptr;
+        if ((st = current_device(&dev, &di)) != KDA_OK) return st;
+        if (rows == 0) return KDA_OK;
+        kda::LogitsParams p{};
+        p.logits = logits;
+        p.out = out;
+        p.stride = logits_stride;
+        p.out_stride = out_stride;
+        p.rows = rows;
+        p.vocab = vocab;
+        // (Without penalties a history changes nothing.)
+        const bool counted = r.repetition || r.presence || r.frequency;
+        p.history = r.history;
+        p.width = counted ? r.history_width : 0;
+        p.lens = r.lens;
+        p.prompt_lens = r.prompt_lens;
+        p.repetition = r.repetition;
+        p.presence = r.presence;
+        p.frequency = r.frequency;
+        p.bias_tokens = r.bias_tokens;
+        p.bias = r.bias;
+        p.num_bias = r.num_bias;
+        p.mask = reinterpret_cast<const uint32_t*>(r.mask);
+        p.mask_stride = r.mask_stride;
+        p.status = di->status;
+        p.sm_count = di->sm_count;
+        const cudaError_t e = kda::launch_penalize(p, logits_dtype, (cudaStream_t)stream);
+        if (e == cudaErrorInvalidValue && rows * (int64_t)vocab > (int64_t)1 << 40)
+            return fail(KDA_ERR_INVALID_ARGUMENT, "rows * vocab is too large for one launch");
+        return e == cudaSuccess ? KDA_OK : cuda_fail(e, "logits penalties launch");
     });
 }
 

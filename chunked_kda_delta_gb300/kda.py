@@ -35,8 +35,8 @@ EXPORTED_SYMBOLS = (
     "kda_last_error_message", "kda_version", "kda_prefill_segment_noalloc", "kda_plan",
     "kda_plan_varlen", "kda_decode", "kda_decode_paged", "kda_pages_alloc", "kda_pages_free",
     "kda_pages_fork", "kda_pages_compact", "kda_pages_copy", "kda_kvcache_append",
-    "kda_kvcache_append_rotary",
-    "kda_kvcache_attention", "kda_beam_select", "kda_set_scratch_allocator",
+    "kda_kvcache_append_rotary", "kda_kvcache_attention", "kda_logits_penalize",
+    "kda_beam_select", "kda_set_scratch_allocator",
 )
 
 STATE_F32 = 0
@@ -80,6 +80,12 @@ class KdaKvCache(ctypes.Structure):
                 ("pages", ctypes.c_int32), ("page_tokens", ctypes.c_int32),
                 ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("tables", ctypes.c_void_p), ("rows", ctypes.c_int32), ("width", ctypes.c_int32)]
+
+
+class KdaLogitsRules(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("history", "lens", "prompt_lens", "repetition", "presence", "frequency", "bias_tokens",
+                                               "bias", "mask")] + [
+        ("mask_stride", ctypes.c_int64), ("history_width", ctypes.c_int32), ("num_bias", ctypes.c_int32)]
 
 
 class KdaScratchAllocator(ctypes.Structure):
@@ -140,6 +146,7 @@ def load_library(path: Optional[str] = None, build_if_missing: bool = False) -> 
                                                   vp, i64, vp]
         lib.kda_kvcache_attention.argtypes = [cache, vp, i32, i32, i64, i64, vp, vp, f32, vp, i64,
                                               vp]
+        lib.kda_logits_penalize.argtypes = [ctypes.POINTER(KdaLogitsRules), i64, i32, vp, i32, i64, vp, i64, vp]
         lib.kda_beam_select.argtypes = [i32, i32, i32, i32, vp, i32, i64, vp, vp, i32, vp, vp, vp,
                                         vp, vp]
         lib.kda_set_scratch_allocator.argtypes = [ctypes.POINTER(KdaScratchAllocator),
@@ -156,7 +163,7 @@ def load_library(path: Optional[str] = None, build_if_missing: bool = False) -> 
                   lib.kda_release_workspaces, lib.kda_decode_paged, lib.kda_pages_alloc,
                   lib.kda_pages_free, lib.kda_pages_fork, lib.kda_pages_compact,
                   lib.kda_pages_copy, lib.kda_kvcache_append, lib.kda_kvcache_append_rotary,
-                  lib.kda_kvcache_attention,
+                  lib.kda_kvcache_attention, lib.kda_logits_penalize,
                   lib.kda_beam_select, lib.kda_set_scratch_allocator):
             f.restype = ctypes.c_int
         if path is None:

@@ -1,5 +1,5 @@
-"""The serving operators: page operations, the 8-bit key/value cache with its attention, and
-beam selection (``include/kda.h``).
+"""The serving operators: page operations, the 8-bit key/value cache with its attention, penalties on
+logits and beam selection (``include/kda.h``).
 
 Thin wrappers of the extension ``_build/_kda_serving.so``, which checks the tensors, allocates what
 is returned and calls the C ABI, asynchronously on the given (or current) stream; every step runs
@@ -164,6 +164,27 @@ def kda_kvcache_attention(q: torch.Tensor, k_codes: torch.Tensor, v_codes: torch
     """
     return (_ext or _binding()).kvcache_attention(q, k_codes, v_codes, k_scale, v_scale, tables, lens,
                                                   cu_tokens, scale, out, _handle(stream))
+
+
+def kda_logits_penalize(logits: torch.Tensor, history: Optional[torch.Tensor] = None, lens: Optional[torch.Tensor] = None,
+                        prompt_lens: Optional[torch.Tensor] = None, repetition: Optional[torch.Tensor] = None,
+                        presence: Optional[torch.Tensor] = None, frequency: Optional[torch.Tensor] = None,
+                        bias_tokens: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+                        mask: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Penalties for repeated tokens, biases and a grammar's mask on logits; returns ``out``.
+
+    logits: fp32, bf16 or fp16 ``[..., vocab]`` (what :func:`kda_beam_select` takes), R rows in all.  The
+    others have R rows in one leading dimension, or logits' leading ones:
+    ``history`` (int32 ``[R, width]``), each row's tokens, prompt first, ``lens`` of them (default: width)
+    with ``prompt_lens`` of the prompt (default: 0), negative ones skipped; ``repetition`` (fp32 ``[R]``)
+    divides positive and multiplies other logits of tokens in the history; ``frequency`` times how
+    often, plus ``presence`` if, a token is in the history behind the prompt is taken off; ``bias`` (fp32
+    ``[R, n]``) is added to the logits of ``bias_tokens`` (int32 ``[R, n]``), of one token several times
+    too; ``mask`` (int32 ``[R, words]``): tokens whose bit ``t % 32`` of word ``t // 32`` is 0 get -inf.
+    ``out`` may be logits itself: only what changes is written then.
+    """
+    return (_ext or _binding()).logits_penalize(logits, history, lens, prompt_lens, repetition, presence, frequency, bias_tokens,
+                                                bias, mask, out, _handle(stream))
 
 
 def kda_beam_select(logits: torch.Tensor, scores: torch.Tensor, num_out: Optional[int] = None,

@@ -461,6 +461,49 @@ kda_status kda_beam_select(int32_t batch, int32_t beams, int32_t vocab, int32_t 
                            float* new_scores, int32_t* tokens, int32_t* parents,
                            uint8_t* new_done, void* stream);
 
+/* kda_logits_penalize -- what applies to the logits of a row before tokens are selected from them
+ * (kda_beam_select), in this order:
+ *   x = x > 0 ? x / repetition : x * repetition   for tokens in the row's history;
+ *   x = x - frequency * c - presence              for tokens that are c > 0 times in the history
+ *                                                 behind the prompt;
+ *   x = x + bias                                  for every entry of the row's list with that token,
+ *                                                 in the list's order;
+ *   x = -inf                                      for tokens whose bit in the row's mask is 0.
+ * fp32, rounded once to the logits' type; logits that none of these applies to keep their bits.
+ *   logits, out    device [rows] rows of vocab values, logits_dtype KDA_LOGITS_*, row strides in
+ *                  elements (>= vocab), aligned to their element size.  out may be logits (with its
+ *                  stride); else it must not overlap any input
+ *   rules          host, read during the call; all its arrays are device memory (4-byte aligned):
+ *     history      int32 [rows][history_width] or NULL: each row's tokens in order, prompt first;
+ *                  negative ones are skipped
+ *     lens         int32 [rows], tokens of each row's history, or NULL: history_width
+ *     prompt_lens  int32 [rows], how many of those are the prompt's, or NULL: none
+ *     repetition, presence, frequency  fp32 [rows] or NULL (1, 0, 0)
+ *     bias_tokens, bias  int32 and fp32 [rows][num_bias] or NULL; negative tokens are skipped
+ *     mask         int32 [rows], mask_stride words each (at least vocab / 32, rounded up), or NULL:
+ *                  token t's bit is bit t % 32 of word t / 32
+ * Tokens >= vocab and lengths out of range are recorded as KDA_ERR_INVALID_ARGUMENT, the tokens skipped, the
+ * lengths taken as the nearest in range; penalties that are not finite, and a repetition that is
+ * not above 0, are recorded and the row's three taken as none.
+ * vocab, rows, history_width, num_bias <= 2^30. */
+typedef struct kda_logits_rules {
+    const int32_t* history;
+    const int32_t* lens;
+    const int32_t* prompt_lens;
+    const float* repetition;
+    const float* presence;
+    const float* frequency;
+    const int32_t* bias_tokens;
+    const float* bias;
+    const int32_t* mask;
+    int64_t mask_stride;
+    int32_t history_width;
+    int32_t num_bias;
+} kda_logits_rules;
+kda_status kda_logits_penalize(const kda_logits_rules* rules, int64_t rows, int32_t vocab,
+                               const void* logits, int32_t logits_dtype, int64_t logits_stride,
+                               void* out, int64_t out_stride, void* stream);
+
 /* Scratch of the page, cache and beam calls (kda_pages_*, kda_kvcache_*, kda_beam_select).  Each call
  * takes its own, in the order of its stream, and gives it back after its last launch: calls share
  * none, whichever threads, streams and captured graphs they come from, and a capture needs no call before it.  By

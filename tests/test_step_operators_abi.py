@@ -7,7 +7,7 @@ import torch
 
 import chunked_kda_delta_gb300 as K
 from chunked_kda_delta_gb300 import build as kbuild
-from chunked_kda_delta_gb300.kda import KdaKvCache
+from chunked_kda_delta_gb300.kda import KdaKvCache, KdaLogitsRules
 
 # Calls that pass validation go on with made-up addresses: they must not reach a GPU.
 pytestmark = pytest.mark.skipif(torch.cuda.is_available(), reason="made-up device addresses")
@@ -61,3 +61,31 @@ def test_rotary_overlaps(lib):
     assert rotary(lib, out=0x60000000 + 128, **fused) == ALIAS
     assert rotary(lib, out=0x60000000 - 128, **fused) == ALIAS
     assert rotary(lib, out=0x60000000 - 512, **dict(fused, os=1024)) == ALIAS
+
+
+def logits(lib, rows=4, vocab=100, x=0x10000000, dt=0, stride=100, out=0x20000000, os=100, **rules):
+    r = dict(history=0x30000000, lens=0x31000000, prompt_lens=0x32000000, repetition=0x33000000, presence=0x34000000, frequency=0x35000000,
+             bias_tokens=0x36000000, bias=0x37000000, mask=0x38000000, mask_stride=4, history_width=20, num_bias=5)
+    r.update(rules)
+    s = KdaLogitsRules(**r)
+    return lib.kda_logits_penalize(ctypes.byref(s), rows, vocab, P(x), dt, stride, P(out), os, None)
+
+
+def test_logits_rules(lib):
+    assert logits(lib) not in (INVALID, ALIAS)
+    assert logits(lib, **{k: None for k in ("lens", "prompt_lens", "repetition", "presence", "frequency", "mask")}) not in (INVALID, ALIAS)
+    assert logits(lib, history=None, history_width=0, bias=None, bias_tokens=None, num_bias=0) not in (INVALID, ALIAS)
+    for bad in (dict(rows=-1), dict(rows=1 << 31), dict(vocab=0), dict(vocab=(1 << 30) + 1, stride=1 << 31, os=1 << 31), dict(dt=3),
+                dict(stride=99), dict(os=99), dict(stride=1 << 33), dict(x=None), dict(x=0x10000002), dict(out=None), dict(out=0x20000001), dict(history=None),
+                dict(history=0x30000002), dict(history_width=-1), dict(num_bias=-1), dict(bias=None), dict(bias_tokens=0x36000001), dict(lens=0x31000002),
+                dict(repetition=0x33000001), dict(mask=0x38000002), dict(mask_stride=3)):
+        assert logits(lib, **bad) == INVALID, bad
+    assert lib.kda_logits_penalize(None, 1, 100, P(0x10000000), 0, 100, P(0x20000000), 100, None) == INVALID
+    assert logits(lib, dt=1, x=0x10000002, out=0x20000002) not in (INVALID, ALIAS)
+
+
+def test_logits_overlaps(lib):
+    assert logits(lib, out=0x10000000) not in (INVALID, ALIAS)               # in place
+    for bad in (dict(out=0x10000004), dict(out=0x10000000, os=104), dict(out=0x30000000), dict(out=0x31000000), dict(out=0x34000000), dict(out=0x36000008),
+                dict(out=0x37000008), dict(out=0x38000010)):
+        assert logits(lib, **bad) == ALIAS, bad
