@@ -159,6 +159,13 @@ __device__ __forceinline__ void bulk_copy_to_peer(uint32_t cdst, uint32_t src, u
         "r"(src), "r"(bytes), "r"(cbar)
         : "memory");
 }
+// Bulk copy of `bytes` (multiple of 16, both addresses 16-byte aligned) into this CTA's shared memory.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+        "l"(src), "r"(bytes), "r"(bar)
+        : "memory");
+}
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 // Wait until the sources of all committed bulk copies have been read.
 __device__ __forceinline__ void bulk_wait_read0() {

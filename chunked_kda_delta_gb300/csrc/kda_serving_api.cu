@@ -563,9 +563,8 @@ kda_status kda_logits_penalize(const kda_logits_rules* rules, int64_t rows, int3
         p.mask_stride = r.mask_stride;
         p.status = di->status;
         p.sm_count = di->sm_count;
+        if (rows * ((int64_t)vocab / 1024 + 2) > 0x7fffffff) return fail(KDA_ERR_INVALID_ARGUMENT, "rows * vocab is too large for one launch");
         const cudaError_t e = kda::launch_penalize(p, logits_dtype, (cudaStream_t)stream);
-        if (e == cudaErrorInvalidValue && rows * (int64_t)vocab > (int64_t)1 << 40)
-            return fail(KDA_ERR_INVALID_ARGUMENT, "rows * vocab is too large for one launch");
         return e == cudaSuccess ? KDA_OK : cuda_fail(e, "logits penalties launch");
     });
 }
