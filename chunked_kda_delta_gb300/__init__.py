@@ -34,6 +34,7 @@ from .serving import (  # noqa: F401
     kda_kvcache_append,
     kda_kvcache_append_rotary,
     kda_kvcache_attention,
+    kda_kvcache_attention_shared,
     kda_logits_penalize,
     kda_beam_select,
 )

@@ -414,7 +414,8 @@ PyObject* kvcache_append_rotary(PyObject* const* a) {
     return THPVariable_Wrap(out);
 }
 
-// (q, k_codes, v_codes, k_scale, v_scale, tables, lens, cu_tokens, scale, out, stream)
+// (q, k_codes, v_codes, k_scale, v_scale, tables, lens, cu_tokens, scale, out, stream), with shared prefixes cu_rows as the last
+template <bool kShared>
 PyObject* kvcache_attention(PyObject* const* a) {
     const Cache x = cache_of(a + 1);
     const Tensor& q = tensor(a[0], "q");
@@ -425,6 +426,14 @@ PyObject* kvcache_attention(PyObject* const* a) {
     if (given(a[8])) {
         scale = PyFloat_AsDouble(a[8]);
         if (scale == -1.0 && PyErr_Occurred()) throw python_error();
+    }
+    const int32_t* cu_rows = nullptr;
+    int64_t groups = 0;
+    if (kShared) {
+        const Tensor& t = tensor(a[11], "cu_rows");
+        if (t.dim() != 1 || t.size(0) < 1 || t.size(0) > INT32_MAX) refuse("cu_rows must be [groups + 1]");
+        cu_rows = ptr<int32_t>(vector(a[11], "cu_rows", {ScalarType::Int}, t.sizes(), x.device));
+        groups = t.size(0) - 1;
     }
     Place on(x.device, a[10]);
     Tensor out;
@@ -437,7 +446,11 @@ PyObject* kvcache_attention(PyObject* const* a) {
     }
     const int64_t os = act_stride(out, "out", q.size(1), x.c.head_dim);
     const TorchScratch scratch(on.own);
-    check(kda_kvcache_attention(&x.c, q.data_ptr(), (int32_t)q.size(1), type, qs, q.size(0), x.lens, x.cu, (float)scale, out.data_ptr(), os, on.stream));
+    if (kShared)
+        check(kda_kvcache_attention_shared(&x.c, q.data_ptr(), (int32_t)q.size(1), type, qs, q.size(0), x.lens, x.cu, cu_rows, (int32_t)groups,
+                                           (float)scale, out.data_ptr(), os, on.stream));
+    else
+        check(kda_kvcache_attention(&x.c, q.data_ptr(), (int32_t)q.size(1), type, qs, q.size(0), x.lens, x.cu, (float)scale, out.data_ptr(), os, on.stream));
     return THPVariable_Wrap(out);
 }
 
@@ -593,7 +606,8 @@ PyMethodDef methods[] = {
     method<pages_copy, 5>("pages_copy"),
     method<kvcache_append, 10>("kvcache_append"),
     method<kvcache_append_rotary, 15>("kvcache_append_rotary"),
-    method<kvcache_attention, 11>("kvcache_attention"),
+    method<kvcache_attention<false>, 11>("kvcache_attention"),
+    method<kvcache_attention<true>, 12>("kvcache_attention_shared"),
     method<logits_penalize, 12>("logits_penalize"),
     method<beam_select, 6>("beam_select"),
     PyMethodDef{nullptr, nullptr, 0, nullptr},

@@ -88,7 +88,7 @@ __device__ __forceinline__ void product_k(float (&acc)[kNT][4], const uint4 (&k)
     }
 }
 
-template <typename T, int kDim, int kNT>
+template <typename T, int kDim, int kNT, int kKind>
 __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(const __grid_constant__ AttentionParams p) {
     constexpr int kCols = 8 * kNT, kKeys = kSlabKeys<kDim>, kBlk = kKeys / 16;  // (blocks of 16 keys)
     constexpr int kHalves = kDim / 64;   // 16-byte loads of a key by a thread
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(c
         if (r >= c.rows) return 0;
         int64_t begin;
         const int n = row_tokens(c, r, begin);
-        return ((int64_t)n * group + kCols - 1) / kCols * c.heads * row_slabs<kDim>(row_length(c, r));
+        return ((int64_t)n * group + kCols - 1) / kCols * c.heads * row_slabs<kDim>(row_length(c, r) - unit_from<kKind>(p, r));
     });
     __syncthreads();
     if (blockIdx.x == 0 && c.rows <= kMaxListed)
@@ -124,16 +124,16 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(c
     for (int64_t w = w_begin; w < w_end;) {
         const int row = row_of(first, c.rows, w);
         int64_t begin;
-        const int n = row_tokens(c, row, begin), len = row_length(c, row), slabs = row_slabs<kDim>(len);
+        const int n = row_tokens(c, row, begin), len = row_length(c, row), from = unit_from<kKind>(p, row), slabs = row_slabs<kDim>(len - from);
         const int64_t i_row = (w - first[row]) / slabs, item = first[row] + i_row * slabs, item_end = item + slabs;
         const int head = (int)(i_row % c.heads), block = (int)(i_row / c.heads);
-        const int slab0 = (int)(w - item);
+        const int slab0 = (int)(w - item) + from / kKeys;
 
         const int rows_all = n * group, row0 = block * kCols;
         // Keys that any, and that every, column of this block sees.
         const int seen_max = min(len, max(0, len - n + (min(rows_all, row0 + kCols) - 1) / group + 1));
         const int seen_min = max(0, min(len, len - n + row0 / group + 1));
-        const int slab1 = min((int)(min(item_end, w_end) - item), (seen_max + kKeys - 1) / kKeys);
+        const int slab1 = min((int)(min(item_end, w_end) - item) + from / kKeys, (seen_max + kKeys - 1) / kKeys);
 
         // Page and scales of the 16 keys of block number b; lane l holds block b0 + l.
         const int32_t* table = c.tables + (int64_t)row * c.width;
@@ -207,6 +207,26 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(c
             l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
             for (int j = 0; j < kMT; ++j) o[nt][j][0] = o[nt][j][1] = o[nt][j][2] = o[nt][j][3] = 0.f;
+        }
+        if (kKind == kKindSuffix && w == item && from > 0) {  // on from the prefix
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+                for (int col = 0; col < 2; ++col) {
+                    const int f = row0 + nt * 8 + 2 * t + col;
+                    if (f >= rows_all) continue;
+                    const int64_t at = (begin + f / group) * p.q_heads + head * group + f % group;
+                    const float2 ml = p.state_ml[at];
+                    m[nt][col] = ml.x + (kLift - kBlockLift);
+                    l[nt][col] = g == 0 ? ml.y : 0.f;  // (summed over the lanes in the end)
+                    const float2* src = reinterpret_cast<const float2*>(p.state_o + at * kDim + kVWords * 4 * g);
+#pragma unroll
+                    for (int j = 0; j < kMT; ++j) {
+                        const float2 y = src[j];
+                        o[nt][j][col] = y.x;
+                        o[nt][j][2 + col] = y.y;
+                    }
+                }
         }
 
         auto scale_of = [&](const float* scales, int32_t page) { return page < 0 ? 0.f : scales[(int64_t)page * c.heads + head]; };
@@ -430,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(c
 // blockIdx.y column tiles; a warp has 16 channels of 8 columns, in the fragments' layout.
 // kShares > 1 (items of many parts): blockIdx.z is the channel tile, and that many warps share the
 // parts.
-template <typename T, int kDim, int kNT, int kShares>
+template <typename T, int kDim, int kNT, int kShares, int kKind>
 __global__ void __launch_bounds__(kShares > 1 ? kShares * 32 : kDim * 2) attention_join_kernel(const __grid_constant__ AttentionParams p) {
     constexpr int kCols = 8 * kNT, kMT = kDim / 16, kVWords = kDim / 32;
     constexpr bool kSplit = kShares > 1;
@@ -441,10 +461,10 @@ __global__ void __launch_bounds__(kShares > 1 ? kShares * 32 : kDim * 2) attenti
     const int group = p.q_heads / c.heads;
     int64_t i = blockIdx.x;
     int row;
-    const bool there = joined_item(c, group, kCols, i, row);
+    const bool there = joined_item<kKind>(p, group, kCols, i, row);
     int64_t begin = 0;
     const int n = there ? row_tokens(c, row, begin) : 0;
-    const int slabs = there ? row_slabs<kDim>(row_length(c, row)) : 0;
+    const int slabs = there ? row_slabs<kDim>(row_length(c, row) - unit_from<kKind>(p, row)) : 0;
     follow_stream();
     if (!there) return;
     const int64_t all = p.first_work[c.rows], w_row = p.first_work[row], w_next = p.first_work[row + 1];
@@ -501,30 +521,30 @@ __global__ void __launch_bounds__(kShares > 1 ? kShares * 32 : kDim * 2) attenti
     }
 }
 
-template <typename T, int kDim, int kNT>
+template <typename T, int kDim, int kNT, int kKind>
 cudaError_t launch_one(const AttentionParams& p, cudaStream_t stream) {
     const CacheParams& c = p.c;
     constexpr int kCols = 8 * kNT;
-    const cudaError_t e = launch_early(attention_kernel<T, kDim, kNT>, dim3(p.ctas), kThreads, 0, stream, 1, p);
+    const cudaError_t e = launch_early(attention_kernel<T, kDim, kNT, kKind>, dim3(p.ctas), kThreads, 0, stream, 1, p);
     if (e != cudaSuccess) return e;
     const int64_t group = p.q_heads / c.heads;
-    const int64_t items = joined_items(c, group, kCols);
+    const int64_t items = joined_items(p, kKind, group, kCols);
     // As many warps to a part of an item as a wave or two hold: few items have many parts each (2 rows
     // of up to 24086 tokens: 20 us with 16, 29 with 8; 34 rows of 135: 17 us with one, 28 with 16).
     const int64_t tiles = items * kNT * (kDim / 16);
     if (tiles <= 2ll * p.sm_count)
-        return launch_early(attention_join_kernel<T, kDim, kNT, 16>, dim3((unsigned)items, kNT, kDim / 16), 512, 0, stream, 1, p);
+        return launch_early(attention_join_kernel<T, kDim, kNT, 16, kKind>, dim3((unsigned)items, kNT, kDim / 16), 512, 0, stream, 1, p);
     if (tiles <= 5ll * p.sm_count)
-        return launch_early(attention_join_kernel<T, kDim, kNT, 4>, dim3((unsigned)items, kNT, kDim / 16), 128, 0, stream, 1, p);
-    return launch_early(attention_join_kernel<T, kDim, kNT, 1>, dim3((unsigned)items, kNT), kDim * 2, 0, stream, 1, p);
+        return launch_early(attention_join_kernel<T, kDim, kNT, 4, kKind>, dim3((unsigned)items, kNT, kDim / 16), 128, 0, stream, 1, p);
+    return launch_early(attention_join_kernel<T, kDim, kNT, 1, kKind>, dim3((unsigned)items, kNT), kDim * 2, 0, stream, 1, p);
 }
 
 // CTAs an SM holds; the same on every device the library runs on.
-template <typename T, int kDim, int kNT>
+template <typename T, int kDim, int kNT, int kKind>
 int resident() {
     static const int count = [] {
         int n = 0;
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attention_kernel<T, kDim, kNT>, kThreads, 0) != cudaSuccess || n < 1) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attention_kernel<T, kDim, kNT, kKind>, kThreads, 0) != cudaSuccess || n < 1) {
             cudaGetLastError();
             n = 1;
         }
@@ -533,15 +553,21 @@ int resident() {
     return count;
 }
 
-template <typename T, int kDim>
+template <typename T, int kDim, int kKind>
 cudaError_t launch_cols(const AttentionParams& p, int cols, cudaStream_t stream) {
-    if (cols == 8) return launch_one<T, kDim, 1>(p, stream);
-    return launch_one<T, kDim, 2>(p, stream);
+    if (cols == 8) return launch_one<T, kDim, 1, kKind>(p, stream);
+    return launch_one<T, kDim, 2, kKind>(p, stream);
 }
 template <typename T, int kDim>
 int resident_cols(int cols) {
-    if (cols == 8) return resident<T, kDim, 1>();
-    return resident<T, kDim, 2>();
+    if (cols == 8) return resident<T, kDim, 1, kKindRows>();
+    return resident<T, kDim, 2, kKindRows>();
+}
+template <int kKind>
+cudaError_t launch_kind(const AttentionParams& p, int cols, bool f16, cudaStream_t stream) {
+    if (p.c.dim == 64)
+        return f16 ? launch_cols<__half, 64, kKind>(p, cols, stream) : launch_cols<__nv_bfloat16, 64, kKind>(p, cols, stream);
+    return f16 ? launch_cols<__half, 128, kKind>(p, cols, stream) : launch_cols<__nv_bfloat16, 128, kKind>(p, cols, stream);
 }
 
 }  // namespace
@@ -578,9 +604,11 @@ int attention_ctas(int32_t dim, int cols, bool f16, int sm_count) {
 
 cudaError_t launch_attention(const AttentionParams& p, int cols, bool f16, cudaStream_t stream) {
     if (cols == kBlockRows) return launch_block_attention(p, f16, stream);
-    if (p.c.dim == 64)
-        return f16 ? launch_cols<__half, 64>(p, cols, stream) : launch_cols<__nv_bfloat16, 64>(p, cols, stream);
-    return f16 ? launch_cols<__half, 128>(p, cols, stream) : launch_cols<__nv_bfloat16, 128>(p, cols, stream);
+    return launch_kind<kKindRows>(p, cols, f16, stream);
+}
+cudaError_t launch_suffix(const AttentionParams& p, int cols, bool f16, cudaStream_t stream) {
+    if (cols == kBlockRows) return launch_block_suffix(p, f16, stream);
+    return launch_kind<kKindSuffix>(p, cols, f16, stream);
 }
 
 }  // namespace kda

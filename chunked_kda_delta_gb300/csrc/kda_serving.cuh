@@ -136,6 +136,16 @@ struct RotaryParams : AppendParams {
 };
 cudaError_t launch_rotary_append(const RotaryParams& p, bool f16, cudaStream_t stream);
 
+// Rows that share a prefix.
+struct SharedGroup {
+    int64_t begin;            // first token of its rows
+    int32_t tokens;           // of all its rows; 0: nothing is shared
+    int32_t shared;           // tokens of the prefix, a multiple of kSharedUnit
+    int32_t row;              // whose table is read
+    int32_t unused;
+};
+constexpr int kSharedUnit = 128;
+
 struct AttentionParams {
     CacheParams c;
     const void* q;
@@ -149,6 +159,12 @@ struct AttentionParams {
     float* part_o;            // [slots][cols * dim], in the layout of the product's fragments
     float* part_ml;           // [slots][cols][2]: maximum and sum
     int32_t ctas, sm_count;
+    // shared prefixes
+    const SharedGroup* group; // [groups]
+    int32_t groups;
+    const int32_t* from;      // [rows]: tokens of the prefix
+    float* state_o;           // [tokens * q_heads][dim], what the prefix left: outputs,
+    float2* state_ml;         // [tokens * q_heads], maxima and sums
 };
 size_t attention_slots(int ctas);
 int attention_cols(const CacheParams& c, int32_t group, int sm_count);
@@ -157,6 +173,19 @@ cudaError_t launch_attention(const AttentionParams& p, int cols, bool f16, cudaS
 // Items of 128 query rows on tcgen05 (kda_kvcache_block.cu): two CTAs an SM, two parts each.
 constexpr int kBlockRows = 128;
 cudaError_t launch_block_attention(const AttentionParams& p, bool f16, cudaStream_t stream);
+// The parts of attention with shared prefixes (kda_kvcache_shared.cu): the groups' prefixes are found, then
+// worked out into the state, then the rows go on from there.
+struct SharedPlan {
+    CacheParams c;
+    const int32_t* cu_rows;   // [groups + 1]
+    int32_t groups;
+    SharedGroup* group;
+    int32_t* from;
+};
+cudaError_t launch_shared_plan(const SharedPlan& p, cudaStream_t stream);
+cudaError_t launch_block_prefix(const AttentionParams& p, bool f16, cudaStream_t stream);
+cudaError_t launch_block_suffix(const AttentionParams& p, bool f16, cudaStream_t stream);
+cudaError_t launch_suffix(const AttentionParams& p, int cols, bool f16, cudaStream_t stream);
 
 // ---- beam selection -------------------------------------------------------------------
 struct BeamParams {

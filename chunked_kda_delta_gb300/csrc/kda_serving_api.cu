@@ -1,7 +1,7 @@
 // kda_serving_api.cu -- the C ABI of the serving operators: page operations, the 8-bit
 // key/value cache, penalties on logits and beam selection.  Validation, scratch layout and launches; the kernels
-// live in kda_pages.cu, kda_kvcache_append.cu, kda_kvcache_rotary.cu, kda_kvcache_attention.cu, kda_logits.cu
-// and kda_beam.cu.
+// live in kda_pages.cu, kda_kvcache_append.cu, kda_kvcache_rotary.cu, kda_kvcache_attention.cu,
+// kda_kvcache_block.cu, kda_kvcache_shared.cu, kda_logits.cu and kda_beam.cu.
 #include <math.h>
 
 #include <exception>
@@ -244,6 +244,91 @@ kda::CacheParams cache_params(const kda_kvcache* c, int64_t num_tokens, const in
     return p;
 }
 
+// Attention over the cache; with cu_rows for groups of rows that share prefixes.
+kda_status attend(const kda_kvcache* cache, const void* q, int32_t num_q_heads, int32_t act_dtype, int64_t q_stride, int64_t num_tokens,
+                  const int32_t* lens, const int32_t* cu_tokens, const int32_t* cu_rows, int32_t groups, float scale, void* out,
+                  int64_t out_stride, void* stream) {
+    kda_status st = check_cache(cache, num_tokens, lens, cu_tokens);
+    if (st != KDA_OK) return st;
+    if (act_dtype != KDA_ACT_BF16 && act_dtype != KDA_ACT_F16)
+        return fail(KDA_ERR_INVALID_ARGUMENT, "unknown act_dtype %d", act_dtype);
+    if (num_q_heads < 1 || num_q_heads > (1 << 16) || num_q_heads % cache->num_kv_heads != 0)
+        return fail(KDA_ERR_INVALID_ARGUMENT, "num_q_heads must be a multiple of num_kv_heads (got %d, %d)", num_q_heads,
+                    cache->num_kv_heads);
+    if (!isfinite(scale)) return fail(KDA_ERR_INVALID_ARGUMENT, "scale must be finite");
+    const int64_t inner = (int64_t)num_q_heads * cache->head_dim;
+    if ((st = check_act("q", q, num_tokens, q_stride, inner)) || (st = check_act("out", out, num_tokens, out_stride, inner))) return st;
+    const size_t blocks = (size_t)cache->pages * cache->num_kv_heads, codes = blocks * cache->page_tokens * cache->head_dim;
+    if ((st = check_overlap({{"out", {out, span(num_tokens, out_stride, inner)}}},
+                            {{"q", {q, span(num_tokens, q_stride, inner)}}, {"k_codes", {cache->k_codes, codes}},
+                             {"v_codes", {cache->v_codes, codes}}, {"k_scale", {cache->k_scale, blocks * 4}},
+                             {"v_scale", {cache->v_scale, blocks * 4}},
+                             {"tables", {cache->tables, (size_t)cache->rows * cache->width * 4}},
+                             {"lens", {lens, (size_t)cache->rows * 4}},
+                             {"cu_tokens", {cu_tokens, ((size_t)cache->rows + 1) * 4}},
+                             {"cu_rows", {cu_rows, ((size_t)groups + 1) * 4}}})) != KDA_OK)
+        return st;
+    const int32_t group = num_q_heads / cache->num_kv_heads;
+    if (num_tokens * group > 0x7fffff00 || (num_tokens * group / 8 + cache->rows) * cache->num_kv_heads > 0x7fffffff)
+        return fail(KDA_ERR_INVALID_ARGUMENT, "too many tokens for one launch");
+    int dev = 0;
+    DeviceInfo* di = nullptr;
+    if ((st = current_device(&dev, &di)) != KDA_OK) return st;
+    if (num_tokens == 0) return KDA_OK;
+    const bool f16 = act_dtype == KDA_ACT_F16;
+    kda::AttentionParams p{};
+    p.c = cache_params(cache, num_tokens, lens, cu_tokens, di->status);
+    const int cols = kda::attention_cols(p.c, group, di->sm_count);
+    p.sm_count = di->sm_count;
+    p.ctas = kda::attention_ctas(cache->head_dim, cols, f16, di->sm_count);
+    const int block_ctas = kda::attention_ctas(cache->head_dim, kda::kBlockRows, f16, di->sm_count);
+    const auto parts_of = [&](int c, int ctas) { return (c == kda::kBlockRows ? (size_t)2 * ctas : kda::attention_slots(ctas)) * c; };
+    // With shared prefixes the parts' place is the prefixes' first, then the rows'.
+    size_t parts = parts_of(cols, p.ctas);
+    if (cu_rows && parts_of(kda::kBlockRows, block_ctas) > parts) parts = parts_of(kda::kBlockRows, block_ctas);
+    const int most_ctas = p.ctas > block_ctas ? p.ctas : block_ctas;
+    const size_t units = (size_t)(groups > cache->rows ? groups : cache->rows), query_rows = cu_rows ? (size_t)num_tokens * num_q_heads : 0;
+    size_t bytes = 0;
+    auto place = [&](size_t n) {
+        const size_t at = bytes;
+        bytes += (n + 255) / 256 * 256;
+        return at;
+    };
+    const size_t at_o = place(parts * cache->head_dim * 4), at_ml = place(parts * 2 * 4), at_split = place((size_t)most_ctas * 32),
+                 at_first = place((units + 1) * 8), at_group = place((size_t)groups * sizeof(kda::SharedGroup)),
+                 at_from = place(cu_rows ? (size_t)cache->rows * 4 : 0), at_state = place(query_rows * cache->head_dim * 4),
+                 at_state_ml = place(query_rows * 8);
+    Scratch ws;
+    if ((st = ws.take(dev, stream, bytes)) != KDA_OK) return st;
+    p.part_o = reinterpret_cast<float*>(ws.base + at_o);
+    p.part_ml = reinterpret_cast<float*>(ws.base + at_ml);
+    p.split_items = ws.base + at_split;
+    p.first_work = reinterpret_cast<int64_t*>(ws.base + at_first);
+    p.q = q;
+    p.out = out;
+    p.q_stride = q_stride;
+    p.out_stride = out_stride;
+    p.q_heads = num_q_heads;
+    p.scale = scale * 1.4426950408889634f;
+    const cudaStream_t on = (cudaStream_t)stream;
+    if (!cu_rows) {
+        const cudaError_t e = kda::launch_attention(p, cols, f16, on);
+        return e == cudaSuccess ? KDA_OK : cuda_fail(e, "cache attention launch");
+    }
+    kda::SharedPlan plan{p.c, cu_rows, groups, reinterpret_cast<kda::SharedGroup*>(ws.base + at_group), reinterpret_cast<int32_t*>(ws.base + at_from)};
+    p.group = plan.group;
+    p.groups = groups;
+    p.from = plan.from;
+    p.state_o = reinterpret_cast<float*>(ws.base + at_state);
+    p.state_ml = reinterpret_cast<float2*>(ws.base + at_state_ml);
+    kda::AttentionParams prefix = p;
+    prefix.ctas = block_ctas;
+    cudaError_t e = kda::launch_shared_plan(plan, on);
+    if (e == cudaSuccess) e = kda::launch_block_prefix(prefix, f16, on);
+    if (e == cudaSuccess) e = kda::launch_suffix(p, cols, f16, on);
+    return e == cudaSuccess ? KDA_OK : cuda_fail(e, "shared attention launch");
+}
+
 }  // namespace
 
 extern "C" {
@@ -449,53 +534,22 @@ kda_status kda_kvcache_attention(const kda_kvcache* cache, const void* q, int32_
                                  const int32_t* lens, const int32_t* cu_tokens, float scale,
                                  void* out, int64_t out_stride, void* stream) {
     return guarded([&] {
-        kda_status st = check_cache(cache, num_tokens, lens, cu_tokens);
+        return attend(cache, q, num_q_heads, act_dtype, q_stride, num_tokens, lens, cu_tokens, nullptr, 0, scale, out, out_stride, stream);
+    });
+}
+
+kda_status kda_kvcache_attention_shared(const kda_kvcache* cache, const void* q, int32_t num_q_heads,
+                                        int32_t act_dtype, int64_t q_stride, int64_t num_tokens,
+                                        const int32_t* lens, const int32_t* cu_tokens,
+                                        const int32_t* cu_rows, int32_t num_groups, float scale,
+                                        void* out, int64_t out_stride, void* stream) {
+    return guarded([&] {
+        const int32_t rows = cache ? cache->rows : 0;
+        if (num_groups < 0 || num_groups > (1 << 24) || (num_groups == 0 && rows > 0))
+            return fail(KDA_ERR_INVALID_ARGUMENT, "num_groups must be in [1, 2^24] (got %d)", num_groups);
+        const kda_status st = check_pointer("cu_rows", cu_rows, ((size_t)num_groups + 1) * 4, 4);
         if (st != KDA_OK) return st;
-        if (act_dtype != KDA_ACT_BF16 && act_dtype != KDA_ACT_F16)
-            return fail(KDA_ERR_INVALID_ARGUMENT, "unknown act_dtype %d", act_dtype);
-        if (num_q_heads < 1 || num_q_heads > (1 << 16) || num_q_heads % cache->num_kv_heads != 0)
-            return fail(KDA_ERR_INVALID_ARGUMENT, "num_q_heads must be a multiple of num_kv_heads (got %d, %d)", num_q_heads,
-                        cache->num_kv_heads);
-        if (!isfinite(scale)) return fail(KDA_ERR_INVALID_ARGUMENT, "scale must be finite");
-        const int64_t inner = (int64_t)num_q_heads * cache->head_dim;
-        if ((st = check_act("q", q, num_tokens, q_stride, inner)) || (st = check_act("out", out, num_tokens, out_stride, inner))) return st;
-        const size_t blocks = (size_t)cache->pages * cache->num_kv_heads, codes = blocks * cache->page_tokens * cache->head_dim;
-        if ((st = check_overlap({{"out", {out, span(num_tokens, out_stride, inner)}}},
-                                {{"q", {q, span(num_tokens, q_stride, inner)}}, {"k_codes", {cache->k_codes, codes}},
-                                 {"v_codes", {cache->v_codes, codes}}, {"k_scale", {cache->k_scale, blocks * 4}},
-                                 {"v_scale", {cache->v_scale, blocks * 4}},
-                                 {"tables", {cache->tables, (size_t)cache->rows * cache->width * 4}},
-                                 {"lens", {lens, (size_t)cache->rows * 4}},
-                                 {"cu_tokens", {cu_tokens, ((size_t)cache->rows + 1) * 4}}})) != KDA_OK)
-            return st;
-        const int32_t group = num_q_heads / cache->num_kv_heads;
-        if (num_tokens * group > 0x7fffff00 || (num_tokens * group / 8 + cache->rows) * cache->num_kv_heads > 0x7fffffff)
-            return fail(KDA_ERR_INVALID_ARGUMENT, "too many tokens for one launch");
-        int dev = 0;
-        DeviceInfo* di = nullptr;
-        if ((st = current_device(&dev, &di)) != KDA_OK) return st;
-        if (num_tokens == 0) return KDA_OK;
-        const bool f16 = act_dtype == KDA_ACT_F16;
-        kda::AttentionParams p{};
-        p.c = cache_params(cache, num_tokens, lens, cu_tokens, di->status);
-        const int cols = kda::attention_cols(p.c, group, di->sm_count);
-        p.sm_count = di->sm_count;
-        p.ctas = kda::attention_ctas(cache->head_dim, cols, f16, di->sm_count);
-        const size_t parts = (cols == kda::kBlockRows ? (size_t)2 * p.ctas : kda::attention_slots(p.ctas)) * cols;
-        Scratch ws;
-        if ((st = ws.take(dev, stream, parts * (cache->head_dim + 2) * 4 + (size_t)p.ctas * 32 + ((size_t)cache->rows + 1) * 8)) != KDA_OK) return st;
-        p.part_o = reinterpret_cast<float*>(ws.base);
-        p.part_ml = p.part_o + parts * cache->head_dim;
-        p.split_items = p.part_ml + parts * 2;
-        p.first_work = reinterpret_cast<int64_t*>(p.part_ml + parts * 2 + (size_t)p.ctas * 8);
-        p.q = q;
-        p.out = out;
-        p.q_stride = q_stride;
-        p.out_stride = out_stride;
-        p.q_heads = num_q_heads;
-        p.scale = scale * 1.4426950408889634f;
-        const cudaError_t e = kda::launch_attention(p, cols, f16, (cudaStream_t)stream);
-        return e == cudaSuccess ? KDA_OK : cuda_fail(e, "cache attention launch");
+        return attend(cache, q, num_q_heads, act_dtype, q_stride, num_tokens, lens, cu_tokens, cu_rows, num_groups, scale, out, out_stride, stream);
     });
 }
 

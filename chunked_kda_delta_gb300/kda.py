@@ -35,7 +35,8 @@ EXPORTED_SYMBOLS = (
     "kda_last_error_message", "kda_version", "kda_prefill_segment_noalloc", "kda_plan",
     "kda_plan_varlen", "kda_decode", "kda_decode_paged", "kda_pages_alloc", "kda_pages_free",
     "kda_pages_fork", "kda_pages_compact", "kda_pages_copy", "kda_kvcache_append",
-    "kda_kvcache_append_rotary", "kda_kvcache_attention", "kda_logits_penalize",
+    "kda_kvcache_append_rotary", "kda_kvcache_attention",
+    "kda_kvcache_attention_shared", "kda_logits_penalize",
     "kda_beam_select", "kda_set_scratch_allocator",
 )
 
@@ -146,6 +147,7 @@ def load_library(path: Optional[str] = None, build_if_missing: bool = False) -> 
                                                   vp, i64, vp]
         lib.kda_kvcache_attention.argtypes = [cache, vp, i32, i32, i64, i64, vp, vp, f32, vp, i64,
                                               vp]
+        lib.kda_kvcache_attention_shared.argtypes = [cache, vp, i32, i32, i64, i64, vp, vp, vp, i32, f32, vp, i64, vp]
         lib.kda_logits_penalize.argtypes = [ctypes.POINTER(KdaLogitsRules), i64, i32, vp, i32, i64, vp, i64, vp]
         lib.kda_beam_select.argtypes = [i32, i32, i32, i32, vp, i32, i64, vp, vp, i32, vp, vp, vp,
                                         vp, vp]
@@ -163,7 +165,8 @@ def load_library(path: Optional[str] = None, build_if_missing: bool = False) -> 
                   lib.kda_release_workspaces, lib.kda_decode_paged, lib.kda_pages_alloc,
                   lib.kda_pages_free, lib.kda_pages_fork, lib.kda_pages_compact,
                   lib.kda_pages_copy, lib.kda_kvcache_append, lib.kda_kvcache_append_rotary,
-                  lib.kda_kvcache_attention, lib.kda_logits_penalize,
+                  lib.kda_kvcache_attention, lib.kda_kvcache_attention_shared,
+                  lib.kda_logits_penalize,
                   lib.kda_beam_select, lib.kda_set_scratch_allocator):
             f.restype = ctypes.c_int
         if path is None:

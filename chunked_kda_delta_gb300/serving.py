@@ -166,6 +166,22 @@ def kda_kvcache_attention(q: torch.Tensor, k_codes: torch.Tensor, v_codes: torch
                                                   cu_tokens, scale, out, _handle(stream))
 
 
+def kda_kvcache_attention_shared(q: torch.Tensor, k_codes: torch.Tensor, v_codes: torch.Tensor,
+                                 k_scale: torch.Tensor, v_scale: torch.Tensor, tables: torch.Tensor,
+                                 lens: torch.Tensor, cu_rows: torch.Tensor,
+                                 cu_tokens: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                                 out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """:func:`kda_kvcache_attention` for rows that share prefixes; returns ``out``.
+
+    Rows ``cu_rows[g]`` to ``cu_rows[g + 1] - 1`` (int32 ``[groups + 1]``) are a group, a request's beams
+    or the users of one system prompt: the keys that all of them have in the same pages (as
+    :func:`kda_pages_fork` leaves them) are gone through once for the group.  The result is the same for
+    any groups.
+    """
+    return (_ext or _binding()).kvcache_attention_shared(q, k_codes, v_codes, k_scale, v_scale, tables, lens,
+                                                         cu_tokens, scale, out, _handle(stream), cu_rows)
+
+
 def kda_logits_penalize(logits: torch.Tensor, history: Optional[torch.Tensor] = None, lens: Optional[torch.Tensor] = None,
                         prompt_lens: Optional[torch.Tensor] = None, repetition: Optional[torch.Tensor] = None,
                         presence: Optional[torch.Tensor] = None, frequency: Optional[torch.Tensor] = None,

@@ -432,6 +432,21 @@ kda_status kda_kvcache_attention(const kda_kvcache* cache, const void* q, int32_
                                  const int32_t* lens, const int32_t* cu_tokens, float scale,
                                  void* out, int64_t out_stride, void* stream);
 
+/* kda_kvcache_attention_shared -- kda_kvcache_attention for rows that share prefixes, the beams of
+ * a request or the users of one system prompt: the keys that all rows of a group have in the same pages
+ * are gone through once for the whole group.  The result is kda_kvcache_attention's (sums in another
+ * order), whatever the groups are: what their rows share is found in the tables, in whole units of 128
+ * tokens, as kda_pages_fork leaves it.
+ *   cu_rows     device int32 [num_groups + 1] (cu_seqlens rules): group g is rows cu_rows[g] ..
+ *               cu_rows[g + 1] - 1; malformed offsets are recorded and nothing is shared
+ *   num_groups  >= 1, unless there are no rows
+ * Everything else as kda_kvcache_attention. */
+kda_status kda_kvcache_attention_shared(const kda_kvcache* cache, const void* q, int32_t num_q_heads,
+                                        int32_t act_dtype, int64_t q_stride, int64_t num_tokens,
+                                        const int32_t* lens, const int32_t* cu_tokens,
+                                        const int32_t* cu_rows, int32_t num_groups, float scale,
+                                        void* out, int64_t out_stride, void* stream);
+
 /* ---------------------------------------------------------------------------------------
  * kda_beam_select -- one step of beam search: the num_out best continuations of each request.
  * Beam w of request b scored scores[b][w]; its token t continues it with

@@ -89,3 +89,21 @@ def test_logits_overlaps(lib):
     for bad in (dict(out=0x10000004), dict(out=0x10000000, os=104), dict(out=0x30000000), dict(out=0x31000000), dict(out=0x34000000), dict(out=0x36000008),
                 dict(out=0x37000008), dict(out=0x38000010)):
         assert logits(lib, **bad) == ALIAS, bad
+
+
+def attend(lib, c=None, q=0x60000000, hq=4, act=0, qs=256, n=3, lens=0x70000000, cu=None, rows=0x73000000, groups=2, scale=0.1, out=0x71000000, os=256):
+    return lib.kda_kvcache_attention_shared(ctypes.byref(c or cache()), P(q), hq, act, qs, n, P(lens), P(cu), P(rows), groups, ctypes.c_float(scale), P(out),
+                                            os, None)
+
+
+def test_shared_attention_rules(lib):
+    assert attend(lib) not in (INVALID, ALIAS)
+    for bad in (dict(page=24), dict(dim=96), dict(heads=0), dict(pages=-1), dict(rows=-1), dict(width=0), dict(k=None), dict(tables=None)):
+        assert attend(lib, c=cache(**bad)) == INVALID, bad
+    for bad in (dict(rows=None), dict(rows=0x73000002), dict(groups=0), dict(groups=-1), dict(groups=1 << 25), dict(hq=3), dict(hq=0), dict(qs=252),
+                dict(qs=128), dict(os=8), dict(q=None), dict(out=None), dict(n=4), dict(n=-1, cu=0x72000000), dict(act=2), dict(lens=None),
+                dict(scale=float("nan"))):
+        assert attend(lib, **bad) == INVALID, bad
+    for bad in (dict(out=0x60000100), dict(out=0x10000000), dict(out=0x70000000), dict(out=0x73000000), dict(out=0x50000000)):
+        assert attend(lib, **bad) == ALIAS, bad
+    assert lib.kda_kvcache_attention_shared(None, None, 1, 0, 64, 0, None, None, P(0x73000000), 0, ctypes.c_float(1), None, 64, None) == INVALID
