@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(kShares > 1 ? kShares * 32 : kDim * 2) attenti
     const int group = p.q_heads / c.heads;
     int64_t i = blockIdx.x;
     int row;
-    const bool there = joined_item<kKind>(p, group, kCols, i, row);
+    const bool there = joined_item(c, group, kCols, i, row);
     int64_t begin = 0;
     const int n = there ? row_tokens(c, row, begin) : 0;
     const int slabs = there ? row_slabs<kDim>(row_length(c, row) - unit_from<kKind>(p, row)) : 0;
@@ -528,7 +528,7 @@ cudaError_t launch_one(const AttentionParams& p, cudaStream_t stream) {
     const cudaError_t e = launch_early(attention_kernel<T, kDim, kNT, kKind>, dim3(p.ctas), kThreads, 0, stream, 1, p);
     if (e != cudaSuccess) return e;
     const int64_t group = p.q_heads / c.heads;
-    const int64_t items = joined_items(p, kKind, group, kCols);
+    const int64_t items = joined_items(c, group, kCols);
     // As many warps to a part of an item as a wave or two hold: few items have many parts each (2 rows
     // of up to 24086 tokens: 20 us with 16, 29 with 8; 34 rows of 135: 17 us with one, 28 with 16).
     const int64_t tiles = items * kNT * (kDim / 16);

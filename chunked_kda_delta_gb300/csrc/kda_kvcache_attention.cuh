@@ -144,25 +144,12 @@ __device__ __forceinline__ int row_of(const int64_t* first, int rows, int64_t w)
     return lo;
 }
 
-// What a launch's rows are: the rows of the batch with all of their keys; the groups of rows that share a
-// prefix, with its keys; or the rows of the batch with the keys behind it, which continue from the state
-// (maximum, sum, output) that the prefix left for each query row.
-enum { kKindRows = 0, kKindPrefix = 1, kKindSuffix = 2 };
-template <int kKind>
-__device__ __forceinline__ int unit_count(const AttentionParams& p) { return kKind == kKindPrefix ? p.groups : p.c.rows; }
-template <int kKind>
-__device__ __forceinline__ int unit_tokens(const AttentionParams& p, int r, int64_t& begin) {
-    if (kKind != kKindPrefix) return row_tokens(p.c, r, begin);
-    begin = p.group[r].begin;
-    return p.group[r].tokens;
-}
-template <int kKind>
-__device__ __forceinline__ int unit_length(const AttentionParams& p, int r) { return kKind == kKindPrefix ? p.group[r].shared : row_length(p.c, r); }
-// Its first key (a multiple of kSharedUnit), the row of its table.
+// What a launch's rows have: all of their keys, or those behind a prefix that is shared (kda_kvcache_shared.cu),
+// which go on from the state (maximum, sum, output) that the prefix left for each query row.
+enum { kKindRows = 0, kKindSuffix = 1 };
+// A row's first key (a multiple of kSharedUnit).
 template <int kKind>
 __device__ __forceinline__ int unit_from(const AttentionParams& p, int r) { return kKind == kKindSuffix ? p.from[r] : 0; }
-template <int kKind>
-__device__ __forceinline__ int unit_row(const AttentionParams& p, int r) { return kKind == kKindPrefix ? p.group[r].row : r; }
 
 // Work of one share.
 __device__ __forceinline__ int64_t share_of(int64_t all, int shares) { return (all + shares - 1) / shares; }
@@ -170,20 +157,7 @@ __device__ __forceinline__ int64_t share_of(int64_t all, int shares) { return (a
 // The row that item number i of the joining launch belongs to, and the item's number in it.
 // Items are counted by an upper bound: row r's first is number (cu[r] * group / cols + r) *
 // heads, as its column blocks are at most n * group / cols + 1.  False: no such item.
-template <int kKind>
-__device__ __forceinline__ bool joined_item(const AttentionParams& p, int group, int cols, int64_t& i, int& row) {
-    const CacheParams& c = p.c;
-    if (kKind == kKindPrefix) {
-        int lo = 0, hi = p.groups;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if ((p.group[mid].begin * group / cols + mid) * c.heads <= i) lo = mid;
-            else hi = mid;
-        }
-        row = lo;
-        i -= (p.group[row].begin * group / cols + row) * c.heads;
-        return i >= 0;
-    }
+__device__ __forceinline__ bool joined_item(const CacheParams& c, int group, int cols, int64_t& i, int& row) {
     if (!c.cu) {
         const int64_t each = (int64_t)c.heads * ((group + cols - 1) / cols);
         row = (int)(i / each);
@@ -200,9 +174,7 @@ __device__ __forceinline__ bool joined_item(const AttentionParams& p, int group,
     }
     return row < c.rows && i >= 0;
 }
-inline int64_t joined_items(const AttentionParams& p, int kind, int64_t group, int cols) {
-    const CacheParams& c = p.c;
-    if (kind == kKindPrefix) return (c.tokens * group / cols + p.groups) * c.heads;
+inline int64_t joined_items(const CacheParams& c, int64_t group, int cols) {
     return c.cu ? (c.tokens * group / cols + c.rows) * c.heads : (int64_t)c.rows * c.heads * ((group + cols - 1) / cols);
 }
 

@@ -29,6 +29,7 @@
 // q's and the scales' handling is that file's too.
 #include "kda_kvcache_attention.cuh"
 #include "kda_ptx.cuh"
+#include "kda_tcgen05.cuh"
 
 namespace kda {
 namespace {
@@ -45,76 +46,21 @@ constexpr int64_t kWaitLimit = 1ll << 20;
 // Two CTAs an SM and no third: the tensor memory is for two.
 constexpr size_t kSmemBytes = 80 * 1024;
 
-// Two floats side by side: one instruction for both.
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpair(uint64_t p, float& a, float& b) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float y;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
-    return y;
-}
-
-// Matrix instructions by one thread of a converged warp: the election is part of each, so that
-// the descriptors stay in uniform registers (issued under `if (lane == 0)` four of them took 500
-// cycles).
-__device__ __forceinline__ void mma_ss_one(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\t.reg .b32 r;\n\telect.sync r|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-__device__ __forceinline__ void mma_ts_one(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\t.reg .b32 r;\n\telect.sync r|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-__device__ __forceinline__ void commit_one(uint32_t bar) {
-    asm volatile(
-        "{\n\t.reg .pred e;\n\t.reg .b32 r;\n\telect.sync r|e, 0xffffffff;\n\t"
-        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
-        : "memory");
-}
-
 // Named barriers for the issuing warp: K is widened; V is, and P is written; q is there.
 constexpr uint32_t kBarK = 1, kBarP = 2, kBarQ = 3;
 
-// fp16 operands, fp32 result; `b_rows`: B's rows are the reduction (channel-major).
-__host__ __device__ constexpr uint32_t idesc_f16(int n, bool b_rows) {
-    return (1u << 4) | ((uint32_t)b_rows << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
-}
-
 // Keys that column block `block` of a row sees, and its tiles (at least one).  (The host sees to it
 // that tokens times group fits in 31 bits.)
-template <int kKind>
 __device__ __forceinline__ int block_seen(int n, int len, int group, int block) {
-    if (kKind == kKindPrefix) return len;
     const int last = min(n * group - block * kRows, kRows) - 1 + block * kRows;
     return min(len, max(0, len - n + last / group + 1));
 }
 __device__ __forceinline__ int tiles_of(int seen) { return seen > kKeys ? (seen + kKeys - 1) / kKeys : 1; }
 __device__ __forceinline__ int blocks_of(int n, int group) { return (n * group + kRows - 1) / kRows; }
 // Tiles of the blocks before `block`, a lane each; the same in all lanes.
-template <int kKind>
 __device__ __forceinline__ int64_t tiles_before(int n, int len, int from, int group, int block) {
     int64_t x = 0;
-    for (int b = threadIdx.x & 31; b < block; b += 32) x += tiles_of(block_seen<kKind>(n, len, group, b) - from);
+    for (int b = threadIdx.x & 31; b < block; b += 32) x += tiles_of(block_seen(n, len, group, b) - from);
 #pragma unroll
     for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
@@ -148,7 +94,6 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
     const CacheParams& c = p.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const bool soft = tid < kSoft, issuer = warp == kSoft / 32;
-    const int rows = unit_count<kKind>(p);
     const int group = p.q_heads / c.heads;
     const int page_shift = __ffs(c.page_tokens) - 1;
     const int64_t block_bytes = (int64_t)c.page_tokens * kDim;
@@ -169,30 +114,30 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
         tmem_relinquish();
     }
     follow_stream();
-    int64_t* first = rows <= kMaxListed ? s_first : p.first_work;
+    int64_t* first = c.rows <= kMaxListed ? s_first : p.first_work;
     // Tiles of the rows.  As many rows as warps: a warp each.  More: a thread each, where a row has few
     // blocks, else its warp for it.
     constexpr int kFewBlocks = 4;
-    if (rows <= kThreads / 32) {
+    if (c.rows <= kThreads / 32) {
         int64_t begin;
-        const int n = warp < rows ? unit_tokens<kKind>(p, warp, begin) : 0, len = warp < rows ? unit_length<kKind>(p, warp) : 0;
-        const int from = warp < rows ? unit_from<kKind>(p, warp) : 0;
-        const int64_t tiles = tiles_before<kKind>(n, len, from, group, blocks_of(n, group));
+        const int n = warp < c.rows ? row_tokens(c, warp, begin) : 0, len = warp < c.rows ? row_length(c, warp) : 0;
+        const int from = warp < c.rows ? unit_from<kKind>(p, warp) : 0;
+        const int64_t tiles = tiles_before(n, len, from, group, blocks_of(n, group));
         if (lane == 0) s_tiles[warp] = tiles;
         __syncthreads();
     }
-    scan_rows<kThreads>(rows, first, s_scan, [&](int r) {
+    scan_rows<kThreads>(c.rows, first, s_scan, [&](int r) {
         int64_t tiles = 0;
-        if (rows <= kThreads / 32) {
-            if (r < rows) tiles = s_tiles[r];
+        if (c.rows <= kThreads / 32) {
+            if (r < c.rows) tiles = s_tiles[r];
         } else {
             int64_t begin;
-            const int n = r < rows ? unit_tokens<kKind>(p, r, begin) : 0, len = r < rows ? unit_length<kKind>(p, r) : 0, blocks = blocks_of(n, group);
-            const int from = r < rows ? unit_from<kKind>(p, r) : 0;
-            for (int x = 0; x < blocks && blocks <= kFewBlocks; ++x) tiles += tiles_of(block_seen<kKind>(n, len, group, x) - from);
+            const int n = r < c.rows ? row_tokens(c, r, begin) : 0, len = r < c.rows ? row_length(c, r) : 0, blocks = blocks_of(n, group);
+            const int from = r < c.rows ? unit_from<kKind>(p, r) : 0;
+            for (int x = 0; x < blocks && blocks <= kFewBlocks; ++x) tiles += tiles_of(block_seen(n, len, group, x) - from);
             for (unsigned many = __ballot_sync(0xffffffffu, blocks > kFewBlocks); many; many &= many - 1) {
                 const int src = __ffs(many) - 1;
-                const int64_t t = tiles_before<kKind>(__shfl_sync(0xffffffffu, n, src), __shfl_sync(0xffffffffu, len, src), __shfl_sync(0xffffffffu, from, src),
+                const int64_t t = tiles_before(__shfl_sync(0xffffffffu, n, src), __shfl_sync(0xffffffffu, len, src), __shfl_sync(0xffffffffu, from, src),
                                                       group, __shfl_sync(0xffffffffu, blocks, src));
                 if (lane == src) tiles = t;
             }
@@ -202,11 +147,11 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (blockIdx.x == 0 && rows <= kMaxListed)
-        for (int r = tid; r <= rows; r += kThreads) p.first_work[r] = s_first[r];
+    if (blockIdx.x == 0 && c.rows <= kMaxListed)
+        for (int r = tid; r <= c.rows; r += kThreads) p.first_work[r] = s_first[r];
     const uint32_t tmem = s_tmem, lanes = (uint32_t)(32 * (warp % 4)) << 16;
-    const int64_t per = share_of(first[rows], p.ctas);
-    const int64_t w_begin = per * blockIdx.x, w_end = min(first[rows], w_begin + per);
+    const int64_t per = share_of(first[c.rows], p.ctas);
+    const int64_t w_begin = per * blockIdx.x, w_end = min(first[c.rows], w_begin + per);
     uint32_t phase_s = 0, phase_o = 0;  // (phase_s: a bit for each buffer)
     // After a wait that ran out, all others end at once and what follows is garbage.
     auto wait = [&](uint32_t bar, uint32_t phase) {
@@ -224,15 +169,15 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
     // The item that begins in this share and ends in another: none yet.
     if (tid == 0) reinterpret_cast<SplitItem*>(p.split_items)[blockIdx.x].last = -1;
     for (int64_t w = w_begin; w < w_end;) {
-        const int row = row_of(first, rows, w);
+        const int row = row_of(first, c.rows, w);
         int64_t begin;
-        const int n = unit_tokens<kKind>(p, row, begin), len = unit_length<kKind>(p, row), from = unit_from<kKind>(p, row);
+        const int n = row_tokens(c, row, begin), len = row_length(c, row), from = unit_from<kKind>(p, row);
         const int64_t each = (first[row + 1] - first[row]) / c.heads;  // tiles of a head's blocks
         const int head = (int)((w - first[row]) / each);
         int64_t item = first[row] + head * each;
         int block = 0, tiles = 0;
         for (int b0 = 0;; b0 += 32) {  // 32 blocks at a time: the one that w falls into
-            const int mine = tiles_of(block_seen<kKind>(n, len, group, b0 + lane) - from);
+            const int mine = tiles_of(block_seen(n, len, group, b0 + lane) - from);
             int64_t end = mine;  // of the blocks up to this lane's
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -252,15 +197,15 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
         const int64_t item_end = item + tiles;
         const int rows_all = n * group, row0 = block * kRows, f = row0 + tid % 128;
         const bool there = f < rows_all;
-        const int seen_max = block_seen<kKind>(n, len, group, block);
-        const int seen_min = kKind == kKindPrefix ? len : max(0, min(len, len - n + row0 / group + 1));
-        const int seen = !there ? 0 : kKind == kKindPrefix ? len : max(0, min(len, len - n + f / group + 1));
+        const int seen_max = block_seen(n, len, group, block);
+        const int seen_min = max(0, min(len, len - n + row0 / group + 1));
+        const int seen = there ? max(0, min(len, len - n + f / group + 1)) : 0;
         const int tile0 = (int)(w - item) + from / kKeys;
         const int tile1 = min((int)(min(item_end, w_end) - item) + from / kKeys, (seen_max + kKeys - 1) / kKeys);
         const bool goes_on = kKind == kKindSuffix && w == item && from > 0;  // from the prefix
         const int64_t state = (begin + (there ? f / group : 0)) * p.q_heads + head * group + (there ? f % group : 0);  // this thread's row there
 
-        const int32_t* table = c.tables + (int64_t)unit_row<kKind>(p, row) * c.width;
+        const int32_t* table = c.tables + (int64_t)row * c.width;
         // This thread's row of q as fp16 into shared memory.
         float factor = 0.f;
         if (soft) {
@@ -559,7 +504,6 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
             p.part_ml[(slot * 2 + 0) * kRows + tid] = m;
             p.part_ml[(slot * 2 + 1) * kRows + tid] = l;
         }
-        if (kKind == kKindPrefix && whole && soft && there) p.state_ml[state] = make_float2(m, l);
 #pragma unroll
         for (int q = 0; q < kDim && soft; q += 16) {
             uint32_t o[16];
@@ -570,13 +514,7 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[i] = 0u;
             }
-            if (whole && kKind == kKindPrefix) {
-#pragma unroll
-                for (int i = 0; i < 16; i += 4)
-                    if (there)
-                        *reinterpret_cast<float4*>(p.state_o + state * kDim + q + i) =
-                            make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]), __uint_as_float(o[i + 2]), __uint_as_float(o[i + 3]));
-            } else if (whole) {
+            if (whole) {
                 if (there) {
 #pragma unroll
                     for (int i = 0; i < 16; i += 8) {
@@ -625,17 +563,17 @@ __global__ void __launch_bounds__(kRows * kShares, kShares == 4 ? 2 : 1) block_j
     } else {
         int64_t i = blockIdx.x;
         int row;
-        const bool there = joined_item<kKind>(p, group, kRows, i, row);
+        const bool there = joined_item(c, group, kRows, i, row);
         begin = n = 0;
-        if (there) n = unit_tokens<kKind>(p, row, begin);
-        const int len = there ? unit_length<kKind>(p, row) : 0, from = there ? unit_from<kKind>(p, row) : 0, blocks = blocks_of(n, group);
+        if (there) n = row_tokens(c, row, begin);
+        const int len = there ? row_length(c, row) : 0, from = there ? unit_from<kKind>(p, row) : 0, blocks = blocks_of(n, group);
         const bool ours = blocks > 0 && i < (int64_t)blocks * c.heads;
         head = ours ? (int)(i / blocks) : 0, block = ours ? (int)(i % blocks) : 0;
-        const int64_t before = tiles_before<kKind>(n, len, from, group, block);
-        const int tiles = ours ? tiles_of(block_seen<kKind>(n, len, group, block) - from) : 0;
+        const int64_t before = tiles_before(n, len, from, group, block);
+        const int tiles = ours ? tiles_of(block_seen(n, len, group, block) - from) : 0;
         follow_stream();
         if (!ours) return;
-        const int64_t per = share_of(p.first_work[unit_count<kKind>(p)], p.ctas);
+        const int64_t per = share_of(p.first_work[c.rows], p.ctas);
         const int64_t each = (p.first_work[row + 1] - p.first_work[row]) / c.heads;
         const int64_t w0 = p.first_work[row] + head * each + before, w1 = w0 + tiles;
         u0 = w0 / per, u1 = (w1 - 1) / per, slot0 = 2 * u0 + (u0 * per >= w0 ? 0 : 1);
@@ -687,13 +625,6 @@ __global__ void __launch_bounds__(kRows * kShares, kShares == 4 ? 2 : 1) block_j
         }
     }
     if (!mine) return;
-    if constexpr (kKind == kKindPrefix) {
-        const int64_t state = (begin + f / group) * p.q_heads + head * group + f % group;
-        if (d0 == 0) p.state_ml[state] = make_float2(top, sum);
-#pragma unroll
-        for (int d = 0; d < kCh; d += 4) *reinterpret_cast<float4*>(p.state_o + state * kDim + d0 + d) = make_float4(acc[d], acc[d + 1], acc[d + 2], acc[d + 3]);
-        return;
-    }
     const float by = sum > 0.f ? 1.f / sum : 0.f;
     T* out = static_cast<T*>(p.out) + (begin + f / group) * p.out_stride + (int64_t)(head * group + f % group) * kDim + d0;
 #pragma unroll
@@ -708,7 +639,7 @@ cudaError_t launch_dim(const AttentionParams& p, cudaStream_t stream) {
     e = launch_early(block_attention_kernel<T, kDim, kKind>, dim3(p.ctas), kThreads, kSmemBytes, stream, 1, p);
     if (e != cudaSuccess) return e;
     // As many threads to a row as one wave holds: few items have many parts each.
-    const int64_t items = joined_items(p, kKind, p.q_heads / p.c.heads, kRows);
+    const int64_t items = joined_items(p.c, p.q_heads / p.c.heads, kRows);
     if (items * (kDim / 4) <= 2 * p.sm_count)
         return launch_early(block_join_kernel<T, kDim, 8, kKind>, dim3((unsigned)items, kDim / 4), kRows * 8, 0, stream, 1, p);
     if (items * (kDim / 8) <= 4 * p.sm_count)
@@ -724,7 +655,6 @@ cudaError_t launch_kind(const AttentionParams& p, bool f16, cudaStream_t stream)
 }  // namespace
 
 cudaError_t launch_block_attention(const AttentionParams& p, bool f16, cudaStream_t stream) { return launch_kind<kKindRows>(p, f16, stream); }
-cudaError_t launch_block_prefix(const AttentionParams& p, bool f16, cudaStream_t stream) { return launch_kind<kKindPrefix>(p, f16, stream); }
 cudaError_t launch_block_suffix(const AttentionParams& p, bool f16, cudaStream_t stream) { return launch_kind<kKindSuffix>(p, f16, stream); }
 
 }  // namespace kda

@@ -165,6 +165,7 @@ struct AttentionParams {
     const int32_t* from;      // [rows]: tokens of the prefix
     float* state_o;           // [tokens * q_heads][dim], what the prefix left: outputs,
     float2* state_ml;         // [tokens * q_heads], maxima and sums
+    int64_t* first_item;      // [groups + 1] (kda_kvcache_prefix.cu)
 };
 size_t attention_slots(int ctas);
 int attention_cols(const CacheParams& c, int32_t group, int sm_count);
@@ -183,7 +184,9 @@ struct SharedPlan {
     int32_t* from;
 };
 cudaError_t launch_shared_plan(const SharedPlan& p, cudaStream_t stream);
-cudaError_t launch_block_prefix(const AttentionParams& p, bool f16, cudaStream_t stream);
+constexpr int kPrefixLanes = 256;  // query rows of an item, and of a part
+int64_t prefix_items(const AttentionParams& p);  // at most
+cudaError_t launch_prefix(const AttentionParams& p, bool f16, cudaStream_t stream);
 cudaError_t launch_block_suffix(const AttentionParams& p, bool f16, cudaStream_t stream);
 cudaError_t launch_suffix(const AttentionParams& p, int cols, bool f16, cudaStream_t stream);
 

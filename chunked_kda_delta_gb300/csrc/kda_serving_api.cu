@@ -1,7 +1,7 @@
 // kda_serving_api.cu -- the C ABI of the serving operators: page operations, the 8-bit
 // key/value cache, penalties on logits and beam selection.  Validation, scratch layout and launches; the kernels
 // live in kda_pages.cu, kda_kvcache_append.cu, kda_kvcache_rotary.cu, kda_kvcache_attention.cu,
-// kda_kvcache_block.cu, kda_kvcache_shared.cu, kda_logits.cu and kda_beam.cu.
+// kda_kvcache_block.cu, kda_kvcache_prefix.cu, kda_kvcache_shared.cu, kda_logits.cu and kda_beam.cu.
 #include <math.h>
 
 #include <exception>
@@ -281,12 +281,14 @@ kda_status attend(const kda_kvcache* cache, const void* q, int32_t num_q_heads, 
     const int cols = kda::attention_cols(p.c, group, di->sm_count);
     p.sm_count = di->sm_count;
     p.ctas = kda::attention_ctas(cache->head_dim, cols, f16, di->sm_count);
-    const int block_ctas = kda::attention_ctas(cache->head_dim, kda::kBlockRows, f16, di->sm_count);
-    const auto parts_of = [&](int c, int ctas) { return (c == kda::kBlockRows ? (size_t)2 * ctas : kda::attention_slots(ctas)) * c; };
     // With shared prefixes the parts' place is the prefixes' first, then the rows'.
-    size_t parts = parts_of(cols, p.ctas);
-    if (cu_rows && parts_of(kda::kBlockRows, block_ctas) > parts) parts = parts_of(kda::kBlockRows, block_ctas);
-    const int most_ctas = p.ctas > block_ctas ? p.ctas : block_ctas;
+    p.q_heads = num_q_heads;
+    p.groups = groups;
+    size_t parts = (cols == kda::kBlockRows ? (size_t)2 * p.ctas : kda::attention_slots(p.ctas)) * cols;
+    if (cu_rows) {
+        const size_t prefix = (size_t)(kda::prefix_items(p) + di->sm_count) * kda::kPrefixLanes;
+        if (prefix > parts) parts = prefix;
+    }
     const size_t units = (size_t)(groups > cache->rows ? groups : cache->rows), query_rows = cu_rows ? (size_t)num_tokens * num_q_heads : 0;
     size_t bytes = 0;
     auto place = [&](size_t n) {
@@ -294,10 +296,10 @@ kda_status attend(const kda_kvcache* cache, const void* q, int32_t num_q_heads, 
         bytes += (n + 255) / 256 * 256;
         return at;
     };
-    const size_t at_o = place(parts * cache->head_dim * 4), at_ml = place(parts * 2 * 4), at_split = place((size_t)most_ctas * 32),
+    const size_t at_o = place(parts * cache->head_dim * 4), at_ml = place(parts * 2 * 4), at_split = place((size_t)p.ctas * 32),
                  at_first = place((units + 1) * 8), at_group = place((size_t)groups * sizeof(kda::SharedGroup)),
                  at_from = place(cu_rows ? (size_t)cache->rows * 4 : 0), at_state = place(query_rows * cache->head_dim * 4),
-                 at_state_ml = place(query_rows * 8);
+                 at_state_ml = place(query_rows * 8), at_item = place(cu_rows ? (units + 1) * 8 : 0);
     Scratch ws;
     if ((st = ws.take(dev, stream, bytes)) != KDA_OK) return st;
     p.part_o = reinterpret_cast<float*>(ws.base + at_o);
@@ -308,7 +310,6 @@ kda_status attend(const kda_kvcache* cache, const void* q, int32_t num_q_heads, 
     p.out = out;
     p.q_stride = q_stride;
     p.out_stride = out_stride;
-    p.q_heads = num_q_heads;
     p.scale = scale * 1.4426950408889634f;
     const cudaStream_t on = (cudaStream_t)stream;
     if (!cu_rows) {
@@ -317,14 +318,14 @@ kda_status attend(const kda_kvcache* cache, const void* q, int32_t num_q_heads, 
     }
     kda::SharedPlan plan{p.c, cu_rows, groups, reinterpret_cast<kda::SharedGroup*>(ws.base + at_group), reinterpret_cast<int32_t*>(ws.base + at_from)};
     p.group = plan.group;
-    p.groups = groups;
     p.from = plan.from;
     p.state_o = reinterpret_cast<float*>(ws.base + at_state);
     p.state_ml = reinterpret_cast<float2*>(ws.base + at_state_ml);
+    p.first_item = reinterpret_cast<int64_t*>(ws.base + at_item);
     kda::AttentionParams prefix = p;
-    prefix.ctas = block_ctas;
+    prefix.ctas = di->sm_count;
     cudaError_t e = kda::launch_shared_plan(plan, on);
-    if (e == cudaSuccess) e = kda::launch_block_prefix(prefix, f16, on);
+    if (e == cudaSuccess) e = kda::launch_prefix(prefix, f16, on);
     if (e == cudaSuccess) e = kda::launch_suffix(p, cols, f16, on);
     return e == cudaSuccess ? KDA_OK : cuda_fail(e, "shared attention launch");
 }
