@@ -191,6 +191,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     auto wait = [&](uint32_t bar, uint32_t phase) {
         if (!mbar_try_wait(bar, phase & 1) && !mbar_wait(bar, phase & 1, s_bad ? 1 : kWaitLimit)) s_bad = 1;
     };
+    // For several barriers at once, a lane each (a wait costs 150 cycles also where it is over).
+    auto wait_lanes = [&](bool some, uint32_t bar, uint32_t phase) {
+        bool done = !some || mbar_test(bar, phase & 1);
+        for (int64_t i = s_bad ? 1 : 64 * kWaitLimit; !__all_sync(0xffffffffu, done) && i > 0; --i)
+            if (!done) done = mbar_test(bar, phase & 1);
+        if (!done) s_bad = 1;
+        __syncwarp();
+    };
     uint32_t base = 0;           // tiles before this item
     uint32_t steps[2] = {0, 0};  // steps of the softmax groups before this item
 
@@ -466,23 +474,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
             const int n = it.steps(tiles, grp);
             const uint32_t t_grp = tmem + grp * kColGroup;
             const uint64_t qd = sdesc(smem_u32(q_sm + grp * kQBytes<kDim>), kLbo, kSbo);
-            int passed_k = 1 - grp, passed_v = 1 - grp;  // the other group's next tile
-            auto pass_k = [&](int end) {
-                for (; !wide && passed_k < end; passed_k += 2) {
-                    wait(k_full(base + passed_k), (base + passed_k) / kSlots);
-                    if (lane == 0) mbar_arrive(k_empty(base + passed_k));
-                }
-            };
-            auto pass_v = [&](int end) {
-                for (; !wide && passed_v < end; passed_v += 2) {
-                    wait(v_full(base + passed_v), (base + passed_v) / kSlots);
-                    if (lane == 0) mbar_arrive(v_empty(base + passed_v));
-                }
+            // Waits for the tile, and for the one before it, which the other group has alone, and passes that one.
+            auto wait_tile = [&](uint32_t full, uint32_t empty, int tile, bool also, uint32_t bar, uint32_t phase) {
+                const uint32_t number = base + tile, before = number - 1;
+                const bool passes = !wide && tile > 0;
+                wait_lanes(lane == 0 ? also : lane == 1 ? tile < tiles : lane == 2 && passes, lane == 0 ? bar : full + 8 * ((lane == 1 ? number : before) % kSlots),
+                           lane == 0 ? phase : (lane == 1 ? number : before) / kSlots);
+                if (lane == 2 && passes) mbar_arrive(empty + 8 * (before % kSlots));
             };
             auto issue_s = [&](int i) {
-                const uint32_t number = uniform(base + (wide ? i : 2 * i + grp)), u = uniform(steps[grp] + i);
-                pass_k(2 * i + grp);
-                wait(k_full(number), number / kSlots);
+                const int tile = wide ? i : 2 * i + grp;
+                const uint32_t number = uniform(base + tile), u = uniform(steps[grp] + i);
+                wait_tile(k_full(0), k_empty(0), tile, i > 1, o_done(grp, u), (u - 2) >> 1);  // S takes the place of its weights
                 tc_fence_after();
                 const uint64_t kd = sdesc(smem_u32(k_sm + number % kSlots * kTileBytes<kDim>), kLbo, kSbo);
 #pragma unroll
@@ -490,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                     mma_ss_one(t_grp + (u & 1) * kKeys, qd + kk * (2 * kLbo / 16), kd + kk * (2 * kLbo / 16), idesc_f16(kKeys, false), kk > 0);
                 commit_one(s_full(grp, u));
                 commit_one(k_empty(number));
-                if (lane == 0) mbar_arrive(s_full(grp, u));
+                if (lane == 1) mbar_arrive(s_full(grp, u));  // (the lane that has waited for the tile)
             };
             if (n > 0) {
                 named_bar_sync(kBarGroup + grp, kRows + 32);
@@ -500,13 +503,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
 #pragma unroll 1
             for (int i = 0; i < n; ++i) {
                 const uint32_t number = uniform(base + (wide ? i : 2 * i + grp)), u = uniform(steps[grp] + i);
-                if (i + 1 < n) {
-                    if (i > 0) wait(o_done(grp, u - 1), (u - 1) >> 1);  // S takes the place of its weights
-                    issue_s(i + 1);
-                }
-                pass_v(2 * i + grp);
-                wait(v_full(number), number / kSlots);
-                wait(p_full(grp, u), u >> 1);
+                if (i + 1 < n) issue_s(i + 1);
+                wait_tile(v_full(0), v_empty(0), wide ? i : 2 * i + grp, true, p_full(grp, u), u >> 1);
                 tc_fence_after();
                 const uint64_t vd = sdesc(smem_u32(v_sm + number % kSlots * kTileBytes<kDim>), kBoxBytes, 1024) | ((uint64_t)2 << 61);
 #pragma unroll
@@ -515,8 +513,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                 commit_one(o_done(grp, u));
                 commit_one(v_empty(number));
             }
-            pass_k(tiles);
-            pass_v(tiles);
+            // A last tile of the other group.
+            const int last = 2 * n + grp - 1;  // (n tiles of this group were 2 i + grp, i < n)
+            if (!wide && last >= 0 && last < tiles && (last & 1) != grp) {
+                wait_lanes(lane < 2, lane == 0 ? k_full(base + last) : v_full(base + last), (base + last) / kSlots);
+                if (lane < 2) mbar_arrive(lane == 0 ? k_empty(base + last) : v_empty(base + last));
+            }
         });
     } else {
         each_item([&](const SharedGroup& sg, const Item& it, int tile0, int tiles) {

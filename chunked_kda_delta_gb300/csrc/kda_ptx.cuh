@@ -68,6 +68,18 @@ __device__ __forceinline__ bool mbar_try_wait_now(uint32_t bar, uint32_t parity)
         : "memory");
     return ok != 0;
 }
+// Whether the phase with this parity is complete, without waiting for it.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ bool mbar_wait_now(uint32_t bar, uint32_t parity, int64_t limit) {
     for (int64_t i = 0; i < limit; ++i)
         if (mbar_try_wait_now(bar, parity)) return true;
