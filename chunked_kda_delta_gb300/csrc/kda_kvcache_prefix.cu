@@ -301,26 +301,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                     if constexpr (kMine == 4) tmem_ld32(t_b + 32, sr + 32);
                 }
                 const Meta* metas = s_meta[(base + it.tile_of(grp, i)) % kMetaTiles] + block0;  // (in registers they would spill)
-                bool missing = false, low = false;
 #pragma unroll
                 for (int x = 0; x < kMine; ++x) {
-                    const Meta b = metas[x];
-                    missing |= b.k < 0.f;
-                    least = fmaxf(least, b.v - kScaleSpan);
+                    least = fmaxf(least, metas[x].v - kScaleSpan);
                 }
                 tmem_wait_ld_regs<16 * kMine>(sr);
-                if (missing) {
-#pragma unroll
-                    for (int x = 0; x < kMine; ++x)
-                        if (metas[x].k < 0.f)
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) sr[16 * x + j] = __float_as_uint(kNegInf);
-                }
                 float top = kNegInf;
 #pragma unroll
                 for (int x = 0; x < kMine; ++x) {
                     const Meta b = metas[x];
-                    low |= b.v < least;
                     float y = max3(__uint_as_float(sr[16 * x]), __uint_as_float(sr[16 * x + 1]), __uint_as_float(sr[16 * x + 2]));
                     float z = max3(__uint_as_float(sr[16 * x + 3]), __uint_as_float(sr[16 * x + 4]), __uint_as_float(sr[16 * x + 5]));
 #pragma unroll
@@ -329,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                         z = max3(z, __uint_as_float(sr[16 * x + k + 2]), __uint_as_float(sr[16 * x + k + 3]));
                     }
                     y = fmaxf(max3(y, z, __uint_as_float(sr[16 * x + 14])), __uint_as_float(sr[16 * x + 15]));
-                    top = fmaxf(top, y == kNegInf ? kNegInf : fmaf(y, b.k * factor, fmaxf(b.v, least)));  // (a scale of 0 makes scores 0)
+                    top = fmaxf(top, b.k < 0.f ? kNegInf : fmaf(y, b.k * factor, fmaxf(b.v, least)));  // (not of a missing page)
                 }
                 // The reference of the weights.
                 const float m_new = top > m + kGrowth || m == kNegInf ? fmaxf(m, top) : m;
@@ -340,9 +329,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
 #pragma unroll
                 for (int x = 0; x < kMine; ++x) {
                     const Meta b = metas[x];
-                    // (A factor of 0 must not make masked scores NaN.)
-                    const float k = b.k * factor > 0.f ? b.k * factor : 0x1p-126f, lv = fmaxf(b.v, least);
-                    const float bias = lv - m_use + kLift;
+                    // (Scores are finite, those of a missing page 0: its weights are 0 by -inf.)
+                    const float k = b.k * factor, lv = fmaxf(b.v, least), bias = b.k < 0.f ? kNegInf : lv - m_use + kLift;
                     const uint64_t k2 = pair(k, k), bias2 = pair(bias, bias);
                     uint64_t acc[2] = {0, 0};  // (+0, +0)
 #pragma unroll
@@ -358,16 +346,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                     unpair(add2(acc[0], acc[1]), sum[0], sum[1]);
                     l += (sum[0] + sum[1]) * exp2_fast(-lv);
                 }
-                if (low) {
-#pragma unroll
-                    for (int x = 0; x < kMine; ++x) {
-                        const float by = exp2_fast(fminf(metas[x].v - least, 0.f));
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) sr[8 * x + j] = brought_down(sr[8 * x + j], by);
-                    }
-                }
 #pragma unroll
                 for (int x = 0; x < kMine; ++x) tmem_st8(t_b + 8 * (block0 + x), *reinterpret_cast<uint32_t(*)[8]>(sr + 8 * x));
+                // Rare, so taken once more from tensor memory: held in registers until here it cost a step 8%.
+                if (fminf(fminf(metas[0].v, metas[kMine > 1].v), fminf(metas[kMine / 2].v, metas[kMine - 1].v)) < least) {
+                    tmem_wait_st();
+#pragma unroll 1
+                    for (int x = 0; x < kMine; ++x) {
+                        const float by = exp2_fast(fminf(metas[x].v - least, 0.f));
+                        uint32_t w[8];
+                        tmem_ld8(t_b + 8 * (block0 + x), w);
+                        tmem_wait_ld_regs<8>(w);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) w[j] = brought_down(w[j], by);
+                        tmem_st8(t_b + 8 * (block0 + x), w);
+                    }
+                }
                 if constexpr (kMine < 4) {  // the other copies' keys
                     const uint32_t zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
