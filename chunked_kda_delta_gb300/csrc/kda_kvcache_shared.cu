@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
     __syncthreads();
     const int ref = s_ref;
     const int64_t begin = c.cu ? c.cu[r0] : r0, end = c.cu ? c.cu[r1] : r1;
-    const bool shares = s_active > 1 && s_tokens == end - begin;  // (malformed offsets: the row's tokens do not count)
+    const bool shares = s_active >= p.least && s_tokens == end - begin;  // (malformed offsets: the row's tokens do not count)
     const int entries = shares ? s_limit / kSharedUnit * kSharedUnit / c.page_tokens : 0;
     if (entries > 0) {
         const int32_t* first = c.tables + (int64_t)ref * c.width;
@@ -98,6 +98,24 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
 }
 
 }  // namespace
+
+// Whether the prefixes' three kernels can be worth their 55 us, if tables were full and rows had them in
+// common but for one row a group.  The kernels for few query rows a row read pages at 8 TB/s (of one
+// another's out of L2 too); those of many take an SM `cycles` for 64 keys of 128 query rows, of one row there,
+// of a group here.  8 heads, dim 128, shared against not (us): 8 rows of 4196 keys 44 and 29, of 16484 63 and 59,
+// of 32868 75 and 94; 8 groups of 4 rows of 4196 keys 71 and 51, of 8292 85 and 82, 16 groups of 16684 192
+// and 270; 8 rows with 6 tokens of 8292 keys 75 and 70, 64 of 16684 392 and 625; pieces of 64 tokens gain nothing.
+// A state past 2^27 numbers would be a workspace of a GB.
+bool sharing_pays(const AttentionParams& p, int cols) {
+    const CacheParams& c = p.c;
+    const int64_t group = p.q_heads / c.heads;
+    if (p.groups >= c.rows || c.tokens * p.q_heads * c.dim > (1 << 27)) return false;
+    const double keys = (double)c.width * c.page_tokens * c.heads, cycles = c.dim == 64 ? 900 : 1350;
+    if (cols < kBlockRows) return (double)(c.rows - p.groups) * keys * 2 * c.dim / 8e6 >= 55;
+    const int64_t each = (c.tokens + c.rows - 1) / c.rows * group;
+    const int64_t saved = c.rows * ((each + kBlockRows - 1) / kBlockRows) - (c.tokens * group + kBlockRows - 1) / kBlockRows;
+    return (double)saved * keys / 64 * cycles / (1900.0 * p.sm_count) >= 55;
+}
 
 cudaError_t launch_shared_plan(const SharedPlan& p, cudaStream_t stream) {
     return launch_early(plan_kernel, dim3((unsigned)p.groups * kCluster), kThreads, 0, stream, kCluster, p);

@@ -180,9 +180,11 @@ struct SharedPlan {
     CacheParams c;
     const int32_t* cu_rows;   // [groups + 1]
     int32_t groups;
+    int32_t least;            // rows with tokens that a group must have to share
     SharedGroup* group;
     int32_t* from;
 };
+bool sharing_pays(const AttentionParams& p, int cols);  // cols: attention_cols
 cudaError_t launch_shared_plan(const SharedPlan& p, cudaStream_t stream);
 constexpr int kPrefixLanes = 256;  // query rows of an item, and of a part
 int64_t prefix_items(const AttentionParams& p);  // at most

@@ -284,12 +284,13 @@ kda_status attend(const kda_kvcache* cache, const void* q, int32_t num_q_heads, 
     // With shared prefixes the parts' place is the prefixes' first, then the rows'.
     p.q_heads = num_q_heads;
     p.groups = groups;
+    if (cu_rows && !kda::sharing_pays(p, cols)) cu_rows = nullptr, groups = 0;
     size_t parts = (cols == kda::kBlockRows ? (size_t)2 * p.ctas : kda::attention_slots(p.ctas)) * cols;
     if (cu_rows) {
         const size_t prefix = (size_t)(kda::prefix_items(p) + di->sm_count) * kda::kPrefixLanes;
         if (prefix > parts) parts = prefix;
     }
-    const size_t units = (size_t)(groups > cache->rows ? groups : cache->rows), query_rows = cu_rows ? (size_t)num_tokens * num_q_heads : 0;
+    const size_t units = (size_t)cache->rows, query_rows = cu_rows ? (size_t)num_tokens * num_q_heads : 0;
     size_t bytes = 0;
     auto place = [&](size_t n) {
         const size_t at = bytes;
@@ -316,7 +317,10 @@ kda_status attend(const kda_kvcache* cache, const void* q, int32_t num_q_heads, 
         const cudaError_t e = kda::launch_attention(p, cols, f16, on);
         return e == cudaSuccess ? KDA_OK : cuda_fail(e, "cache attention launch");
     }
-    kda::SharedPlan plan{p.c, cu_rows, groups, reinterpret_cast<kda::SharedGroup*>(ws.base + at_group), reinterpret_cast<int32_t*>(ws.base + at_from)};
+    // (A tile of the prefixes' kernel is 1.3 us of an SM, as much as two rows' with few query rows each: 32 pairs of
+    // rows of 16684 keys took 308 us with shared prefixes and 274 without, 21 groups of three 226 and 268.)
+    const int32_t least = cols == 8 ? 3 : 2;
+    kda::SharedPlan plan{p.c, cu_rows, groups, least, reinterpret_cast<kda::SharedGroup*>(ws.base + at_group), reinterpret_cast<int32_t*>(ws.base + at_from)};
     p.group = plan.group;
     p.from = plan.from;
     p.state_o = reinterpret_cast<float*>(ws.base + at_state);

@@ -176,7 +176,8 @@ def kda_kvcache_attention_shared(q: torch.Tensor, k_codes: torch.Tensor, v_codes
     Rows ``cu_rows[g]`` to ``cu_rows[g + 1] - 1`` (int32 ``[groups + 1]``) are a group, a request's beams
     or the users of one system prompt: the keys that all of them have in the same pages (as
     :func:`kda_pages_fork` leaves them) are gone through once for the group.  The result is the same for
-    any groups.
+    any groups.  Where the sizes say that nothing is to be gained (small tables, as many groups as rows)
+    nothing is shared, and ``cu_rows`` not read.
     """
     return (_ext or _binding()).kvcache_attention_shared(q, k_codes, v_codes, k_scale, v_scale, tables, lens,
                                                          cu_tokens, scale, out, _handle(stream), cu_rows)

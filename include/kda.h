@@ -436,9 +436,11 @@ kda_status kda_kvcache_attention(const kda_kvcache* cache, const void* q, int32_
  * a request or the users of one system prompt: the keys that all rows of a group have in the same pages
  * are gone through once for the whole group.  The result is kda_kvcache_attention's (sums in another
  * order), whatever the groups are: what their rows share is found in the tables, in whole units of 128
- * tokens, as kda_pages_fork leaves it.
+ * tokens, as kda_pages_fork leaves it.  Where the sizes say that nothing is to be gained (small tables, as
+ * many groups as rows) cu_rows is not read.
  *   cu_rows     device int32 [num_groups + 1] (cu_seqlens rules): group g is rows cu_rows[g] ..
- *               cu_rows[g + 1] - 1; malformed offsets are recorded and nothing is shared
+ *               cu_rows[g + 1] - 1; nothing is shared with malformed offsets, which are
+ *               recorded where they are read
  *   num_groups  >= 1, unless there are no rows
  * Everything else as kda_kvcache_attention. */
 kda_status kda_kvcache_attention_shared(const kda_kvcache* cache, const void* q, int32_t num_q_heads,

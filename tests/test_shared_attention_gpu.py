@@ -13,26 +13,27 @@ from step_testutil import DT, F8, cu_of, ints
 pytestmark = pytest.mark.gpu
 
 
-def make_cache(rng, groups, page, hkv, d, spare=3):
+def make_cache(rng, groups, page, hkv, d, spare=3, full=True):
     """groups: lists of (tokens in common with the group's first row, tokens in all), one for each row.  Pages of
     whole common tokens are shared, the others the row's own; what a page holds past a row's tokens is NaN where
-    nobody else holds it."""
+    nobody else holds it.  full: tables of a width with which sharing can pay."""
     tables, lens = [], []
     pages = sum(-(-n // page) for g in groups for _, n in g) + spare
     order, at = rng.permutation(pages), 0
     kc, vc = (rng.integers(0, 256, (pages, hkv, page, d), dtype=np.uint8) for _ in range(2))
     for c in (kc, vc):
         c[(c & 0x7F) == 0x7F] = 0x11
-    width = max([1] + [-(-n // page) for g in groups for _, n in g])
+    rows = sum(len(g) for g in groups)
+    width = max([1] + [-(-n // page) for g in groups for _, n in g]) + (4_000_000 // page // max(1, rows - len(groups)) if full else 0)
     for g in groups:
         first = None
         for common, n in g:
-            need, full = -(-n // page), min(common, n) // page if first is not None else 0
+            need, same = -(-n // page), min(common, n) // page if first is not None else 0
             t = np.full(width, -1)
-            t[:full] = first[:full] if first is not None else 0
-            t[full:need] = order[at: at + need - full]
-            at += need - full
-            if n % page and need > full:
+            t[:same] = first[:same] if first is not None else 0
+            t[same:need] = order[at: at + need - same]
+            at += need - same
+            if n % page and need > same:
                 for c in (kc, vc):
                     c[t[need - 1], :, n % page:] |= 0x7F
             first = t if first is None else first
@@ -46,8 +47,8 @@ def gpu_cache(kc, vc, ks, vs, tables):
     return (torch.as_tensor(kc).cuda().view(F8), torch.as_tensor(vc).cuda().view(F8), torch.as_tensor(ks).cuda(), torch.as_tensor(vs).cuda(), ints(tables))
 
 
-def check(rng, groups, counts, hq, hkv, d, page, dtype, cu=True, q_scale=1.0, change=None, cu_rows=None, status=0, exact=True):
-    kc, vc, ks, vs, tables, lens = make_cache(rng, groups, page, hkv, d)
+def check(rng, groups, counts, hq, hkv, d, page, dtype, cu=True, q_scale=1.0, change=None, cu_rows=None, status=0, exact=True, full=True):
+    kc, vc, ks, vs, tables, lens = make_cache(rng, groups, page, hkv, d, full=full)
     if change:
         change(kc, vc, ks, vs, tables)
     q = torch.as_tensor(rng.standard_normal((sum(counts), hq, d)) * q_scale).to(DT[dtype])
@@ -88,11 +89,11 @@ def test_several_tokens(hq, hkv, d, page):
 @pytest.mark.parametrize("d,page,group,dtype", [(128, 16, 8, "bf16"), (128, 128, 5, "fp16"), (64, 32, 8, "bf16"), (64, 64, 7, "fp16")])
 def test_pieces_of_prompts_behind_a_prefix(d, page, group, dtype):
     # rows of more query rows than the kernel for few of them takes
-    groups = [[(0, 900), (512, 700), (512, 613)], [(0, 300), (128, 333)]]
-    check(np.random.default_rng(d + page), groups, [150, 77, 100, 40, 180], 2 * group, 2, d, page, dtype)
+    groups = [[(0, 900), (512, 700), (512, 613)] + [(512, 600)] * 9, [(0, 300), (128, 333)]]
+    check(np.random.default_rng(d + page), groups, [9, 7, 50, 1, 3, 60, 1, 0, 1, 1, 1, 2, 9, 12], 2 * group, 2, d, page, dtype)
 
 
-@pytest.mark.parametrize("rows,hq,hkv,d,shared,page", [(2, 2, 1, 128, 128, 128), (33, 8, 1, 64, 640, 16), (70, 16, 2, 128, 384, 64), (300, 4, 1, 64, 256, 32)])
+@pytest.mark.parametrize("rows,hq,hkv,d,shared,page", [(2, 20, 1, 128, 128, 128), (3, 2, 1, 128, 128, 128), (33, 8, 1, 64, 640, 16), (70, 16, 2, 128, 384, 64), (300, 4, 1, 64, 256, 32)])
 def test_large_groups(rows, hq, hkv, d, shared, page):
     rng = np.random.default_rng(rows)
     group = [(0, shared + 20)] + [(shared, shared + int(n)) for n in rng.integers(1, 60, rows - 1)]
@@ -112,8 +113,8 @@ def test_long_prefixes_and_many_groups(d):
 
 def test_group_sizes_past_the_kernels_lists():
     rng = np.random.default_rng(1)
-    groups = [[(0, 140), (128, 131)] for _ in range(1200)]
-    check(rng, groups, [1] * 2400, 2, 1, 64, 16, "bf16", cu=False, exact=False)
+    groups = [[(0, 140), (128, 131), (128, 129)] for _ in range(1200)]
+    check(rng, groups, [1] * 3600, 2, 1, 64, 16, "bf16", cu=False, exact=False)
 
 
 def test_rows_without_tokens_do_not_limit_the_prefix():
@@ -189,6 +190,12 @@ def test_queries_of_all_sizes():
 @pytest.mark.parametrize("cu_rows", [[1, 12], [0, 11], [0, 5, 4, 12], [0, -3, 12], [0, 13, 12], [0, 4, 40]])
 def test_malformed_groups_share_nothing(cu_rows):
     check(np.random.default_rng(7), BEAMS, [1] * 12, 8, 2, 64, 32, "bf16", cu=False, cu_rows=cu_rows, status=1)
+    check(np.random.default_rng(7), BEAMS, [1] * 12, 8, 2, 64, 32, "bf16", cu=False, cu_rows=cu_rows, full=False)  # not read
+
+
+@pytest.mark.parametrize("counts", [[1] * 12, [3, 1, 7, 4, 1, 1, 9, 2, 0, 6, 1, 1]])
+def test_small_tables(counts):
+    check(np.random.default_rng(11), BEAMS, counts, 16, 2, 64, 16, "bf16", full=False)
 
 
 def test_any_groups_give_the_same():
