@@ -7,12 +7,13 @@
 // fp32, rounded once; a token that nothing applies to keeps its bits.
 //
 // HBM-bound: the logits are read and written once, mask bits and histories beside them.  Few tokens of
-// a vocabulary are touched by histories and biases, so two kinds of warps share a CTA's segment of a row:
-//   half of them copy the segment and put -inf where the mask says so (in place they read only loads of 16 bytes
-//   that the mask takes in part, and write none that it leaves alone);
-//   the others count the touched tokens in shared memory, by their place in the segment or, in long segments
-//   with short histories, in a hash table (linear probing, a third of it free), work them out from the logits as
-//   they came, and store them when the copy is done.
+// a vocabulary are touched by histories and biases: a CTA counts those of its segment of a row in shared memory,
+// by their place in the segment or, in long segments with short histories, in a hash table (linear probing, a
+// third of it free), while bulk copies bring the first chunks of the segment; touched and masked logits are
+// changed in the chunks, which leave by bulk copies.  (To fetch and store them one by one beside the copy is
+// a memory request each: 2000 of a row's 131072 made it 36 us, against 24.6 of the copy alone.)  In place, and
+// where out's 16-byte boundaries are not those of the logits, through registers: in place only loads of 16
+// bytes that the mask takes in part are read, and none written that it leaves alone.
 // Counts are whole numbers, so their order does not matter; biases of one token are added in the order of
 // the list.
 #include <cuda_bf16.h>
@@ -100,14 +101,13 @@ __device__ __forceinline__ void take_out(uint4& v, uint32_t pass) {
     }
 }
 
-constexpr int kHalf = 256, kThreads = 2 * kHalf;  // threads of a kind
+constexpr int kThreads = 512;
+constexpr int kUnitLoads = 256;                     // segments are whole multiples of as many loads of 16 bytes
 constexpr int kVecs = 4;                            // 16-byte loads of a thread under way
 constexpr int kResident = 2;                        // CTAs an SM
-constexpr uint32_t kBarTable = 1;
-
-constexpr int kRing = 3;                            // chunks of a longer segment under way
-constexpr uint32_t kBarCopy = 2;
-constexpr int64_t kWaitLimit = 1ll << 20;
+constexpr int kRing = 3, kChunkBytes = 16384;       // chunks of a segment under way
+constexpr int kMostChunks = 64;                     // of a segment
+constexpr int64_t kWaitLimit = 1ll << 14;
 
 // The tokens of a segment: [t0, t0 + reach) as far as they lie in the row.
 template <typename Raw>
@@ -128,10 +128,10 @@ __device__ __forceinline__ uint32_t allowed(const uint32_t* mask, int t, uint32_
     return __funnelshift_r(lo, hi, shift) << (from - t) & in;
 }
 
-// The copy of the tokens [at, at + kVecs * kCopy loads) of a segment, by kCopy threads; through registers.
-template <typename T, int kCopy, typename Raw>
+// The copy of the tokens [at, at + kVecs * kThreads loads) of a segment, through registers.
+template <typename T, typename Raw>
 __device__ __forceinline__ void copy_piece(const Segment<Raw>& g, int at, int end, int tid) {
-    constexpr int kEach = 16 / sizeof(Raw), kUnit = kCopy * kEach;
+    constexpr int kEach = 16 / sizeof(Raw), kUnit = kThreads * kEach;
     constexpr uint32_t kAll = (1u << kEach) - 1;
     const bool place = g.src == g.dst;
     const bool even = (((uintptr_t)g.src ^ (uintptr_t)g.dst) & 15) == 0;  // src has dst's 16-byte boundaries too
@@ -173,66 +173,11 @@ __device__ __forceinline__ void copy_piece(const Segment<Raw>& g, int at, int en
     }
 }
 
-// The copy of a segment by kCopy threads.  Longer ones come through a ring of chunks in shared memory, as many
-// bytes under way as HBM wants without a register for each.
-template <typename T, int kCopy, typename Raw>
-__device__ __forceinline__ void copy_segment(const Segment<Raw>& g, unsigned char* ring, uint64_t* s_bar, int32_t* status, int tid) {
-    constexpr int kEach = 16 / sizeof(Raw), kUnit = kCopy * kEach, kChunk = kVecs * kUnit;
+template <typename T, typename Raw>
+__device__ __forceinline__ void copy_segment(const Segment<Raw>& g, int tid) {
     if (g.src == g.dst && !g.mask) return;
     const int end = min(g.reach, g.vocab - g.t0);
-    const bool even = (((uintptr_t)g.src ^ (uintptr_t)g.dst) & 15) == 0;
-    if (!ring || g.src == g.dst || !even) {
-        for (int at = 0; at < end; at += kChunk) copy_piece<T, kCopy>(g, at, end, tid);
-        return;
-    }
-    // Whole loads of 16 bytes in the row: [first, last) of the segment; what is left has less than a load at
-    // either end.
-    const int first = g.t0 < 0 ? kEach : 0, last = end / kEach * kEach, chunks = (last - first + kChunk - 1) / kChunk;
-    if (tid < 2 * kEach) {
-        const int t = tid < kEach ? (first ? g.t0 + tid : -1) : (g.t0 + last + tid - kEach < g.t0 + end ? g.t0 + last + tid - kEach : -1);
-        if (t >= 0) g.dst[t] = allowed<1>(g.mask, t, 1u, g.vocab) ? g.src[t] : Logit<T>::rounded(-INFINITY);
-    }
-    const uint32_t ring_at = ptx::smem_u32(ring), bar = ptx::smem_u32(s_bar);
-    auto request = [&](int c) {
-        const uint32_t bytes = (uint32_t)min(kChunk, last - first - c * kChunk) * sizeof(Raw), slot = c % kRing;
-        ptx::mbar_arrive_expect_tx(bar + 8 * slot, bytes);
-        ptx::bulk_load(ring_at + slot * (kChunk * sizeof(Raw)), g.src + g.t0 + first + c * kChunk, bytes, bar + 8 * slot);
-    };
-    if (tid == 0)
-        for (int c = 0; c < min(kRing, chunks); ++c) request(c);
-    uint32_t pass[kVecs], next[kVecs];
-    auto masks = [&](int c, uint32_t (&bits)[kVecs]) {
-#pragma unroll
-        for (int k = 0; k < kVecs; ++k) {
-            const int at = first + c * kChunk + k * kUnit + tid * kEach;
-            bits[k] = at < last ? allowed<kEach>(g.mask, g.t0 + at, (1u << kEach) - 1, g.vocab) : 0u;
-        }
-    };
-    masks(0, next);
-    bool ok = true;
-    for (int c = 0; c < chunks; ++c) {
-        const uint32_t slot = c % kRing;
-#pragma unroll
-        for (int k = 0; k < kVecs; ++k) pass[k] = next[k];
-        if (c + 1 < chunks) masks(c + 1, next);
-        // (After a wait that ran out nothing more is asked for, and what follows is garbage.)
-        ok = ptx::mbar_wait_now(bar + 8 * slot, c / kRing & 1, ok ? kWaitLimit : 1024) && ok;
-        uint4 x[kVecs];
-#pragma unroll
-        for (int k = 0; k < kVecs; ++k) x[k] = reinterpret_cast<const uint4*>(ring + slot * (kChunk * sizeof(Raw)))[k * kCopy + tid];
-        if (c + kRing < chunks) {
-            ptx::named_bar_sync(kBarCopy, kCopy);  // everyone has read the slot
-            if (tid == 0 && ok) request(c + kRing);
-        }
-#pragma unroll
-        for (int k = 0; k < kVecs; ++k) {
-            const int at = first + c * kChunk + k * kUnit + tid * kEach;
-            if (at >= last) continue;
-            if (pass[k] != (1u << kEach) - 1) take_out<T>(x[k], pass[k]);
-            *reinterpret_cast<uint4*>(g.dst + g.t0 + at) = x[k];
-        }
-    }
-    if (!ok) report(status, kStatusTimeout);
+    for (int at = 0; at < end; at += kVecs * kThreads * (16 / (int)sizeof(Raw))) copy_piece<T>(g, at, end, tid);
 }
 
 // The touched tokens, in entries of shared memory: by their place in the segment (p.direct), or hashed.
@@ -242,17 +187,26 @@ struct Table {
     float* sum;       // of the biases
     int entries, shift, t0;
     bool direct;
+    int* tokens;      // touched ones of each chunk; NULL: not counted
+    int first, last, log_chunk;
+    // 0 for the tokens before the chunks, kMostChunks + 1 for those behind.
+    __device__ __forceinline__ int chunk_of(int32_t token) const {
+        const int at = token - t0;
+        return at < first ? 0 : at >= last ? kMostChunks + 1 : 1 + ((at - first) >> log_chunk);
+    }
     __device__ __forceinline__ uint32_t entry(int32_t token) const {
         if (direct) {
-            key[token - t0] = token;
+            if (tokens) {
+                if (atomicExch(key + token - t0, token) < 0) atomicAdd(tokens + chunk_of(token), 1);
+            } else {
+                key[token - t0] = token;
+            }
             return token - t0;
         }
         uint32_t at = (uint32_t)token * 0x9e3779b1u >> shift;
         for (;; at = (at + 1) & (entries - 1)) {  // (ends: a third of the entries stays free)
-            const int32_t k = key[at];
-            if (k == token) return at;
-            if (k >= 0) continue;
             const int32_t old = atomicCAS(key + at, -1, token);
+            if (old < 0 && tokens) atomicAdd(tokens + chunk_of(token), 1);
             if (old < 0 || old == token) return at;
         }
     }
@@ -268,7 +222,6 @@ struct Touches {
     int32_t bias_token;
     float bias_value;
     Penalties rules;
-    template <int kCount>
     __device__ __forceinline__ void read(const LogitsParams& p, int64_t row, int tid) {
         len = p.width > 0 && p.lens ? p.lens[row] : p.width;
         prompt = p.width > 0 && p.prompt_lens ? p.prompt_lens[row] : 0;
@@ -280,37 +233,28 @@ struct Touches {
         edge[1] = tail < p.width ? __ldg(history + tail) : -1;
 #pragma unroll
         for (int k = 0; k < kKept; ++k)
-            quad[k] = k * kCount + tid < quads ? __ldg(reinterpret_cast<const int4*>(history + head) + k * kCount + tid) : make_int4(-1, -1, -1, -1);
+            quad[k] = k * kThreads + tid < quads ? __ldg(reinterpret_cast<const int4*>(history + head) + k * kThreads + tid) : make_int4(-1, -1, -1, -1);
         bias_token = tid < p.num_bias ? p.bias_tokens[row * p.num_bias + tid] : -1;
         bias_value = tid < p.num_bias ? p.bias[row * p.num_bias + tid] : 0.f;
         rules = Penalties{p.repetition ? p.repetition[row] : 1.f, p.presence ? p.presence[row] : 0.f, p.frequency ? p.frequency[row] : 0.f};
     }
 };
 
-// Counts them and works them out, by kCount threads.
-template <typename T, int kCount, typename Raw>
-__device__ __forceinline__ void touch_segment(const LogitsParams& p, const Segment<Raw>& g, const Table& table, Touches& own, int64_t row, int tid) {
-    using L = Logit<T>;
-    __shared__ int32_t s_token[kCount];
-    __shared__ float s_value[kCount];
-    __shared__ int s_counts[kCount / 32];
-    const int lane = tid & 31, warp = tid >> 5;
-    auto sync = [] { ptx::named_bar_sync(kBarTable, kCount); };
+// Counts them and adds up their biases; returns the row's rules.
+template <typename Raw>
+__device__ __forceinline__ Penalties count_touched(const LogitsParams& p, const Segment<Raw>& g, const Table& table, Touches& own, int64_t row, int tid) {
+    __shared__ int32_t s_token[kThreads];
+    __shared__ float s_value[kThreads];
     bool bad = false;
     auto ours = [&](int32_t token) {
         bad |= token >= p.vocab;
         return token >= max(g.t0, 0) && token < p.vocab && token - g.t0 < g.reach;
     };
-    // The few logits of a hash table are asked for right away.
-    auto entry = [&](int32_t token) {
-        if (!table.direct) asm volatile("prefetch.global.L2 [%0];" ::"l"(g.src + token));
-        return table.entry(token);
-    };
     if ((own.len < 0 || own.len > p.width) && tid == 0) report(p.status, kStatusBadIndex);
     const int len = max(0, min(own.len, p.width)), prompt = max(0, min(own.prompt, len));
     auto count = [&](int32_t token, int i) {
         if (i >= len || !ours(token)) return;
-        uint32_t* word = table.word + entry(token);
+        uint32_t* word = table.word + table.entry(token);
         if (i < prompt) atomicOr(word, kPrompt);
         else atomicAdd(word, 1u);
     };
@@ -325,21 +269,20 @@ __device__ __forceinline__ void touch_segment(const LogitsParams& p, const Segme
         count(own.edge[0], tid);
         count(own.edge[1], own.head + 4 * quads + tid);
 #pragma unroll
-        for (int k = 0; k < Touches::kKept; ++k) count4(own.quad[k], own.head + 4 * (k * kCount + tid));
-        constexpr int kAhead = 4;
+        for (int k = 0; k < Touches::kKept; ++k) count4(own.quad[k], own.head + 4 * (k * kThreads + tid));
+        constexpr int kQuads = 4;
         const int used = min(quads, (len - own.head + 3) / 4);
-        for (int i0 = Touches::kKept * kCount + tid; i0 < used; i0 += kAhead * kCount) {
-            int4 q[kAhead];
+        for (int i0 = Touches::kKept * kThreads + tid; i0 < used; i0 += kQuads * kThreads) {
+            int4 q[kQuads];
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k)
-                q[k] = i0 + k * kCount < used ? __ldg(reinterpret_cast<const int4*>(own.history + own.head) + i0 + k * kCount) : make_int4(-1, -1, -1, -1);
+            for (int k = 0; k < kQuads; ++k)
+                q[k] = i0 + k * kThreads < used ? __ldg(reinterpret_cast<const int4*>(own.history + own.head) + i0 + k * kThreads) : make_int4(-1, -1, -1, -1);
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) count4(q[k], own.head + 4 * (i0 + k * kCount));
+            for (int k = 0; k < kQuads; ++k) count4(q[k], own.head + 4 * (i0 + k * kThreads));
         }
     }
-    // Biases, as many at a time as there are threads: those of this segment side by side, in order; the first of
-    // each token adds up all of them.
-    for (int i0 = 0; i0 < p.num_bias; i0 += kCount) {
+    // Biases, as many at a time as there are threads.
+    for (int i0 = 0; i0 < p.num_bias; i0 += kThreads) {
         int32_t token = own.bias_token;
         float value = own.bias_value;
         if (i0 > 0) {
@@ -347,34 +290,23 @@ __device__ __forceinline__ void touch_segment(const LogitsParams& p, const Segme
             value = i0 + tid < p.num_bias ? p.bias[row * p.num_bias + i0 + tid] : 0.f;
         }
         const bool mine = ours(token);
-        const uint32_t some = __ballot_sync(0xffffffffu, mine);
-        if (i0 > 0) sync();  // (the round before is over)
-        if (lane == 0) s_counts[warp] = __popc(some);
-        sync();
-        int slot = __popc(some & ((1u << lane) - 1)), n = 0;
-#pragma unroll
-        for (int w = 0; w < kCount / 32; ++w) {
-            if (w < warp) slot += s_counts[w];
-            n += s_counts[w];
-        }
-        if (mine) {
-            s_token[slot] = token;
-            s_value[slot] = value;
-        }
-        sync();
-        if (tid < n) {
-            const int32_t t = s_token[tid];
-            bool leads = true;  // the first with this token
-#pragma unroll 8
-            for (int i = 0; i < tid; ++i) leads &= s_token[i] != t;
+        const uint32_t at = mine ? table.entry(token) : 0;
+        const bool again = mine && atomicOr(table.word + at, kBiased) & kBiased;
+        if (!__syncthreads_or(again)) {
+            if (mine) table.sum[at] = value;
+        } else {  // a token several times: its first thread adds up all of them, in order
+            s_token[tid] = mine ? token : -1;
+            s_value[tid] = value;
+            __syncthreads();
+            bool leads = mine;
+            for (int i = 0; i < tid && leads; ++i) leads = s_token[i] != token;
             if (leads) {
-                const uint32_t at = entry(t);
-                float sum = table.word[at] & kBiased ? table.sum[at] + s_value[tid] : s_value[tid];
-#pragma unroll 8
-                for (int i = tid + 1; i < n; ++i) sum = s_token[i] == t ? sum + s_value[i] : sum;
+                float sum = table.sum[at];
+                for (int i = tid; i < kThreads; ++i)
+                    if (s_token[i] == token) sum += s_value[i];
                 table.sum[at] = sum;
-                atomicOr(table.word + at, kBiased);
             }
+            __syncthreads();
         }
     }
     if (bad) report(p.status, kStatusBadIndex);
@@ -383,16 +315,23 @@ __device__ __forceinline__ void touch_segment(const LogitsParams& p, const Segme
         if (tid == 0) report(p.status, kStatusBadIndex);
         rules = Penalties{1.f, 0.f, 0.f};
     }
-    sync();
+    __syncthreads();
+    return rules;
+}
+
+// The touched logits, out of memory and into it.
+template <typename T, typename Raw>
+__device__ __forceinline__ void change_in_memory(const Segment<Raw>& g, const Table& table, const Penalties& rules, int tid) {
+    using L = Logit<T>;
     // The touched logits, which take their words' place; those that the mask takes are left out.
     constexpr int kTouched = 8;
-    for (int i0 = tid; i0 < table.entries; i0 += kTouched * kCount) {
+    for (int i0 = tid; i0 < table.entries; i0 += kTouched * kThreads) {
         int32_t token[kTouched];
         Raw y[kTouched];
         uint32_t bits[kTouched];
 #pragma unroll
         for (int k = 0; k < kTouched; ++k) {
-            const int i = i0 + k * kCount;
+            const int i = i0 + k * kThreads;
             token[k] = i < table.entries ? table.key[i] : -1;
             bits[k] = ~0u;
             if (token[k] < 0) continue;
@@ -401,7 +340,7 @@ __device__ __forceinline__ void touch_segment(const LogitsParams& p, const Segme
         }
 #pragma unroll
         for (int k = 0; k < kTouched; ++k) {
-            const int i = i0 + k * kCount;
+            const int i = i0 + k * kThreads;
             if (token[k] < 0) continue;
             const uint32_t word = table.word[i];
             if (bits[k] >> (token[k] & 31) & 1) table.word[i] = L::rounded(rules.apply(L::value(y[k]), word, word & kBiased ? table.sum[i] : 0.f));
@@ -410,23 +349,175 @@ __device__ __forceinline__ void touch_segment(const LogitsParams& p, const Segme
     }
 }
 
-// kTouches 1: each half of the threads has its kind of work; 2 (segments of few loads): all do the one, then the
-// other.
-template <typename T, int kTouches>
+// A segment through the ring: touched tokens and then the mask's are changed in its chunks.
+template <typename T, bool kTouched, typename Raw>
+__device__ __forceinline__ void through_ring(const LogitsParams& p, const Segment<Raw>& g, Table table, uint16_t* list, unsigned char* ring, uint64_t* s_bar, int64_t row, int tid) {
+    using L = Logit<T>;
+    constexpr int kEach = 16 / sizeof(Raw), kChunk = kChunkBytes / sizeof(Raw), kUnit = kThreads * kEach, kLoads = kChunk / kUnit;
+    constexpr uint32_t kAll = (1u << kEach) - 1;
+    // Whole loads of 16 bytes in the row: [first, last) of the segment; what is left has less than a load at
+    // either end.
+    const int end = min(g.reach, g.vocab - g.t0), first = g.t0 < 0 ? kEach : 0, last = max(first, end / kEach * kEach);
+    const int chunks = (last - first + kChunk - 1) / kChunk;
+    const uint32_t ring_at = ptx::smem_u32(ring), bar = ptx::smem_u32(s_bar);
+    auto bytes_of = [&](int c) { return (uint32_t)min(kChunk, last - first - c * kChunk) * (uint32_t)sizeof(Raw); };
+    auto request = [&](int c) {
+        const uint32_t slot = c % kRing;
+        ptx::mbar_arrive_expect_tx(bar + 8 * slot, bytes_of(c));
+        ptx::bulk_load(ring_at + slot * kChunkBytes, g.src + g.t0 + first + c * kChunk, bytes_of(c), bar + 8 * slot);
+    };
+    if (tid == 0)
+        for (int c = 0; c < min(kRing, chunks); ++c) request(c);
+    // In segments of several chunks each has a list of its touched tokens' entries, behind one another.
+    __shared__ int s_tokens[kMostChunks + 2], s_begin[kMostChunks + 3];
+    const bool lists = kTouched && chunks > 1;
+    Touches own;
+    if constexpr (kTouched) {
+        own.read(p, row, tid);
+        table.first = first;
+        table.last = last;
+        table.log_chunk = 31 - __clz(kChunk);
+        table.tokens = lists ? s_tokens : nullptr;
+        if (lists && tid < kMostChunks + 2) s_tokens[tid] = 0;
+    }
+    const int edge = tid < kEach ? tid : last + tid - kEach;  // of the tokens outside of whole loads
+    if (tid < 2 * kEach && (tid < kEach ? first > 0 : true) && g.t0 + edge >= 0 && edge < end)
+        g.dst[g.t0 + edge] = allowed<1>(g.mask, g.t0 + edge, 1u, g.vocab) ? g.src[g.t0 + edge] : L::rounded(-INFINITY);
+    uint32_t even[kLoads], odd[kLoads];  // mask bits of chunks, asked for two chunks ahead
+    auto masks = [&](int c, uint32_t (&bits)[kLoads]) {
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) {
+            const int at = first + c * kChunk + k * kUnit + tid * kEach;
+            bits[k] = at < last ? allowed<kEach>(g.mask, g.t0 + at, kAll, g.vocab) : kAll;
+        }
+    };
+    if (g.mask) masks(0, even), masks(1, odd);
+    __syncthreads();
+    Penalties rules;
+    if constexpr (kTouched) rules = count_touched(p, g, table, own, row, tid);
+    else if (!g.mask && tid) return;  // (nothing to change)
+    // body(entry) for all touched tokens.
+    auto each_touched = [&](auto&& body) {
+        for (int i = 4 * tid; i < p.entries; i += 4 * kThreads) {
+            const int4 keys = *reinterpret_cast<const int4*>(table.key + i);
+            if (keys.x >= 0) body(keys.x, i);
+            if (keys.y >= 0) body(keys.y, i + 1);
+            if (keys.z >= 0) body(keys.z, i + 2);
+            if (keys.w >= 0) body(keys.w, i + 3);
+        }
+    };
+    if (lists) {
+        if (tid < 32) {
+            constexpr int kMine = (kMostChunks + 2 + 31) / 32;
+            int n[kMine], sum = 0;
+#pragma unroll
+            for (int k = 0; k < kMine; ++k) sum += n[k] = kMine * tid + k < kMostChunks + 2 ? s_tokens[kMine * tid + k] : 0;
+            int at = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, at, o);
+                if (tid >= o) at += u;
+            }
+            at -= sum;
+#pragma unroll
+            for (int k = 0; k < kMine; ++k) {
+                if (kMine * tid + k < kMostChunks + 3) s_begin[kMine * tid + k] = at;
+                if (kMine * tid + k < kMostChunks + 2) s_tokens[kMine * tid + k] = at;
+                at += n[k];
+            }
+        }
+        __syncthreads();
+        each_touched([&](int32_t token, int i) { list[atomicAdd(s_tokens + table.chunk_of(token), 1)] = (uint16_t)i; });
+        __syncthreads();
+    }
+    auto changed = [&](Raw x, int at) {
+        const uint32_t word = table.word[at];
+        return L::rounded(rules.apply(L::value(x), word, word & kBiased ? table.sum[at] : 0.f));
+    };
+    bool ok = true;
+    auto step = [&](int c, uint32_t (&bits)[kLoads]) {
+        const uint32_t slot = c % kRing;
+        unsigned char* chunk = ring + slot * kChunkBytes;
+        // (After a wait that ran out nothing more is asked for, and what follows is garbage.)
+        ok = ptx::mbar_wait(bar + 8 * slot, c / kRing & 1, ok ? kWaitLimit : 1) && ok;
+        if constexpr (kTouched) {
+            const int from = g.t0 + first + c * kChunk;
+            auto change = [&](int32_t token, int at) {
+                Raw* x = reinterpret_cast<Raw*>(chunk) + (token - from);
+                *x = changed(*x, at);
+            };
+            if (lists) {
+                for (int i = s_begin[c + 1] + tid; i < s_begin[c + 2]; i += kThreads) change(table.key[list[i]], list[i]);
+            } else {
+                each_touched([&](int32_t token, int at) {
+                    if (token - g.t0 >= first && token - g.t0 < last) change(token, at);
+                });
+            }
+            if (g.mask) __syncthreads();
+        }
+        if (g.mask) {
+#pragma unroll
+            for (int k = 0; k < kLoads; ++k) {
+                if (bits[k] == kAll) continue;
+                uint4* at = reinterpret_cast<uint4*>(chunk) + k * kThreads + tid;
+                uint4 x = *at;
+                take_out<T>(x, bits[k]);
+                *at = x;
+            }
+            masks(c + 2, bits);
+        }
+        if (kTouched || g.mask) {
+            ptx::fence_proxy_async_smem();
+            __syncthreads();
+        }
+        if (tid == 0 && ok) {
+            ptx::bulk_store(g.dst + g.t0 + first + c * kChunk, ring_at + slot * kChunkBytes, bytes_of(c));
+            ptx::bulk_commit();
+            if (c > 0 && c - 1 + kRing < chunks) {
+                ptx::bulk_wait_read<1>();  // the chunk before has left its slot
+                request(c - 1 + kRing);
+            }
+        }
+    };
+    for (int c = 0; c < chunks; c += 2) {
+        step(c, even);
+        if (c + 1 < chunks) step(c + 1, odd);
+    }
+    if constexpr (kTouched) {
+        auto at_edge = [&](int32_t token, int at) {
+            if (allowed<1>(g.mask, token, 1u, g.vocab)) g.dst[token] = changed(g.src[token], at);
+        };
+        if (lists) {
+            if (first > 0)
+                for (int i = tid; i < s_begin[1]; i += kThreads) at_edge(table.key[list[i]], list[i]);
+            if (last < end)
+                for (int i = s_begin[kMostChunks + 1] + tid; i < s_begin[kMostChunks + 2]; i += kThreads) at_edge(table.key[list[i]], list[i]);
+        } else if (first > 0 || last < end) {
+            each_touched([&](int32_t token, int at) {
+                if (token - g.t0 < first || token - g.t0 >= last) at_edge(token, at);
+            });
+        }
+    }
+    if (tid == 0) ptx::bulk_wait_read0();
+    if (!ok) report(p.status, kStatusTimeout);
+}
+
+template <typename T, bool kThroughRing, bool kTouched>
 __global__ void __launch_bounds__(kThreads, kResident) penalize_kernel(const __grid_constant__ LogitsParams p) {
     using Raw = typename Logit<T>::Raw;
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ __align__(8) uint64_t s_bar[kRing];
     const int tid = threadIdx.x;
-    const size_t table_bytes = (size_t)p.entries * (p.num_bias > 0 ? 12 : 8);
+    const size_t table_bytes = (size_t)p.entries * (p.num_bias > 0 ? 12 : 8), list_bytes = (size_t)p.entries * 2;
     Table table{reinterpret_cast<int32_t*>(smem), reinterpret_cast<uint32_t*>(smem) + p.entries, reinterpret_cast<float*>(smem) + 2 * p.entries,
-                p.entries, p.shift, 0, p.direct};
-    if (kTouches)
+                p.entries, p.shift, 0, p.direct, nullptr, 0, 0, 0};
+    if (kTouched)
         for (int i = tid; i < p.entries / 4; i += kThreads) {
             reinterpret_cast<int4*>(table.key)[i] = make_int4(-1, -1, -1, -1);
             reinterpret_cast<uint4*>(table.word)[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (p.num_bias > 0) reinterpret_cast<float4*>(table.sum)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
-    if (tid == 0) {
+    if (kThroughRing && tid == 0) {
         for (int i = 0; i < kRing; ++i) ptx::mbar_init(ptx::smem_u32(s_bar + i), 1);
         ptx::fence_mbar_init();
     }
@@ -442,26 +533,25 @@ __global__ void __launch_bounds__(kThreads, kResident) penalize_kernel(const __g
     g.t0 = (int)(blockIdx.x % p.segs) * p.seg_len - (int)(((uintptr_t)g.dst & 15) / sizeof(Raw));
     if (g.t0 >= p.vocab) return;
     table.t0 = g.t0;
-    unsigned char* ring = p.ring ? smem + table_bytes : nullptr;
-    Touches own;
-    if (kTouches == 2 || (kTouches == 1 && tid < kHalf)) own.read<kTouches == 1 ? kHalf : kThreads>(p, row, tid);
-    __syncthreads();
-    if constexpr (kTouches != 1) copy_segment<T, kThreads>(g, ring, s_bar, p.status, tid);
-    if constexpr (kTouches == 1) {
-        if (tid >= kHalf) copy_segment<T, kHalf>(g, ring, s_bar, p.status, tid - kHalf);
-        else touch_segment<T, kHalf>(p, g, table, own, row, tid);
-    } else if constexpr (kTouches == 2) {
-        touch_segment<T, kThreads>(p, g, table, own, row, tid);
-    }
-    if constexpr (kTouches != 0) {
-        __syncthreads();
-        for (int i = 4 * tid; i < p.entries; i += 4 * kThreads) {
-            const int4 keys = *reinterpret_cast<const int4*>(table.key + i);
-            const uint4 words = *reinterpret_cast<const uint4*>(table.word + i);
-            if (keys.x >= 0) g.dst[keys.x] = (Raw)words.x;
-            if (keys.y >= 0) g.dst[keys.y] = (Raw)words.y;
-            if (keys.z >= 0) g.dst[keys.z] = (Raw)words.z;
-            if (keys.w >= 0) g.dst[keys.w] = (Raw)words.w;
+    if constexpr (kThroughRing) {
+        through_ring<T, kTouched>(p, g, table, reinterpret_cast<uint16_t*>(smem + table_bytes), smem + table_bytes + list_bytes, s_bar, row, tid);
+    } else {
+        Touches own;
+        if constexpr (kTouched) own.read(p, row, tid);
+        copy_segment<T>(g, tid);
+        if constexpr (kTouched) {
+            __syncthreads();
+            const Penalties rules = count_touched(p, g, table, own, row, tid);
+            change_in_memory<T>(g, table, rules, tid);
+            __syncthreads();
+            for (int i = 4 * tid; i < p.entries; i += 4 * kThreads) {
+                const int4 keys = *reinterpret_cast<const int4*>(table.key + i);
+                const uint4 words = *reinterpret_cast<const uint4*>(table.word + i);
+                if (keys.x >= 0) g.dst[keys.x] = (Raw)words.x;
+                if (keys.y >= 0) g.dst[keys.y] = (Raw)words.y;
+                if (keys.z >= 0) g.dst[keys.z] = (Raw)words.z;
+                if (keys.w >= 0) g.dst[keys.w] = (Raw)words.w;
+            }
         }
     }
 }
@@ -473,7 +563,7 @@ cudaError_t launch_type(LogitsParams& p, cudaStream_t stream) {
     const int64_t touches = (int64_t)p.width + p.num_bias;
     const bool place = p.out == p.logits;
     if (place && !p.mask && touches == 0) return cudaSuccess;
-    const int each = 16 / sizeof(T), unit = kHalf * each;
+    const int each = 16 / sizeof(T), unit = kUnitLoads * each;
     const bool even = ((uintptr_t)p.out & 15) == 0 && (p.out_stride * sizeof(T) & 15) == 0;
     // Segments of whole units, as few as fill the CTAs' places well; in place, where it is the chain of loads that
     // counts, of a chunk.
@@ -486,6 +576,7 @@ cudaError_t launch_type(LogitsParams& p, cudaStream_t stream) {
     }
     int64_t len = (units + segs - 1) / segs * unit;
     if (place && !touches && len > 2 * kVecs * unit) len = 2 * kVecs * unit;
+    if (len > kMostChunks * (kChunkBytes / (int)sizeof(T))) len = kMostChunks * (kChunkBytes / (int)sizeof(T));
     // A table holds the most tokens that a segment can have touched: hashed with a third of it free.
     const bool hashed = 3 * touches <= 2 * kMostEntries;
     if (!hashed && len > kMostEntries) len = kMostEntries;
@@ -499,11 +590,12 @@ cudaError_t launch_type(LogitsParams& p, cudaStream_t stream) {
         p.direct = !hashed || len <= (int64_t)1 << log;
         p.entries = p.direct ? (int32_t)len : 1 << log;
     }
-    // With touched tokens, halves of the threads where the copy is long enough to hide the other half's work.
-    const int chunk = kVecs * unit * (touches ? 1 : 2);
-    p.ring = !place && len > chunk;
-    const auto kernel = !touches ? penalize_kernel<T, 0> : p.ring ? penalize_kernel<T, 1> : penalize_kernel<T, 2>;
-    const size_t smem = (size_t)p.entries * (p.num_bias > 0 ? 12 : 8) + (p.ring ? (size_t)kRing * chunk * sizeof(T) : 0);
+    // Rows of out have the boundaries of the logits' rows.
+    const bool ring = !place && (((uintptr_t)p.out ^ (uintptr_t)p.logits) & 15) == 0 && (p.rows == 1 || ((p.out_stride ^ p.stride) * sizeof(T) & 15) == 0);
+    const auto kernel = ring ? (touches ? penalize_kernel<T, true, true> : penalize_kernel<T, true, false>)
+                             : (touches ? penalize_kernel<T, false, true> : penalize_kernel<T, false, false>);
+    const int64_t chunks = (len * (int64_t)sizeof(T) + kChunkBytes - 1) / kChunkBytes;
+    const size_t smem = (size_t)p.entries * (p.num_bias > 0 ? 12 : 8) + (ring ? (size_t)p.entries * 2 + (size_t)(chunks < kRing ? chunks : kRing) * kChunkBytes : 0);
     if (smem > 40 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;

@@ -238,7 +238,6 @@ struct LogitsParams {
     int32_t segs, seg_len;    // segments of a row, their tokens
     int32_t entries, shift;   // of the table of a segment's touched tokens: 2^(32 - shift), or
     bool direct;              // one for each token
-    bool ring;                // segments come through shared memory
 };
 cudaError_t launch_penalize(LogitsParams p, int dtype, cudaStream_t stream);
 
