@@ -25,10 +25,11 @@ def reference(x, rules):
             g = [float(rules[k][r]) if k in rules else d for k, d in (("repetition", 1.0), ("presence", 0.0), ("frequency", 0.0))]
             if not (np.isfinite(g).all() and g[0] > 0):
                 g = [1.0, 0.0, 0.0]
+            behind = np.bincount([t for t in h[p:n].tolist() if 0 <= t < vocab], minlength=vocab)
             for t in set(h[:n].tolist()):
                 if not 0 <= t < vocab:
                     continue
-                c = int((h[p:n] == t).sum())
+                c = int(behind[t])
                 y[r, t] = y[r, t] / g[0] if y[r, t] > 0 else y[r, t] * g[0]
                 size[r, t] += abs(y[r, t]) + abs(g[2] * c) + abs(g[1])
                 y[r, t] -= (g[2] * c + g[1]) if c else 0.0
@@ -118,6 +119,33 @@ def test_large(rows, vocab):
     made = make(rng, rows, vocab, width=300, biases=20, mask=0.9)
     x = torch.as_tensor(rng.standard_normal((rows, vocab)).astype(np.float32) * 5).to(torch.bfloat16)
     check(call(x.cuda(), made), x, made, "bf16", adds=20)
+
+
+# Rows enough that a row is one segment, of several chunks: with edges outside of 16-byte loads, and all touched tokens
+# in one chunk.
+@pytest.mark.parametrize("dtype,vocab", [("bf16", 25003), ("fp16", 8201), ("fp32", 8193)])
+@pytest.mark.parametrize("pad,skip", [(0, 0), (1, 1), (24, 3)])
+@pytest.mark.parametrize("rules", [dict(width=300, biases=20, mask=0.9), dict(width=64, biases=600), dict(mask=0.3), dict(width=7000, lens=False)])
+def test_segments_of_several_chunks(dtype, vocab, pad, skip, rules):
+    rng = np.random.default_rng(vocab + pad)
+    rows = 300
+    made = make(rng, rows, vocab, **rules)
+    if rules.get("biases") == 600:
+        made["history"] = np.where(made["history"] >= 0, 8192 - made["history"] % 90, -1)
+        made["bias_tokens"] %= 100
+    whole = torch.as_tensor(rng.standard_normal((rows, vocab + pad)).astype(np.float32) * 5).to(DT[dtype])
+    x = whole[:, skip: skip + vocab]
+    target = torch.zeros(rows, vocab + pad, device="cuda", dtype=DT[dtype])
+    call(whole.cuda()[:, skip: skip + vocab], made, out=target[:, skip: skip + vocab])
+    check(target[:, skip: skip + vocab], x, made, dtype, adds=rules.get("biases", 0))
+    assert (target[:, :skip] == 0).all() and (target[:, skip + vocab:] == 0).all()
+
+
+def test_vocabularies_past_a_segments_chunks():
+    rng = np.random.default_rng(4)
+    made = make(rng, 300, 600_001, width=50, biases=3, mask=0.9)
+    x = torch.randn(300, 600_001, device="cuda").to(torch.bfloat16)
+    assert torch.equal(call(x, made), call(x.clone(), made, out=x))
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "fp16"])
