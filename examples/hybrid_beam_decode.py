@@ -2,10 +2,13 @@
 
 Shows the serving calls together, as a server uses them: the prompts go through the KDA prefill
 and into the 8-bit key/value cache; every step then runs the recurrent KDA step on a pool of
-states, appends to and attends over the paged cache, selects beams, and reorders both kinds of
-pages by the selection; finished requests give their pages back and the pools are compacted.
+states, appends to and attends over the paged cache (what the beams of a request share is gone
+through once), selects beams, and reorders both kinds of pages by the selection; finished requests give their pages back and the pools are compacted.
 
-    python examples/hybrid_beam_decode.py [--requests 3] [--beams 4] [--steps 12]
+    python examples/hybrid_beam_decode.py [--requests 3] [--beams 4] [--steps 12] [--rotary] [--repetition 1.2]
+
+--rotary turns queries and keys of the attention by their positions as they are appended;
+--repetition penalises the logits of tokens that a beam already has.
 
 Needs a GB300 (there is no CPU path).  Weights are random: the tokens mean nothing, but
 every run prints the same ones.
@@ -65,8 +68,11 @@ class Model:
 class Server:
     """The model with pools of states and of cache pages for rows = requests x beams."""
 
-    def __init__(self, model, requests, beams, max_tokens, page=16, device="cuda"):
+    def __init__(self, model, requests, beams, max_tokens, page=16, device="cuda", rotary=False):
         self.m, self.requests, self.beams, self.page = model, requests, beams, page
+        angle = torch.arange(max_tokens, device=device)[:, None] * 10000.0 ** (-torch.arange(0, D, 2, device=device) / D)
+        self.rotary = torch.cat([angle.cos(), angle.sin()], 1) if rotary else None
+        self.groups = torch.arange(requests + 1, dtype=torch.int32, device=device) * beams
         rows = requests * beams
         kda, full = (sum(k == kind for k in model.layers) for kind in ("kda", "full"))
         width = -(-max_tokens // page)
@@ -88,6 +94,13 @@ class Server:
         for i, kind in enumerate(self.m.layers):
             yield i, kind, seen[kind]
             seen[kind] += 1
+
+    def append(self, q, k, v, layer, cu=None):
+        """Appends k and v to a layer's cache; returns the queries to attend with."""
+        if self.rotary is not None:
+            return K.kda_kvcache_append_rotary(q, k, v, self.rotary, *self.cache(layer), self.table, self.lens, cu_tokens=cu)
+        K.kda_kvcache_append(k, v, *self.cache(layer), self.table, self.lens, cu_tokens=cu)
+        return q
 
     def prefill(self, prompts):
         """Runs the prompts as the first beam of each request; returns the last tokens' hidden."""
@@ -112,7 +125,7 @@ class Server:
                 o, final = K.kda_prefill(q, k, v, g, beta, cu_seqlens=cu_req, output_final_state=True)
                 self.states[j][at] = final
             else:
-                K.kda_kvcache_append(k, v, *self.cache(j), self.table, self.lens, cu_tokens=cu)
+                q = self.append(q, k, v, j, cu)
                 o = K.kda_kvcache_attention(q, *self.cache(j), self.table, self.lens + want, cu_tokens=cu)
             x = self.m.mix(i, x, o)
         self.lens = self.lens + want
@@ -135,12 +148,12 @@ class Server:
                 g, beta = self.m.gates(i, x)
                 o = K.kda_decode_paged(q, k, v, g, beta, self.states[j], state_pages)
             elif all_live:
-                K.kda_kvcache_append(k, v, *self.cache(j), self.table, self.lens)
-                o = K.kda_kvcache_attention(q, *self.cache(j), self.table, after)
+                q = self.append(q, k, v, j)
+                o = K.kda_kvcache_attention_shared(q, *self.cache(j), self.table, after, self.groups)
             else:  # only the rows that have a token
                 o = torch.zeros_like(q)
-                K.kda_kvcache_append(k[live], v[live], *self.cache(j), self.table, self.lens, cu_tokens=cu)
-                o[live] = K.kda_kvcache_attention(q[live], *self.cache(j), self.table, after, cu_tokens=cu)
+                o[live] = K.kda_kvcache_attention_shared(self.append(q[live], k[live], v[live], j, cu), *self.cache(j), self.table, after,
+                                                         self.groups, cu_tokens=cu)
             x = self.m.mix(i, x, o)
         self.lens = after
         return x
@@ -164,12 +177,12 @@ class Server:
         return live, states
 
 
-def decode(requests=3, beams=4, steps=12, eos=1, seed=0):
+def decode(requests=3, beams=4, steps=12, eos=1, seed=0, rotary=False, repetition=1.0):
     """Beam search over random prompts; returns [(score, tokens)] for each request, best first."""
     g = torch.Generator().manual_seed(seed)
     prompts = [torch.randint(2, 900, (int(n),), generator=g) for n in torch.randint(5, 60, (requests,), generator=g)]
     model = Model()
-    server = Server(model, requests, beams, max_tokens=60 + steps + 1)
+    server = Server(model, requests, beams, max_tokens=60 + steps + 1, rotary=rotary)
     rows = requests * beams
     hidden = server.prefill(prompts)
     # The first selection: one beam of each request is there, the others score -inf.
@@ -179,7 +192,10 @@ def decode(requests=3, beams=4, steps=12, eos=1, seed=0):
     scores[:, 0] = 0
     done = torch.zeros(requests, beams, dtype=torch.bool, device="cuda")
     history = torch.zeros(rows, 0, dtype=torch.int32, device="cuda")
+    penalty = torch.full((rows,), repetition, device="cuda")
     for _ in range(steps):
+        if repetition != 1.0 and history.shape[1] > 0:
+            K.kda_logits_penalize(logits, history=history, repetition=penalty, out=logits)
         scores, tokens, parents, done = K.kda_beam_select(logits, scores, done=done, eos=eos)
         parents, tokens = parents.view(rows), tokens.view(rows)
         server.reorder(parents)
@@ -200,8 +216,10 @@ def main():
     ap.add_argument("--requests", type=int, default=3)
     ap.add_argument("--beams", type=int, default=4)
     ap.add_argument("--steps", type=int, default=12)
+    ap.add_argument("--rotary", action="store_true")
+    ap.add_argument("--repetition", type=float, default=1.0)
     a = ap.parse_args()
-    answers, server = decode(a.requests, a.beams, a.steps)
+    answers, server = decode(a.requests, a.beams, a.steps, rotary=a.rotary, repetition=a.repetition)
     for r, beams in enumerate(answers):
         print(f"request {r}")
         for score, tokens in beams:
