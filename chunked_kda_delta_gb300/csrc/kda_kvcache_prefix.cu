@@ -244,17 +244,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
 #pragma unroll
                     for (int k = 0; k < kQ; ++k) to[k] = some ? __ldg(src + 4 * k) : make_uint4(0u, 0u, 0u, 0u);
                 };
-                uint4 r[kQ], next[kQ];
-                read(0, r);
+                // (All of them at once: each chain of loads is 2000 cycles and more here.)
+                uint4 r[4][kQ];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) read(x, r[x]);
                 unsigned char* dst = q_sm + grp * kQBytes<kDim> + 4 * (warp % 4) * kSbo + lane % 8 * 16 + lane / 8 * kLbo;
                 // (Loops that run once or a few times are not unrolled: their instructions come from memory.)
 #pragma unroll 1
                 for (int x = 0; x < 4; ++x) {
-                    if (x < 3) read(x + 1, next);
                     float a = 0.f;
 #pragma unroll
                     for (int k = 0; k < kQ; ++k) {
-                        const uint32_t u[4] = {r[k].x, r[k].y, r[k].z, r[k].w};
+                        const uint32_t u[4] = {r[0][k].x, r[0][k].y, r[0][k].z, r[0][k].w};
 #pragma unroll
                         for (int y = 0; y < 4; ++y) {
                             const float2 v = Act<T>::two(u[y]);
@@ -268,14 +269,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                     const float up = copysignf(exp2f((float)(14 - e)), p.scale);
 #pragma unroll
                     for (int k = 0; k < kQ; ++k) {
-                        uint32_t u[4] = {r[k].x, r[k].y, r[k].z, r[k].w};
+                        uint32_t u[4] = {r[0][k].x, r[0][k].y, r[0][k].z, r[0][k].w};
 #pragma unroll
                         for (int y = 0; y < 4; ++y) {
                             const float2 v = Act<T>::two(u[y]);
                             u[y] = pack_half2(v.x * up, v.y * up);
                         }
                         *reinterpret_cast<uint4*>(dst + x * kSbo + 4 * k * kLbo) = make_uint4(u[0], u[1], u[2], u[3]);
-                        r[k] = next[k];
+                        r[0][k] = r[1][k], r[1][k] = r[2][k], r[2][k] = r[3][k];
                     }
                     const float mine = __shfl_sync(0xffffffffu, exp2f((float)(e - 14)) * fabsf(p.scale), lane % 8);
                     if (lane / 8 == x) factor = mine;
@@ -448,11 +449,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                         for (int k = 0; k < 32; ++k) s_o[(q + k) * kLanes + at] = n > 0 ? __uint_as_float(o[k]) * scale : 0.f;
                     }
                     named_bar_sync(kBarSoft, kLanes);
-#pragma unroll 1
+                    constexpr int kMost = 8;  // copies of 32 rows
+#pragma unroll 2
                     for (int k = first_ch; k < kPass; k += copies) {
-                        float sum = s_o[k * kLanes + mine] + s_o[k * kLanes + mine + spread];
-                        for (int x = 2; x < copies; x += 2) sum += s_o[k * kLanes + mine + (x << log_spread)] + s_o[k * kLanes + mine + ((x + 1) << log_spread)];
-                        part_o[(pass + k) * kLanes + mine] = sum;
+                        float o[kMost];
+#pragma unroll
+                        for (int x = 0; x < kMost; ++x) o[x] = x < copies ? s_o[k * kLanes + mine + (x << log_spread)] : 0.f;
+                        part_o[(pass + k) * kLanes + mine] = ((o[0] + o[1]) + (o[2] + o[3])) + ((o[4] + o[5]) + (o[6] + o[7]));
                     }
                 }
             }
@@ -586,9 +589,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                     if (lane < kBlocks && ahead >= 0) bulk_prefetch(codes_of(n + kPrefetch, ahead), 16 * kDim);
                 }
                 const uint32_t number = base + j0 + n * kSlots;
-                const float ks = __shfl_sync(0xffffffffu, meta.k, inside * kBlocks + lane % kBlocks), vs = __shfl_sync(0xffffffffu, meta.v, inside * kBlocks + lane % kBlocks);
-                // What a scale of 0 makes of V is to leave no trace: zero, as is what is missing.
-                const unsigned some = __ballot_sync(0xffffffffu, ks >= 0.f && (vs > 0.f || !v));
+                // What is missing is zero, and what a scale of 0 makes of V, to leave no trace.  (K does without the scales until its
+                // codes are widened: the first ones are 3 us on their way.)
+                const int block = inside * kBlocks + lane % kBlocks;
+                const bool there = __shfl_sync(0xffffffffu, pages, block) >= 0;
+                unsigned some = __ballot_sync(0xffffffffu, there);
+                if (v) {  // (the whole warp)
+                    const float vs = __shfl_sync(0xffffffffu, meta.v, block);
+                    some &= __ballot_sync(0xffffffffu, vs > 0.f);
+                }
                 wait(v ? v_empty(number) : k_empty(number), (number / kSlots & 1) ^ 1);
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
@@ -615,7 +624,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                             *reinterpret_cast<uint4*>(hi_at + i * row8) = hi;
                         }
                     }
-                    if (half && !v && lane < kBlocks) s_meta[number % kMetaTiles][lane] = Meta{ks, log2f(vs)};
+                    if (half && !v) {
+                        const Meta of{__shfl_sync(0xffffffffu, meta.k, block), __shfl_sync(0xffffffffu, meta.v, block)};
+                        if (lane < kBlocks) s_meta[number % kMetaTiles][lane] = Meta{of.k, log2f(of.v)};
+                    }
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (half && lane == 0) mbar_arrive(v ? v_full(number) : k_full(number));
