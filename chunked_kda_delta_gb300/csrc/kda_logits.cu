@@ -11,7 +11,9 @@
 // by their place in the segment or, in long segments with short histories, in a hash table (linear probing, a
 // third of it free), while bulk copies bring the first chunks of the segment; touched and masked logits are
 // changed in the chunks, which leave by bulk copies.  (To fetch and store them one by one beside the copy is
-// a memory request each: 2000 of a row's 131072 made it 36 us, against 24.6 of the copy alone.)  In place, and
+// a memory request each: for 256 rows of 131072 bf16 with 2000 tokens each, 100 biases and a mask 42.8 us.  So it
+// is 34.4, 3.9 TB/s: the copy alone takes 24.6, the count before it, in which only the first chunks come, most
+// of the rest, latency of shared memory and of first instructions.)  In place, and
 // where out's 16-byte boundaries are not those of the logits, through registers: in place only loads of 16
 // bytes that the mask takes in part are read, and none written that it leaves alone.
 // Counts are whole numbers, so their order does not matter; biases of one token are added in the order of

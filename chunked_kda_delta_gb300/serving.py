@@ -4,7 +4,7 @@ logits and beam selection (``include/kda.h``).
 Thin wrappers of the extension ``_build/_kda_serving.so``, which checks the tensors, allocates what
 is returned and calls the C ABI, asynchronously on the given (or current) stream; every step runs
 in the library's CUDA kernels and there is no fallback.  Calls in a row: appending one token to 256
-rows 5.2 us, a selection of 4 from 4 beams 8.2, a fork of a cache's tables 14.7 (GB300); with this
+rows 5.2 us, with rotation 7.5, a selection of 4 from 4 beams 8.2, a fork of a cache's tables 14.7 (GB300); with this
 marshalling in Python and ctypes, where the host was the bound, 13.0, 25.3 and 33.9.
 Results and scratch are torch's memory of the call's stream: inside ``torch.cuda.graph`` they belong to
 the graph, and no call is needed before it.  (A capture begun without torch has to keep to the C

@@ -483,8 +483,8 @@ kda_status kda_beam_select(int32_t batch, int32_t beams, int32_t vocab, int32_t 
  *   x = x > 0 ? x / repetition : x * repetition   for tokens in the row's history;
  *   x = x - frequency * c - presence              for tokens that are c > 0 times in the history
  *                                                 behind the prompt;
- *   x = x + bias                                  for every entry of the row's list with that token,
- *                                                 in the list's order;
+ *   x = x + b                                     b: the sum, in the list's order, of the biases of
+ *                                                 the row's entries with that token;
  *   x = -inf                                      for tokens whose bit in the row's mask is 0.
  * fp32, rounded once to the logits' type; logits that none of these applies to keep their bits.
  *   logits, out    device [rows] rows of vocab values, logits_dtype KDA_LOGITS_*, row strides in
@@ -521,7 +521,8 @@ kda_status kda_logits_penalize(const kda_logits_rules* rules, int64_t rows, int3
                                const void* logits, int32_t logits_dtype, int64_t logits_stride,
                                void* out, int64_t out_stride, void* stream);
 
-/* Scratch of the page, cache and beam calls (kda_pages_*, kda_kvcache_*, kda_beam_select).  Each call
+/* Scratch of the page, cache and beam calls (kda_pages_*, kda_kvcache_*, kda_beam_select; with shared
+ * prefixes up to 2 GB, more is worked out without them).  Each call
  * takes its own, in the order of its stream, and gives it back after its last launch: calls share
  * none, whichever threads, streams and captured graphs they come from, and a capture needs no call before it.  By
  * default it comes from a memory pool of the library (cudaMallocFromPoolAsync; inside a capture it
