@@ -440,8 +440,8 @@ __device__ __forceinline__ void through_ring(const LogitsParams& p, const Segmen
     auto step = [&](int c, uint32_t (&bits)[kLoads]) {
         const uint32_t slot = c % kRing;
         unsigned char* chunk = ring + slot * kChunkBytes;
-        // (After a wait that ran out nothing more is asked for, and what follows is garbage.)
-        ok = ptx::mbar_wait(bar + 8 * slot, c / kRing & 1, ok ? kWaitLimit : 1) && ok;
+        // (After a wait that ran out nothing more is asked for; what is under way is waited for, and what follows is garbage.)
+        ok = ptx::mbar_wait(bar + 8 * slot, c / kRing & 1, ok ? kWaitLimit : 64) && ok;
         if constexpr (kTouched) {
             const int from = g.t0 + first + c * kChunk;
             for (int i = s_begin[c + 1] + tid; i < s_begin[c + 2]; i += kThreads) {
