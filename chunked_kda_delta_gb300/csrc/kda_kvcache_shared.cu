@@ -4,7 +4,9 @@
 // A group's prefix is the longest run of table entries that are the same in all of its rows with new
 // tokens, as far as every one of them sees all of its keys (before its first new token), in whole units of
 // kSharedUnit tokens: pages and tiles of every kernel end there.  So the result is the attention's,
-// whatever the groups are.  A cluster has a group; its warps compare a row with the first one each.
+// whatever the groups are.  A group's tokens lie one after another and no two groups' tokens meet: what comes after
+// counts on that, so with malformed offsets of any row nothing is shared.  A cluster has a group; its CTAs look at the
+// offsets of a part of all rows each, its warps compare a row with the first one each.
 // Bound by the launch and three dependent loads; the tables are read once (8 groups of 8 rows of 261 pages: 4 us).
 #include "kda_kvcache_attention.cuh"
 #include "kda_ptx.cuh"
@@ -44,6 +46,17 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
         for (int64_t r = (int64_t)blockIdx.x * kThreads + tid; r < c.rows; r += (int64_t)gridDim.x * kThreads) p.from[r] = 0;
         return;
     }
+    if (c.cu) {
+        bool malformed = rank == 0 && tid == 0 && (c.cu[0] != 0 || c.cu[c.rows] != c.tokens);
+        for (int r = rank * kThreads + tid; r < c.rows; r += kCluster * kThreads) {
+            const int a = c.cu[r], b = c.cu[r + 1];
+            malformed |= a < 0 || b < a || b > c.tokens;
+        }
+        if (malformed) {
+            s_equal = 0;
+            report(c.status, kStatusBadSeqlens);
+        }
+    }
     const int r0 = p.cu_rows[g], r1 = p.cu_rows[g + 1];
     for (int r = r0 + tid; r < r1; r += kThreads) {
         int64_t begin;
@@ -57,7 +70,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
     __syncthreads();
     const int ref = s_ref;
     const int64_t begin = c.cu ? c.cu[r0] : r0, end = c.cu ? c.cu[r1] : r1;
-    const bool shares = s_active >= p.least && s_tokens == end - begin;  // (malformed offsets: the row's tokens do not count)
+    const bool shares = s_active >= p.least && s_tokens == end - begin;  // (malformed offsets: s_equal is 0 somewhere)
     const int entries = shares ? s_limit / kSharedUnit * kSharedUnit / c.page_tokens : 0;
     if (entries > 0) {
         const int32_t* first = c.tables + (int64_t)ref * c.width;

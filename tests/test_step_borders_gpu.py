@@ -1,0 +1,96 @@
+"""Calls of a decoding step's operators at the borders of what they document: offsets, lengths and tokens out of range,
+values that are not finite, scales any distance apart, scratch, threads; and what rows are found to share."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import chunked_kda_delta_gb300 as K
+from chunked_kda_delta_gb300.kda import KdaKvCache, KdaScratchAllocator
+from step_testutil import ints
+
+pytestmark = pytest.mark.gpu
+P = lambda t: None if t is None else ctypes.c_void_p(t.data_ptr() if isinstance(t, torch.Tensor) else t)  # noqa: E731
+
+
+class Scratch:
+    """Scratch of this thread's calls: their sizes, and whatever `give` returns (nothing: the calls end there)."""
+
+    def __init__(self, give=lambda size: None):
+        def allocate(context, size, stream):
+            self.sizes.append(size)
+            return give(size)
+        self.sizes = []
+        fields = KdaScratchAllocator._fields_
+        self.a = KdaScratchAllocator(fields[0][1](allocate), fields[1][1](lambda context, p, size, stream: None), 0)
+
+    def __enter__(self):
+        assert K.load_library().kda_set_scratch_allocator(ctypes.byref(self.a), None) == 0
+        return self
+
+    def __exit__(self, *error):
+        assert K.load_library().kda_set_scratch_allocator(None, None) == 0
+
+
+def found_in_scratch(groups, lens, tables, page, hq, hkv, counts=None, cu=None, cu_rows=None, compare=True):
+    """Runs attention of rows with shared prefixes on the caller's scratch and returns that as bytes."""
+    lib, held = K.load_library(), []
+
+    def give(size):
+        held.append(torch.full((size,), 0xEE, dtype=torch.uint8, device="cuda"))
+        return held[-1].data_ptr()
+
+    rows, d, pages = len(lens), 64, int(tables.max()) + 1
+    gen = torch.Generator("cuda").manual_seed(1)
+    codes = [(torch.randn(pages, hkv, page, d, device="cuda", generator=gen) * 50).to(torch.float8_e4m3fn) for _ in range(2)]
+    scales = [torch.rand(pages, hkv, device="cuda", generator=gen) / 50 + 0.01 for _ in range(2)]
+    tab = torch.full((rows, 4_000_000 // page), -1, dtype=torch.int32, device="cuda")
+    tab[:, : tables.shape[1]] = ints(tables)
+    tokens = rows if cu is None else counts
+    q = torch.randn(tokens, hq, d, device="cuda", generator=gen).bfloat16()
+    ln, gr, out = ints(lens), ints(cu_rows if cu_rows is not None else np.cumsum([0] + groups)), torch.zeros_like(q)
+    c = KdaKvCache(*(t.data_ptr() for t in codes + scales), pages, page, hkv, d, tab.data_ptr(), rows, tab.shape[1])
+    with Scratch(give) as s:
+        assert lib.kda_kvcache_attention_shared(ctypes.byref(c), P(q), hq, 0, hq * d, tokens, P(ln), P(cu), P(gr), gr.numel() - 1, ctypes.c_float(0.1), P(out),
+                                                hq * d, P(torch.cuda.current_stream().cuda_stream)) == 0
+    torch.cuda.synchronize()
+    assert len(s.sizes) == 1
+    if compare:
+        want = K.kda_kvcache_attention(q, *codes, *scales, tab, ln, cu_tokens=cu, scale=0.1)
+        assert (out.double() - want.double()).abs().max() <= 2.0 ** -7 * want.abs().max()
+    return held[0].cpu().numpy().tobytes()
+
+
+def records(begin, tokens, shared, row):
+    """A group: first token, its rows' tokens, tokens of the prefix, the row whose table is read."""
+    return np.array([(b, t, s, r, 0) if s else (b, 0, 0, 0, 0) for b, t, s, r in zip(begin, tokens, shared, row)],
+                    dtype=[("begin", "<i8"), ("tokens", "<i4"), ("shared", "<i4"), ("row", "<i4"), ("unused", "<i4")]).tobytes()
+
+
+def private(rows, pages):
+    return np.arange(rows * pages).reshape(rows, pages)
+
+
+@pytest.mark.parametrize("cu_rows", [[0, 3, 5], [1, 3, 6], [0, 7, 6], [0, -1, 6]])
+def test_malformed_groups_share_nothing(cu_rows):
+    tables, lens = np.repeat(private(2, 32), 3, 0), np.full(6, 500)
+    K.kda_get_device_status()
+    got = found_in_scratch([3, 3], lens, tables, 16, 16, 1, cu_rows=cu_rows)
+    assert K.kda_get_device_status() != 0
+    assert records([0, 0], [0, 0], [0, 0], [0, 0]) in got and np.zeros(6, "<i4").tobytes() in got
+
+
+# Offsets that go back, leave the tokens or do not begin or end with them, also where a group's rows add up to what its
+# first and last offset say, and where groups come again.
+@pytest.mark.parametrize("cu", [[0, 3, 2, 4, 5, 7, 8], [-3, 2, 5, 9, 4, 6, 8], [0, 2, 6, 3, 8, 11, 8], [0, 4, 8, 0, 4, 8, 8], [1, 2, 3, 4, 5, 6, 8], [0, 2, 3, 4, 5, 6, 7],
+                                [0, 4, 2, 6, 20, 8, 8], [0, 8, 8, 0, 8, 0, 8]])
+@pytest.mark.parametrize("groups", [[6], [1, 5], [3, 3], [2, 1, 2, 1]])
+def test_nothing_is_shared_with_malformed_offsets(cu, groups):
+    tables, lens = np.tile(private(1, 32), (6, 1)), np.full(6, 500)
+    K.kda_get_device_status()
+    got = found_in_scratch(groups, lens, tables, 16, 16, 1, counts=8, cu=ints(cu), compare=False)
+    assert K.kda_get_device_status() != 0
+    begin = np.cumsum([0] + groups)[:-1]
+    assert records([cu[r] for r in begin], groups, [0] * len(groups), begin) in got
+    assert np.zeros(6, "<i4").tobytes() in got
