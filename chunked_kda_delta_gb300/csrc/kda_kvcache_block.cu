@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
     __shared__ int64_t s_first[kMaxListed + 1], s_scan[kThreads / 32], s_tiles[kThreads / 32];
     __shared__ __align__(16) Meta s_meta[4][kBlocks];
     __shared__ volatile int s_bad;  // a wait ran out
-    __shared__ __align__(8) uint64_t s_bar[3];
+    __shared__ __align__(8) uint64_t s_bar[4];
     __shared__ uint32_t s_tmem;
     unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     unsigned char* v_sm = smem;
@@ -100,12 +100,14 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
     // S of a tile is there (one barrier for each buffer: S(j + 1) may be done before the softmax has
     // seen S(j), and a barrier must not run two phases ahead of a waiter); O += P V is done.
     const uint32_t bar_s = smem_u32(&s_bar[0]), bar_o = smem_u32(&s_bar[2]);
+    const uint32_t drained = smem_u32(&s_bar[3]);  // after a wait that ran out: the issuing warp's products
     auto bar_of = [&](int j) { return bar_s + 8 * (j & 1); };  // j: tiles of the item so far
 
     if (tid == 0) {
         mbar_init(bar_of(0), 1 + kBlocks);  // S is computed, and the widening warps' scales are there
         mbar_init(bar_of(1), 1 + kBlocks);
         mbar_init(bar_o, 1);
+        mbar_init(drained, 1);
         fence_mbar_init();
         s_bad = 0;
     }
@@ -153,7 +155,8 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
     const int64_t per = share_of(first[c.rows], p.ctas);
     const int64_t w_begin = per * blockIdx.x, w_end = min(first[c.rows], w_begin + per);
     uint32_t phase_s = 0, phase_o = 0;  // (phase_s: a bit for each buffer)
-    // After a wait that ran out, all others end at once and what follows is garbage.
+    // After a wait that ran out, all others end at once and what follows is garbage; but products under way are waited
+    // for before the CTA gives its memory back.
     auto wait = [&](uint32_t bar, uint32_t phase) {
         if (!mbar_try_wait_now(bar, phase) && !mbar_wait_now(bar, phase, s_bad ? 1 : kWaitLimit)) s_bad = 1;
     };
@@ -535,9 +538,16 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
         tc_fence_after();
         w = item_end;
     }
-    if (s_bad && tid == 0) report(c.status, kStatusTimeout);
     tc_fence_before();
     __syncthreads();
+    if (s_bad) {  // (the same for all from here on)
+        if (tid == 0) report(c.status, kStatusTimeout);
+        if (issuer) {
+            commit_one(drained);
+            mbar_wait_now(drained, 0, kWaitLimit);
+        }
+        __syncthreads();
+    }
     if (warp == 0) tmem_dealloc(tmem, kColumns);
 }
 

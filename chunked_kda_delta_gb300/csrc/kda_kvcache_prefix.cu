@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     __shared__ float2 s_ml[kLanes];
     __shared__ __align__(16) Meta s_meta[kMetaTiles][kBlocks];
     __shared__ volatile int s_bad;  // a wait ran out
-    __shared__ __align__(8) uint64_t s_bar[4 * kSlots + 12 + 2 * kWidenWarps];
+    __shared__ __align__(8) uint64_t s_bar[4 * kSlots + 12 + 2 * kWidenWarps + 2];
     __shared__ uint32_t s_tmem;
     unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     unsigned char* v_sm = smem;
@@ -140,6 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     auto o_done = [&](int grp, uint32_t n) { return bars + 8 * (4 * kSlots + 4 + 2 * grp + (n & 1)); };  // O += P V of a step is done
     auto p_full = [&](int grp, uint32_t n) { return bars + 8 * (4 * kSlots + 8 + 2 * grp + (n & 1)); };  // P of a step is there
     const uint32_t raw_full = bars + 8 * (4 * kSlots + 12);  // codes of half a tile of a widening warp
+    const uint32_t drained = raw_full + 8 * 2 * kWidenWarps;  // after a wait that ran out: an issuing warp's products
 
     if (tid == 0) {
         for (uint32_t i = 0; i < kSlots; ++i) {
@@ -157,6 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
             mbar_init(p_full(grp, 1), 4);
         }
         for (int i = 0; i < 2 * kWidenWarps; ++i) mbar_init(raw_full + 8 * i, 2);
+        for (int grp = 0; grp < 2; ++grp) mbar_init(drained + 8 * grp, 1);
         fence_mbar_init();
         s_bad = 0;
     }
@@ -194,14 +196,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     const uint32_t tmem = uniform(s_tmem);
     const int64_t all = first[p.groups], per = quotient(all + p.ctas - 1, p.ctas);
     const int64_t w_begin = per * blockIdx.x, w_end = min(all, w_begin + per);
-    // After a wait that ran out, all others end at once and what follows is garbage.
+    // After a wait that ran out, all others end at once and what follows is garbage; but what is under way, codes on
+    // their way into shared memory and products, is waited for before the CTA gives its memory back.
     auto wait = [&](uint32_t bar, uint32_t phase) {
         if (!mbar_try_wait(bar, phase & 1) && !mbar_wait(bar, phase & 1, s_bad ? 1 : kWaitLimit)) s_bad = 1;
     };
     // For several barriers at once, a lane each (a wait costs 150 cycles also where it is over).
     auto wait_lanes = [&](bool some, uint32_t bar, uint32_t phase) {
         bool done = !some || mbar_test(bar, phase & 1);
-        for (int64_t i = s_bad ? 1 : 64 * kWaitLimit; !__all_sync(0xffffffffu, done) && i > 0; --i)
+        // (Each lane counts for itself and all leave together: they need not have seen the same of s_bad.)
+        for (int64_t i = s_bad ? 1 : 64 * kWaitLimit; !__all_sync(0xffffffffu, done || i <= 0); --i)
             if (!done) done = mbar_test(bar, phase & 1);
         if (!done) s_bad = 1;
         __syncwarp();
@@ -210,6 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     uint32_t steps[2] = {0, 0};  // steps of the softmax groups before this item
 
     uint32_t raw_base = 0;       // blocks of a widening warp before this item
+    bool stuck = false;          // its codes did not come: it asks for no more
     // Every kind of warps goes through the share's items by itself: body(group, item, its first tile, its tiles).
     auto each_item = [&](auto&& body) {
         for (int64_t w = w_begin; w < w_end;) {
@@ -557,6 +562,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                 return codes + ((int64_t)page * c.heads + it.head) * block_bytes + ((first_key(n) + lane * 16) & (c.page_tokens - 1)) * kDim;
             };
             unsigned char* own_raw = raw_sm + mine * kKeys * kDim;
+            // This warp's own copies, which wait for nobody: with the whole limit also after another wait ran out.
+            auto wait_codes = [&](uint32_t bar, uint32_t phase) {
+                const bool done = stuck || mbar_try_wait(bar, phase & 1) || mbar_wait(bar, phase & 1, kWaitLimit);
+                if (!__all_sync(0xffffffffu, done)) s_bad = 1, stuck = true;
+            };
             // Asks for the codes of half a tile, a lane for 16 keys.
             auto request = [&](int n, int half, int batch) {
                 const int32_t page = page_of(n, batch);
@@ -570,8 +580,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                     }
                 }
             };
-            request(0, 0, 0);
-            request(0, 1, 0);
+            if (!stuck) {
+                request(0, 0, 0);
+                request(0, 1, 0);
+            }
             // A lane's pieces of 32 keys: key lane % 8 and every eighth from it, and of them the 16 channels that go with lane / 8 and
             // h: a diagonal, eight lanes have eight keys, and together all banks of what is read and of what is written.
             const int key = lane % 8;
@@ -608,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                 wait(v ? v_empty(number) : k_empty(number), (number / kSlots & 1) ^ 1);
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
-                    wait(raw_full + 8 * (2 * mine + half), raw_base + n);
+                    wait_codes(raw_full + 8 * (2 * mine + half), raw_base + n);
                     const unsigned char* src = own_raw + half * 32 * kDim + key * kDim;
                     uint4 raw[kDim / 64][4];
 #pragma unroll
@@ -638,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (half && lane == 0) mbar_arrive(v ? v_full(number) : k_full(number));
-                    if (n + 1 < own) request(n + 1, half, batch);
+                    if (n + 1 < own && !stuck) request(n + 1, half, batch);
                 }
                 if (inside == kBatch - 1) {
                     pages = pages_next;
@@ -648,9 +660,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
             raw_base += own;
         });
     }
-    if (s_bad && tid == 0) report(c.status, kStatusTimeout);
     tc_fence_before();
     __syncthreads();
+    if (s_bad) {  // (the same for all from here on)
+        if (tid == 0) report(c.status, kStatusTimeout);
+        if (warp == kIssuer || warp == kIssuer + 1) {
+            commit_one(drained + 8 * (warp - kIssuer));
+            mbar_wait(drained + 8 * (warp - kIssuer), 0, kWaitLimit);
+        }
+        __syncthreads();
+    }
     if (warp == kIssuer) tmem_dealloc(tmem, 512);
 }
 
