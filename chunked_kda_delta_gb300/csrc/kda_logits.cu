@@ -588,7 +588,9 @@ cudaError_t launch_type(LogitsParams& p, cudaStream_t stream) {
     const int64_t chunks = (len * (int64_t)sizeof(T) + kChunkBytes - 1) / kChunkBytes;
     const size_t smem = (size_t)p.entries * (p.num_bias > 0 ? 12 : 8) + (ring ? (size_t)p.entries * 2 + (size_t)(chunks < kRing ? chunks : kRing) * kChunkBytes : 0);
     if (smem > 40 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        // (The most that any call needs, not this one: the limit is the kernel's, for calls of other threads too.)
+        const int most = ring ? kMostEntries * 14 + kRing * kChunkBytes : kMostEntries * 12;
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
         if (e != cudaSuccess) return e;
     }
     return launch_early(kernel, dim3((unsigned)(p.rows * p.segs)), kThreads, smem, stream, 1, p);

@@ -1,17 +1,44 @@
 """Calls of a decoding step's operators at the borders of what they document: offsets, lengths and tokens out of range,
 values that are not finite, scales any distance apart, scratch, threads; and what rows are found to share."""
 import ctypes
+from concurrent.futures import ThreadPoolExecutor
 
 import numpy as np
 import pytest
 import torch
 
 import chunked_kda_delta_gb300 as K
-from chunked_kda_delta_gb300.kda import KdaKvCache, KdaScratchAllocator
+import test_logits_gpu as logits
+from chunked_kda_delta_gb300.kda import KdaKvCache, KdaLogitsRules, KdaScratchAllocator
 from step_testutil import ints
 
 pytestmark = pytest.mark.gpu
 P = lambda t: None if t is None else ctypes.c_void_p(t.data_ptr() if isinstance(t, torch.Tensor) else t)  # noqa: E731
+
+
+def test_penalties_from_several_threads():
+    # the C calls run at the same time and need different amounts of shared memory for the same kernel
+    lib = K.load_library()
+    rng = np.random.default_rng(1)
+    rows, vocab, jobs = 300, 25003, []
+    x = torch.as_tensor(rng.standard_normal((rows, vocab)).astype(np.float32)).cuda().bfloat16()
+    for width, biases in ((100, 20), (2000, 100), (100, 20), (5000, 300)):
+        made = logits.make(rng, rows, vocab, width=width, biases=biases, lens=False)
+        t = {k: ints(v) if v.dtype == np.int64 else torch.as_tensor(v).cuda() for k, v in made.items()}
+        rules = KdaLogitsRules(history_width=width, num_bias=biases, **{k: v.data_ptr() for k, v in t.items()})
+        jobs.append((t, rules, torch.zeros_like(x), K.kda_logits_penalize(x, **t), torch.cuda.Stream().cuda_stream))
+    torch.cuda.synchronize()
+
+    def work(job):
+        _, rules, out, _, stream = job
+        return {lib.kda_logits_penalize(ctypes.byref(rules), rows, vocab, P(x), 1, vocab, P(out), vocab, P(stream)) for _ in range(1500)}
+
+    with ThreadPoolExecutor(len(jobs)) as pool:
+        codes = list(pool.map(work, jobs))
+    torch.cuda.synchronize()
+    assert codes == [{0}] * len(jobs)
+    for _, _, out, want, _ in jobs:
+        assert torch.equal(out, want)
 
 
 class Scratch:
