@@ -749,13 +749,15 @@ cudaError_t launch_dim(const AttentionParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     e = launch_early(prefix_kernel<T, kDim>, dim3(p.ctas), kThreads, kSmemBytes<kDim>, stream, 1, p);
     if (e != cudaSuccess) return e;
-    return launch_early(prefix_join_kernel<kDim>, dim3((unsigned)prefix_items(p), kDim / kJoinCh), kJoinThreads, 0, stream, 1, p);
+    return launch_early(prefix_join_kernel<kDim>, dim3((unsigned)prefix_items(p, p.least), kDim / kJoinCh), kJoinThreads, 0, stream, 1, p);
 }
 
 }  // namespace
 
-int64_t prefix_items(const AttentionParams& p) {
-    return (p.c.tokens * (p.q_heads / p.c.heads) / kLanes + p.groups) * p.c.heads;
+// (Groups that share have at least `least` rows with tokens each.)
+int64_t prefix_items(const AttentionParams& p, int32_t least) {
+    const int64_t most = (p.c.tokens < p.c.rows ? p.c.tokens : p.c.rows) / least;
+    return (p.c.tokens * (p.q_heads / p.c.heads) / kLanes + (most < p.groups ? most : p.groups)) * p.c.heads;
 }
 cudaError_t launch_prefix(const AttentionParams& p, bool f16, cudaStream_t stream) {
     if (p.c.dim == 64) return f16 ? launch_dim<__half, 64>(p, stream) : launch_dim<__nv_bfloat16, 64>(p, stream);

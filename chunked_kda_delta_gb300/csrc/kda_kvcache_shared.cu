@@ -118,11 +118,11 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const __grid_constant__ 
 // of a group here.  8 heads, dim 128, shared against not (us): 8 rows of 4196 keys 44 and 29, of 16484 63 and 59,
 // of 32868 75 and 94; 8 groups of 4 rows of 4196 keys 71 and 51, of 8292 85 and 82, 16 groups of 16684 192
 // and 270; 8 rows with 6 tokens of 8292 keys 75 and 70, 64 of 16684 392 and 625; pieces of 64 tokens gain nothing.
-// A state past 2^27 numbers would be a workspace of a GB.
-bool sharing_pays(const AttentionParams& p, int cols) {
+// (State and parts past kMostSharedScratch are the caller's to refuse; a state of 2^27 numbers alone is 512 MB.)
+bool sharing_pays(const AttentionParams& p, int cols, int32_t least) {
     const CacheParams& c = p.c;
     const int64_t group = p.q_heads / c.heads;
-    if (p.groups >= c.rows || c.tokens * p.q_heads * c.dim > (1 << 27)) return false;
+    if (p.groups >= c.rows || c.rows < least || c.tokens < least || c.tokens * p.q_heads * c.dim > (1 << 27)) return false;
     const double keys = (double)c.width * c.page_tokens * c.heads, cycles = c.dim == 64 ? 900 : 1350;
     if (cols < kBlockRows) return (double)(c.rows - p.groups) * keys * 2 * c.dim / 8e6 >= 55;
     const int64_t each = (c.tokens + c.rows - 1) / c.rows * group;

@@ -161,7 +161,7 @@ struct AttentionParams {
     int32_t ctas, sm_count;
     // shared prefixes
     const SharedGroup* group; // [groups]
-    int32_t groups;
+    int32_t groups, least;    // least: SharedPlan's
     const int32_t* from;      // [rows]: tokens of the prefix
     float* state_o;           // [tokens * q_heads][dim], what the prefix left: outputs,
     float2* state_ml;         // [tokens * q_heads], maxima and sums
@@ -184,10 +184,11 @@ struct SharedPlan {
     SharedGroup* group;
     int32_t* from;
 };
-bool sharing_pays(const AttentionParams& p, int cols);  // cols: attention_cols
+bool sharing_pays(const AttentionParams& p, int cols, int32_t least);  // cols: attention_cols
 cudaError_t launch_shared_plan(const SharedPlan& p, cudaStream_t stream);
 constexpr int kPrefixLanes = 256;  // query rows of an item, and of a part
-int64_t prefix_items(const AttentionParams& p);  // at most
+int64_t prefix_items(const AttentionParams& p, int32_t least);  // at most
+constexpr size_t kMostSharedScratch = (size_t)1 << 31;  // bytes; calls that would take more share nothing
 cudaError_t launch_prefix(const AttentionParams& p, bool f16, cudaStream_t stream);
 cudaError_t launch_block_suffix(const AttentionParams& p, bool f16, cudaStream_t stream);
 cudaError_t launch_suffix(const AttentionParams& p, int cols, bool f16, cudaStream_t stream);

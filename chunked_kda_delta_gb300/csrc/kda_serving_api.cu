@@ -284,23 +284,32 @@ kda_status attend(const kda_kvcache* cache, const void* q, int32_t num_q_heads, 
     // With shared prefixes the parts' place is the prefixes' first, then the rows'.
     p.q_heads = num_q_heads;
     p.groups = groups;
-    if (cu_rows && !kda::sharing_pays(p, cols)) cu_rows = nullptr, groups = 0;
-    size_t parts = (cols == kda::kBlockRows ? (size_t)2 * p.ctas : kda::attention_slots(p.ctas)) * cols;
-    if (cu_rows) {
-        const size_t prefix = (size_t)(kda::prefix_items(p) + di->sm_count) * kda::kPrefixLanes;
-        if (prefix > parts) parts = prefix;
-    }
-    const size_t units = (size_t)cache->rows, query_rows = cu_rows ? (size_t)num_tokens * num_q_heads : 0;
-    size_t bytes = 0;
+    // (A tile of the prefixes' kernel is 1.3 us of an SM, as much as two rows' with few query rows each: 32 pairs of
+    // rows of 16684 keys took 308 us with shared prefixes and 274 without, 21 groups of three 226 and 268.)
+    const int32_t least = cols == 8 ? 3 : 2;
+    if (cu_rows && !kda::sharing_pays(p, cols, least)) cu_rows = nullptr;
+    const size_t units = (size_t)cache->rows;
+    size_t bytes, at_o, at_ml, at_split, at_first, at_group, at_from, at_state, at_state_ml, at_item;
     auto place = [&](size_t n) {
         const size_t at = bytes;
         bytes += (n + 255) / 256 * 256;
         return at;
     };
-    const size_t at_o = place(parts * cache->head_dim * 4), at_ml = place(parts * 2 * 4), at_split = place((size_t)p.ctas * 32),
-                 at_first = place((units + 1) * 8), at_group = place((size_t)groups * sizeof(kda::SharedGroup)),
-                 at_from = place(cu_rows ? (size_t)cache->rows * 4 : 0), at_state = place(query_rows * cache->head_dim * 4),
-                 at_state_ml = place(query_rows * 8), at_item = place(cu_rows ? (units + 1) * 8 : 0);
+    for (;;) {
+        size_t parts = (cols == kda::kBlockRows ? (size_t)2 * p.ctas : kda::attention_slots(p.ctas)) * cols;
+        if (cu_rows) {
+            const size_t prefix = (size_t)(kda::prefix_items(p, least) + di->sm_count) * kda::kPrefixLanes;
+            if (prefix > parts) parts = prefix;
+        }
+        const size_t query_rows = cu_rows ? (size_t)num_tokens * num_q_heads : 0;
+        bytes = 0;
+        at_o = place(parts * cache->head_dim * 4), at_ml = place(parts * 2 * 4), at_split = place((size_t)p.ctas * 32);
+        at_first = place((units + 1) * 8), at_group = place(cu_rows ? (size_t)groups * sizeof(kda::SharedGroup) : 0);
+        at_from = place(cu_rows ? units * 4 : 0), at_state = place(query_rows * cache->head_dim * 4);
+        at_state_ml = place(query_rows * 8), at_item = place(cu_rows ? (units + 1) * 8 : 0);
+        if (!cu_rows || bytes <= kda::kMostSharedScratch) break;
+        cu_rows = nullptr;  // worked out without shared prefixes
+    }
     Scratch ws;
     if ((st = ws.take(dev, stream, bytes)) != KDA_OK) return st;
     p.part_o = reinterpret_cast<float*>(ws.base + at_o);
@@ -317,9 +326,6 @@ kda_status attend(const kda_kvcache* cache, const void* q, int32_t num_q_heads, 
         const cudaError_t e = kda::launch_attention(p, cols, f16, on);
         return e == cudaSuccess ? KDA_OK : cuda_fail(e, "cache attention launch");
     }
-    // (A tile of the prefixes' kernel is 1.3 us of an SM, as much as two rows' with few query rows each: 32 pairs of
-    // rows of 16684 keys took 308 us with shared prefixes and 274 without, 21 groups of three 226 and 268.)
-    const int32_t least = cols == 8 ? 3 : 2;
     kda::SharedPlan plan{p.c, cu_rows, groups, least, reinterpret_cast<kda::SharedGroup*>(ws.base + at_group), reinterpret_cast<int32_t*>(ws.base + at_from)};
     p.group = plan.group;
     p.from = plan.from;
@@ -328,6 +334,7 @@ kda_status attend(const kda_kvcache* cache, const void* q, int32_t num_q_heads, 
     p.first_item = reinterpret_cast<int64_t*>(ws.base + at_item);
     kda::AttentionParams prefix = p;
     prefix.ctas = di->sm_count;
+    prefix.least = least;
     cudaError_t e = kda::launch_shared_plan(plan, on);
     if (e == cudaSuccess) e = kda::launch_prefix(prefix, f16, on);
     if (e == cudaSuccess) e = kda::launch_suffix(p, cols, f16, on);

@@ -60,6 +60,38 @@ class Scratch:
         assert K.load_library().kda_set_scratch_allocator(None, None) == 0
 
 
+def scratch_sizes(rows, groups, hq, hkv, d, width=1024):
+    """Bytes of scratch that the calls with and without shared prefixes ask for."""
+    lib, at, sizes = K.load_library(), iter(range(1 << 40, 1 << 47, 1 << 40)), []
+    # (addresses far apart: no work is put on the stream without scratch)
+    c = KdaKvCache(*(next(at) for _ in range(4)), 1 << 10, 64, hkv, d, next(at), rows, width)
+    q, lens, cu_rows, out = (next(at) for _ in range(4))
+    with Scratch() as s:
+        tail = (ctypes.c_float(0.1), P(out), hq * d, None)
+        assert lib.kda_kvcache_attention_shared(ctypes.byref(c), P(q), hq, 0, hq * d, rows, P(lens), None, P(cu_rows), groups, *tail) == 4
+        assert lib.kda_kvcache_attention(ctypes.byref(c), P(q), hq, 0, hq * d, rows, P(lens), None, *tail) == 4
+    return s.sizes
+
+
+@pytest.mark.parametrize("rows,groups,hq,hkv,d", [(16384, 4096, 64, 8, 128), (2048, 512, 64, 64, 128), (16384, 16383, 64, 64, 128), (2048, 1024, 64, 64, 128),
+                                                  (4096, 2048, 64, 8, 128), (1024, 512, 32, 32, 128), (32768, 9000, 64, 32, 64)])
+def test_scratch_of_shared_prefixes_is_bounded(rows, groups, hq, hkv, d):
+    shared, _ = scratch_sizes(rows, groups, hq, hkv, d)
+    assert shared <= 2 ** 31
+
+
+def test_scratch_where_prefixes_are_shared_and_where_not():
+    state = 1024 * 64 * 128 * 4
+    shared, alone = scratch_sizes(1024, 256, 64, 8, 128)
+    assert state < shared <= 2 ** 31 and alone < state
+    shared, alone = scratch_sizes(2, 1, 8, 1, 128, width=1 << 16)  # (of rows with so few query rows three share, not two)
+    assert shared == alone
+    shared, alone = scratch_sizes(3, 1, 8, 1, 128, width=1 << 16)
+    assert shared > alone
+    shared, alone = scratch_sizes(16384, 4096, 64, 64, 128)  # (of too many groups' and heads' prefixes the parts would take 35 GB)
+    assert shared == alone
+
+
 def found_in_scratch(groups, lens, tables, page, hq, hkv, counts=None, cu=None, cu_rows=None, compare=True):
     """Runs attention of rows with shared prefixes on the caller's scratch and returns that as bytes."""
     lib, held = K.load_library(), []
