@@ -208,7 +208,9 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(c
 #pragma unroll
             for (int j = 0; j < kMT; ++j) o[nt][j][0] = o[nt][j][1] = o[nt][j][2] = o[nt][j][3] = 0.f;
         }
+        float least = kScaleLeast;  // that a log2 of v's scale counts as: the same for the warp
         if (kKind == kKindSuffix && w == item && from > 0) {  // on from the prefix
+            least = p.state_ml[(begin + row0 / group) * p.q_heads + head * group + row0 % group].z;  // (as in all of its rows)
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
@@ -216,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(c
                     const int f = row0 + nt * 8 + 2 * t + col;
                     if (f >= rows_all) continue;
                     const int64_t at = (begin + f / group) * p.q_heads + head * group + f % group;
-                    const float2 ml = p.state_ml[at];
+                    const float4 ml = p.state_ml[at];
                     m[nt][col] = ml.x + (kLift - kBlockLift);
                     l[nt][col] = g == 0 ? ml.y : 0.f;  // (summed over the lanes in the end)
                     const float2* src = reinterpret_cast<const float2*>(p.state_o + at * kDim + kVWords * 4 * g);
@@ -232,7 +234,6 @@ __global__ void __launch_bounds__(kThreads, kNT == 1 ? 3 : 2) attention_kernel(c
         auto scale_of = [&](const float* scales, int32_t page) { return page < 0 ? 0.f : scales[(int64_t)page * c.heads + head]; };
         auto log_of = [&](int32_t page) { return page < 0 ? 0.f : log2f(scale_of(c.v_scale, page)); };
         float k_scales = scale_of(c.k_scale, pages), v_logs = log_of(pages);
-        float least = kScaleLeast;  // that a log2 of v's scale counts as
         int b0 = slab0 * kBlk;  // block of lane 0
 
         uint4 kr[kBlk][2][kHalves];  // [16 keys][key g, g + 8][channel half]

@@ -145,7 +145,7 @@ __device__ __forceinline__ int row_of(const int64_t* first, int rows, int64_t w)
 }
 
 // What a launch's rows have: all of their keys, or those behind a prefix that is shared (kda_kvcache_shared.cu),
-// which go on from the state (maximum, sum, output) that the prefix left for each query row.
+// which go on from the state (maximum, sum, least scale, output) that the prefix left for each query row.
 enum { kKindRows = 0, kKindSuffix = 1 };
 // A row's first key (a multiple of kSharedUnit).
 template <int kKind>

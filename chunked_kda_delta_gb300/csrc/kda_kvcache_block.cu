@@ -381,8 +381,8 @@ __global__ void __launch_bounds__(kThreads, 2) block_attention_kernel(const __gr
         } else {
             float least = kScaleLeast;  // that a log2 of v's scale counts as
             if (goes_on && there) {
-                const float2 ml = p.state_ml[state];
-                m = ml.x, l = ml.y;
+                const float4 ml = p.state_ml[state];
+                m = ml.x, l = ml.y, least = ml.z;
             }
             for (int tile = tile0; tile < tile1; ++tile) {
                 wait_s(tile - tile0);

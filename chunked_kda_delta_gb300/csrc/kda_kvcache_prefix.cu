@@ -22,7 +22,8 @@
 //
 // Softmax as in kda_kvcache_block.cu: O is rescaled only when a row's maximum has grown by more than 2^8 over
 // the one in use; v's scale enters the exponent and leaves the sum again by blocks of 16 keys; q's and the
-// scales' handling is kda_kvcache_attention.cu's.
+// scales' handling is kda_kvcache_attention.cu's.  The maximum holds the prefix's largest scale, so what a scale counts
+// as at least goes into the state with it.
 //
 // What bounds it: for items of up to 128 rows shared memory, where a widened tile of head_dim 128 is written and read
 // for 1024 cycles (codes in, out, operands in, K and V by the matrix instructions); it takes 1250.  For wider ones the
@@ -113,7 +114,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
     constexpr uint32_t kColO = 128, kColGroup = 256;  // tensor memory of a softmax group: S and P, O
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     __shared__ int64_t s_first[kMaxListed + 1], s_item[kMaxListed + 1], s_scan[kThreads / 32];
-    __shared__ float2 s_ml[kLanes];
+    __shared__ float s_ml[3][kLanes];
     __shared__ __align__(16) Meta s_meta[kMetaTiles][kBlocks];
     __shared__ volatile int s_bad;  // a wait ran out
     __shared__ __align__(8) uint64_t s_bar[4 * kSlots + 12 + 2 * kWidenWarps + 2];
@@ -235,8 +236,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
         each_item([&](const SharedGroup& sg, const Item& it, int tile0, int tiles) {
             const int grp = warp / 4, t = tid % kRows;
             if (tiles == 0) {  // (half of a wide item's tile)
-                p.part_ml[(it.number + blockIdx.x) * 2 * kLanes + tid] = kNegInf;
-                p.part_ml[(it.number + blockIdx.x) * 2 * kLanes + kLanes + tid] = 0.f;
+                float* part_ml = p.part_ml + (it.number + blockIdx.x) * 3 * kLanes + tid;
+                part_ml[0] = kNegInf;
+                part_ml[kLanes] = 0.f;
+                part_ml[2 * kLanes] = kScaleLeast;
                 return;
             }
             // Rows of a narrow item stand `copies` times among the 128.
@@ -412,19 +415,19 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
             // joined in shared memory first, in q's place.
             const int64_t slot = it.number + blockIdx.x;
             const int at = grp * kRows + t;
-            float* part_ml = p.part_ml + slot * 2 * kLanes;
+            float* part_ml = p.part_ml + slot * 3 * kLanes;
             float scale = 1.f;
             if (!it.wide) {
                 named_bar_sync(kBarSoft, kLanes);  // both groups are done with q
-                s_ml[at] = make_float2(m, l);
+                s_ml[0][at] = m, s_ml[1][at] = l, s_ml[2][at] = least;
                 named_bar_sync(kBarSoft, kLanes);
                 const int mine = at & (spread - 1);
                 float top = kNegInf, sum = 0.f;
 #pragma unroll 1
-                for (int x = mine; x < kLanes; x += spread) top = fmaxf(top, s_ml[x].x);
+                for (int x = mine; x < kLanes; x += spread) top = fmaxf(top, s_ml[0][x]), least = fmaxf(least, s_ml[2][x]);
                 const float use = top == kNegInf ? 0.f : top;
 #pragma unroll 1
-                for (int x = mine; x < kLanes; x += spread) sum += rescaled(s_ml[x].y, exp2_fast(0.5f * (s_ml[x].x - use)));
+                for (int x = mine; x < kLanes; x += spread) sum += rescaled(s_ml[1][x], exp2_fast(0.5f * (s_ml[0][x] - use)));
                 scale = exp2_fast(0.5f * (m - use));
                 scale *= scale;
                 m = top, l = sum;
@@ -432,6 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(const __grid_consta
             if (it.wide || at < spread) {
                 part_ml[at] = m;
                 part_ml[kLanes + at] = l;
+                part_ml[2 * kLanes + at] = least;
             }
             float* part_o = p.part_o + slot * kDim * kLanes;
             if (it.wide) {
@@ -679,7 +683,7 @@ constexpr int kJoinThreads = 256, kJoinCh = 16;
 
 template <int kDim>
 __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_constant__ AttentionParams p) {
-    __shared__ float s_part[kJoinCh + 2][kJoinThreads];
+    __shared__ float s_part[kJoinCh + 3][kJoinThreads];
     const int tid = threadIdx.x, d0 = blockIdx.y * kJoinCh, heads = p.q_heads / p.c.heads;
     follow_stream();
     const int64_t number = blockIdx.x, all = p.first_work[p.groups];
@@ -694,10 +698,11 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
     const int log_lanes = it.rows > 128 ? 8 : it.rows > 64 ? 7 : it.rows > 32 ? 6 : 5, shares = kJoinThreads >> log_lanes;
     const int lane = tid & ((1 << log_lanes) - 1), share = tid >> log_lanes;
 
-    float top = kNegInf, sum = 0.f, acc[kJoinCh];
+    float top = kNegInf, sum = 0.f, least = kScaleLeast, acc[kJoinCh];
 #pragma unroll
     for (int d = 0; d < kJoinCh; ++d) acc[d] = 0.f;
-    auto add = [&](float mk, float lk, const float* o) {
+    auto add = [&](float mk, float lk, float least_k, const float* o) {
+        least = fmaxf(least, least_k);
         const float m = fmaxf(top, mk), use = m == kNegInf ? 0.f : m;
         const float ha = exp2_fast(0.5f * (top - use)), hb = exp2_fast(0.5f * (mk - use)), a = ha * ha, b = hb * hb;
         top = m;
@@ -707,24 +712,26 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
     };
     constexpr int kAhead = 3;
     for (int64_t u = u0 + share; u <= u1; u += kAhead * shares) {
-        float mk[kAhead], lk[kAhead], o[kAhead][kJoinCh];
+        float mk[kAhead], lk[kAhead], least_k[kAhead], o[kAhead][kJoinCh];
 #pragma unroll
         for (int x = 0; x < kAhead; ++x) {
             const int64_t at = u + x * shares, slot = it.number + at;
             if (at > u1) continue;
-            mk[x] = p.part_ml[slot * 2 * kLanes + lane];
-            lk[x] = p.part_ml[slot * 2 * kLanes + kLanes + lane];
+            mk[x] = p.part_ml[slot * 3 * kLanes + lane];
+            lk[x] = p.part_ml[slot * 3 * kLanes + kLanes + lane];
+            least_k[x] = p.part_ml[slot * 3 * kLanes + 2 * kLanes + lane];
 #pragma unroll
             for (int d = 0; d < kJoinCh; ++d) o[x][d] = p.part_o[(slot * kDim + d0 + d) * kLanes + lane];
         }
 #pragma unroll
         for (int x = 0; x < kAhead; ++x)
-            if (u + x * shares <= u1) add(mk[x], lk[x], o[x]);
+            if (u + x * shares <= u1) add(mk[x], lk[x], least_k[x], o[x]);
     }
     const int used = (int)min((int64_t)shares, u1 - u0 + 1);  // shares that have a part
     if (share && share < used) {
         s_part[kJoinCh][tid] = top;
         s_part[kJoinCh + 1][tid] = sum;
+        s_part[kJoinCh + 2][tid] = least;
 #pragma unroll
         for (int d = 0; d < kJoinCh; ++d) s_part[d][tid] = acc[d];
     }
@@ -734,11 +741,11 @@ __global__ void __launch_bounds__(kJoinThreads) prefix_join_kernel(const __grid_
         float o[kJoinCh];
 #pragma unroll
         for (int d = 0; d < kJoinCh; ++d) o[d] = s_part[d][(x << log_lanes) + lane];
-        add(s_part[kJoinCh][(x << log_lanes) + lane], s_part[kJoinCh + 1][(x << log_lanes) + lane], o);
+        add(s_part[kJoinCh][(x << log_lanes) + lane], s_part[kJoinCh + 1][(x << log_lanes) + lane], s_part[kJoinCh + 2][(x << log_lanes) + lane], o);
     }
     const int f = it.block * kLanes + lane;
     const int64_t state = (sg.begin + f / heads) * p.q_heads + it.head * heads + f % heads;
-    if (d0 == 0) p.state_ml[state] = make_float2(top, sum);
+    if (d0 == 0) p.state_ml[state] = make_float4(top, sum, least, 0.f);
 #pragma unroll
     for (int d = 0; d < kJoinCh; d += 4) *reinterpret_cast<float4*>(p.state_o + state * kDim + d0 + d) = make_float4(acc[d], acc[d + 1], acc[d + 2], acc[d + 3]);
 }

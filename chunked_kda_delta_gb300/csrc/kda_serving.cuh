@@ -164,7 +164,7 @@ struct AttentionParams {
     int32_t groups, least;    // least: SharedPlan's
     const int32_t* from;      // [rows]: tokens of the prefix
     float* state_o;           // [tokens * q_heads][dim], what the prefix left: outputs,
-    float2* state_ml;         // [tokens * q_heads], maxima and sums
+    float4* state_ml;         // [tokens * q_heads]: maximum, sum, what a log2 of v's scale counts as at least
     int64_t* first_item;      // [groups + 1] (kda_kvcache_prefix.cu)
 };
 size_t attention_slots(int ctas);

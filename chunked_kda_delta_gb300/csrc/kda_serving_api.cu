@@ -297,16 +297,18 @@ kda_status attend(const kda_kvcache* cache, const void* q, int32_t num_q_heads, 
     };
     for (;;) {
         size_t parts = (cols == kda::kBlockRows ? (size_t)2 * p.ctas : kda::attention_slots(p.ctas)) * cols;
+        size_t part_ml = parts * 2;
         if (cu_rows) {
             const size_t prefix = (size_t)(kda::prefix_items(p, least) + di->sm_count) * kda::kPrefixLanes;
             if (prefix > parts) parts = prefix;
+            if (3 * prefix > part_ml) part_ml = 3 * prefix;
         }
         const size_t query_rows = cu_rows ? (size_t)num_tokens * num_q_heads : 0;
         bytes = 0;
-        at_o = place(parts * cache->head_dim * 4), at_ml = place(parts * 2 * 4), at_split = place((size_t)p.ctas * 32);
+        at_o = place(parts * cache->head_dim * 4), at_ml = place(part_ml * 4), at_split = place((size_t)p.ctas * 32);
         at_first = place((units + 1) * 8), at_group = place(cu_rows ? (size_t)groups * sizeof(kda::SharedGroup) : 0);
         at_from = place(cu_rows ? units * 4 : 0), at_state = place(query_rows * cache->head_dim * 4);
-        at_state_ml = place(query_rows * 8), at_item = place(cu_rows ? (units + 1) * 8 : 0);
+        at_state_ml = place(query_rows * 16), at_item = place(cu_rows ? (units + 1) * 8 : 0);
         if (!cu_rows || bytes <= kda::kMostSharedScratch) break;
         cu_rows = nullptr;  // worked out without shared prefixes
     }
@@ -330,7 +332,7 @@ kda_status attend(const kda_kvcache* cache, const void* q, int32_t num_q_heads, 
     p.group = plan.group;
     p.from = plan.from;
     p.state_o = reinterpret_cast<float*>(ws.base + at_state);
-    p.state_ml = reinterpret_cast<float2*>(ws.base + at_state_ml);
+    p.state_ml = reinterpret_cast<float4*>(ws.base + at_state_ml);
     p.first_item = reinterpret_cast<int64_t*>(ws.base + at_item);
     kda::AttentionParams prefix = p;
     prefix.ctas = di->sm_count;

@@ -8,9 +8,11 @@ import pytest
 import torch
 
 import chunked_kda_delta_gb300 as K
+import serving_testutil as ref
 import test_logits_gpu as logits
 from chunked_kda_delta_gb300.kda import KdaKvCache, KdaLogitsRules, KdaScratchAllocator
-from step_testutil import ints
+from step_testutil import cu_of, ints
+from test_shared_attention_gpu import gpu_cache, make_cache
 
 pytestmark = pytest.mark.gpu
 P = lambda t: None if t is None else ctypes.c_void_p(t.data_ptr() if isinstance(t, torch.Tensor) else t)  # noqa: E731
@@ -39,6 +41,27 @@ def test_penalties_from_several_threads():
     assert codes == [{0}] * len(jobs)
     for _, _, out, want, _ in jobs:
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("order", [1, -1, 0])
+@pytest.mark.parametrize("small,large", [(0, 2.0 ** 110), (2.0 ** -70, 2.0 ** 60), (2.0 ** -20, 2.0 ** 110)])
+@pytest.mark.parametrize("n,hq,d,shared", [(1, 4, 64, 256), (1, 16, 128, 256), (1, 24, 64, 256), (100, 8, 64, 256), (60, 16, 128, 128), (1, 8, 64, 5120)])
+def test_scales_of_values_any_distance_apart(n, hq, d, shared, small, large, order):
+    # equal scores; scales of v are large in the prefix and small behind it, or the other way, or either by
+    # chance.  Keys of small scales keep their share of the weights.  The bound is the one of rows that share nothing.
+    rng = np.random.default_rng(shared + d)
+    behind = 200 if shared < 5120 else 3000
+    kc, vc, ks, vs, tables, lens = make_cache(rng, [[(0, shared + behind)] + [(shared, shared + behind - i) for i in range(1, 4)]], 16, 2, d)
+    first = np.zeros(len(vs), bool)
+    first[tables[0, : shared // 16]] = True
+    vs[:] = np.where(rng.random(len(vs)) < 0.5 if order == 0 else first == (order > 0), large, small)[:, None]
+    q = torch.zeros(4 * n, hq, d, dtype=torch.bfloat16)
+    want, weight = ref.attention(q.double().numpy(), kc, vc, ks, vs, tables, lens, [n] * 4, 16, 0.125)
+    got = K.kda_kvcache_attention_shared(q.cuda(), *gpu_cache(kc, vc, ks, vs, tables), ints(lens), ints([0, 4]), cu_tokens=cu_of([n] * 4),
+                                         scale=0.125).double().cpu().numpy()
+    assert np.isfinite(got).all()
+    allowed = 2.0 ** -8 * np.abs(want) + 2.0 ** -10 * weight + 1e-6
+    assert (np.abs(got - want) <= allowed).all(), np.max(np.abs(got - want) / allowed)
 
 
 class Scratch:
