@@ -4,7 +4,8 @@
 // Each pair (a, b) of a head's first `rot` channels turns by its token's angle:
 //   a' = a cos - b sin,  b' = b cos + a sin,
 // in fp32 with the error of one product put back (Kahan's a b - c d: within 1.5 units in the last
-// place also where the two terms cancel).  Rotated keys go to the cache's quantisation as they are,
+// place also where the two terms cancel); an infinite product makes the result infinite, or NaN where two
+// cancel.  Rotated keys go to the cache's quantisation as they are,
 // without a rounding to 16 bits between; queries are rounded once.  Quantisation as in
 // kda_kvcache_append.cu; a table of cosines 1 and sines 0 gives its codes bit for bit.
 //
@@ -12,7 +13,7 @@
 // HBM-bound: 2 bytes read and 2 written for a value of q, 2 and 1 for k and v.  The table's rows
 // (4 rot bytes a token, twice a head's values) come from L2; a thread turns several heads of q
 // with the angles it holds, so that they are not read for each: four, two of them loaded at a time, so that
-// four blocks fit an SM (5 prompts of up to 8191 tokens, 32 heads over 8 of 128, bf16: 139 us, 5.0 TB/s, 54% of the
+// four blocks fit an SM (5 prompts of up to 8191 tokens, 32 heads over 8 of 128, bf16: 140.4 us, 5.0 TB/s, 54% of the
 // issue slots; eight heads, four at a time 146, two heads 142; three blocks 151, five 172).  One token a row
 // (256 rows, 64 heads over 8 of 128) takes 7.5 us, a chain of length -> table -> page -> scale -> store; one
 // row 4.8.
@@ -26,7 +27,9 @@ constexpr int kQHeads = 4;  // of a block, for each set of threads that has its 
 constexpr int kStepWarps = 4;
 
 __device__ __forceinline__ float minus_products(float a, float c, float b, float s) {  // a c - b s
-    const float w = __fmul_rn(b, s), e = fmaf(b, s, -w);
+    // (An infinite product has no error to put back: inf - inf would be NaN.  To look at the results instead and work out
+    // again what is NaN spills: 191 us for the prompts above.)
+    const float w = __fmul_rn(b, s), e = fabsf(w) < INFINITY ? fmaf(b, s, -w) : 0.f;
     return __fadd_rn(fmaf(a, c, -w), -e);
 }
 

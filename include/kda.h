@@ -389,7 +389,8 @@ kda_status kda_kvcache_append(const kda_kvcache* cache, const void* k, const voi
  * their token's angles, of which row x of `rotary` has the cosines and then the sines:
  *     a' = a cos - b sin,  b' = b cos + a sin
  * with pair i (i, i + rotary_dim / 2), or with interleaved (2 i, 2 i + 1); the other channels stay.
- * fp32 with an error of at most 2 units in the last place of the result.  Rotated keys are quantised
+ * fp32 with an error of at most 2 units in the last place of the result; infinite values, and products that
+ * overflow fp32, give infinities or, where two cancel or meet a factor of 0, NaN.  Rotated keys are quantised
  * from these fp32 values by the append's rules; queries are rounded once to act_dtype.
  *   q, q_out       device [num_tokens][num_q_heads][head_dim] of act_dtype, token strides in elements
  *                  (multiples of 8), 16-byte aligned.  q_out may be q (with its stride); else it

@@ -10,8 +10,9 @@ import torch
 import chunked_kda_delta_gb300 as K
 import serving_testutil as ref
 import test_logits_gpu as logits
+import test_rotary_gpu as rotary
 from chunked_kda_delta_gb300.kda import KdaKvCache, KdaLogitsRules, KdaScratchAllocator
-from step_testutil import cu_of, ints
+from step_testutil import DT, cu_of, ints, rotary_table, rotate
 from test_shared_attention_gpu import gpu_cache, make_cache
 
 pytestmark = pytest.mark.gpu
@@ -41,6 +42,70 @@ def test_penalties_from_several_threads():
     assert codes == [{0}] * len(jobs)
     for _, _, out, want, _ in jobs:
         assert torch.equal(out, want)
+
+
+def rotated(x, rows, inter):
+    """x [T, H, D] turned by rows in 64 bits, products that leave fp32 infinite."""
+    y = x.astype(np.float64)
+    half = rows.shape[1] // 2
+    with np.errstate(all="ignore"):
+        for i in range(half):
+            a, b = (2 * i, 2 * i + 1) if inter else (i, i + half)
+            c, s = (rows[:, j, None].astype(np.float64) for j in (i, half + i))
+            over = lambda z: np.where(np.abs(z) > np.finfo(np.float32).max, np.copysign(np.inf, z), z)  # noqa: E731
+            y[:, :, a], y[:, :, b] = over(x[:, :, a] * c) - over(x[:, :, b] * s), over(x[:, :, b] * c) + over(x[:, :, a] * s)
+    return y
+
+
+@pytest.mark.parametrize("n", [1, 20])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_infinite_values_are_rotated_to_infinities(n, inter, dtype):
+    # at angles that are not 0, either member of a pair or both; and products past fp32 under a scaled table
+    rng = np.random.default_rng(n)
+    lens, counts, d, rot = [7, 30], [n, n], 64, 64
+    codes, scales, tab, x = rotary.make(rng, lens, counts, 3, 2, d, 16, dtype)
+    i, j = (0, 1) if inter else (0, 32)  # channels of a pair
+    inf = float("inf")
+    x[0, 0, i], x[0, 1, j], x[0, 2, j] = inf, inf, -inf   # queries
+    x[0, 3, j], x[0, 4, i] = inf, -inf                    # keys
+    x[n, 0, i], x[n, 0, j] = inf, inf
+    x[n, 3, i], x[n, 3, j] = inf, -inf
+    rows = rotary_table(64, rot)
+    rows[30:] *= 1.5
+    if dtype == "bf16":
+        x[n, 1, j], x[n, 2, i] = 3e38, -3e38
+        x[n, 4, j] = 3e38
+        rows[30:, [0, rot // 2]] = -1.25, 1.5  # of the first pair: cosine and sine
+    at = rotary.places(lens, counts)
+    dev = rotary.device(codes, scales, tab)
+    q, k, v = x.cuda().split([3, 2, 2], 1)
+    K.kda_get_device_status()
+    out = K.kda_kvcache_append_rotary(q, k, v, torch.as_tensor(rows).cuda(), *dev, ints(lens), cu_tokens=cu_of(counts) if n > 1 else None, interleaved=inter)
+    assert K.kda_get_device_status() == 9
+    want = rotated(x[:, :3].double().numpy(), rows[at], inter)
+    got = out.double().cpu().numpy()
+    assert np.isinf(want).any() and np.isnan(want).any()
+    assert (np.isnan(got) == np.isnan(want)).all()
+    top = float(torch.finfo(DT[dtype]).max)
+    big = np.abs(want) > top * (1 + 2.0 ** -12)
+    assert (got[big] == np.copysign(np.inf, want[big])).all()
+    ok = np.isfinite(want) & (np.abs(want) <= top)
+    eps = torch.finfo(DT[dtype]).eps / 2
+    assert (np.abs(got[ok] - want[ok]) <= (eps + 2.0 ** -21) * np.abs(want[ok]) + 2.0 ** -25).all()
+    # keys: infinities are the largest code, NaN is 0, and neither enters a page's scale
+    want = rotated(x[:, 3:5].double().numpy(), rows[at], inter)
+    got = dev[0].double().cpu().numpy()
+    for token in (0, n):
+        r, pos = token // n, lens[token // n]
+        c = got[tab[r, pos // 16], :, pos % 16]
+        assert (c[np.isposinf(want[token])] == 448).all() and (c[np.isneginf(want[token])] == -448).all() and (c[np.isnan(want[token])] == 0).all()
+    assert np.isinf(want[0]).sum() >= 4
+    fine = np.where(np.isfinite(want), want, 0)
+    for page in np.unique([tab[r, p // 16] for r in range(2) for p in range(lens[r], lens[r] + n)]):
+        mine = [fine[t] for t in range(2 * n) if tab[t // n, at[t] // 16] == page]
+        top = np.maximum(np.abs(mine).max((0, 2)) / 448, 0 if any(at[t] % 16 == 0 for t in range(2 * n) if tab[t // n, at[t] // 16] == page) else scales[0][page])
+        assert (np.abs(dev[2][page].double().cpu().numpy() - top) <= 2.0 ** -21 * top).all()
 
 
 @pytest.mark.parametrize("order", [1, -1, 0])
