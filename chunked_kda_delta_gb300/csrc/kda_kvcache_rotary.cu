@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, kDim * kPage <= 8192 ? 4 : 2) rotary
     const int64_t i = unit - (begin / kPage + 2ll * row);
     const int32_t len = c.lens[row];
     const bool is_q = (int)blockIdx.y >= 2 * c.heads;
-    // (Queries of a row of negative length are turned as if it had none.)
+    // (Tokens of a row of negative length have no pages; their queries are turned by their places from 0 on.)
     if (len < 0 && tid == 0) report(c.status, kStatusBadIndex);
     if (i < 0 || (len < 0 && !is_q)) return;
     const int32_t held = max(len, 0);
@@ -258,14 +258,14 @@ __global__ void __launch_bounds__(kThreads, kDim * kPage <= 8192 ? 4 : 2) rotary
     const int64_t last = min(p0 + kPage, held + (end - begin));
     if (first >= last) return;
     const int n = (int)(last - first), off = (int)(first - p0);
-    const int64_t token0 = begin + first - held;
+    const int64_t token0 = begin + first - held, place0 = first - held + len;
 
     if (is_q) {
         const Item it(j, p.rot, p.interleaved);
         const int head0 = ((int)blockIdx.y - 2 * c.heads) * kQHeads * kSets, head1 = min(p.q_heads, head0 + kQHeads * kSets);
         for (int t = t0; t < n; t += kTokens) {
             const int64_t token = token0 + t;
-            const float* angle_row = table_row(p, token, first + t);
+            const float* angle_row = table_row(p, token, place0 + t);
             const bool turns = it.turns && angle_row;
             Angles angles;
             if (turns) angles.read(angle_row, p.rot, j);

@@ -398,8 +398,8 @@ kda_status kda_kvcache_append(const kda_kvcache* cache, const void* k, const voi
  *   rotary         device fp32 [num_positions][rotary_dim], 16-byte aligned
  *   rotary_dim     multiple of 16, at most head_dim
  *   positions      device int32 [num_tokens]: each token's row of `rotary`; NULL: its place in the
- *                  cache.  Tokens with a position outside of the table are not turned, and recorded as
- *                  KDA_ERR_INVALID_ARGUMENT
+ *                  cache, lens[r] + i for token i of row r.  Tokens with a position outside of the
+ *                  table are not turned, and recorded as KDA_ERR_INVALID_ARGUMENT
  * Tokens without a page are dropped and recorded, their queries turned all the same.  Everything else as
  * kda_kvcache_append. */
 kda_status kda_kvcache_append_rotary(const kda_kvcache* cache, const void* q, const void* k, const void* v,

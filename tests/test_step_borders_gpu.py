@@ -12,7 +12,7 @@ import serving_testutil as ref
 import test_logits_gpu as logits
 import test_rotary_gpu as rotary
 from chunked_kda_delta_gb300.kda import KdaKvCache, KdaLogitsRules, KdaScratchAllocator
-from step_testutil import DT, cu_of, ints, rotary_table, rotate
+from step_testutil import DT, check_quantised, cu_of, ints, rotary_table, rotate
 from test_shared_attention_gpu import gpu_cache, make_cache
 
 pytestmark = pytest.mark.gpu
@@ -241,3 +241,30 @@ def test_nothing_is_shared_with_malformed_offsets(cu, groups):
     begin = np.cumsum([0] + groups)[:-1]
     assert records([cu[r] for r in begin], groups, [0] * len(groups), begin) in got
     assert np.zeros(6, "<i4").tobytes() in got
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("n", [1, 3])
+def test_rows_of_negative_length(n, inter):
+    # their tokens have no pages; queries of places before 0 are outside of the table, those from 0 on are turned
+    rng = np.random.default_rng(n)
+    lens, counts = [20, -2, 5], [n] * 3
+    codes, scales, tab, x = rotary.make(rng, [20, 0, 5], counts, 3, 2, 64, 16, "bf16")
+    rows = rotary_table(40, 64)
+    at = rotary.places(lens, counts)
+    plain = np.concatenate([np.ones((1, 32)), np.zeros((1, 32))], 1).astype(np.float32)
+    for positions in (None, at[::-1].copy() + 2):
+        dev = rotary.device(codes, scales, tab)
+        q, k, v = x.cuda().split([3, 2, 2], 1)
+        K.kda_get_device_status()
+        out = K.kda_kvcache_append_rotary(q, k, v, torch.as_tensor(rows).cuda(), *dev, ints(lens), cu_tokens=cu_of(counts) if n > 1 else None,
+                                          positions=None if positions is None else ints(positions), interleaved=inter)
+        assert K.kda_get_device_status() == 1
+        by = at if positions is None else positions
+        turned = np.where((by < 0)[:, None], plain, rows[np.maximum(by, 0)])
+        y = [rotate(t.double().numpy(), turned, inter) for t in x.split([3, 2, 2], 1)[:2]]
+        rotary.check_q(out, y[0], "bf16")
+        there = [0, 2]
+        keep = np.concatenate([np.arange(r * n, r * n + n) for r in there])
+        check_quantised(y[1][keep], codes[0], dev[0].view(torch.uint8).cpu().numpy(), scales[0], dev[2].cpu().numpy(), tab[there],
+                        [lens[r] for r in there], [n] * 2, 16)
