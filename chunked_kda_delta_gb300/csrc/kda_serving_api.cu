@@ -580,8 +580,9 @@ kda_status kda_logits_penalize(const kda_logits_rules* rules, int64_t rows, int3
         for (const int64_t s : {logits_stride, out_stride})
             if (s < vocab || s > (int64_t)1 << 32)
                 return fail(KDA_ERR_INVALID_ARGUMENT, "logits_stride and out_stride must be at least vocab (got %lld)", (long long)s);
-        if (r.history_width < 0 || r.history_width > (1 << 30) || r.num_bias < 0 || r.num_bias > (1 << 30))
-            return fail(KDA_ERR_INVALID_ARGUMENT, "history_width and num_bias must be in [0, 2^30] (got %d, %d)", r.history_width, r.num_bias);
+        // (A token's count has 30 bits.)
+        if (r.history_width < 0 || r.history_width >= (1 << 30) || r.num_bias < 0 || r.num_bias > (1 << 30))
+            return fail(KDA_ERR_INVALID_ARGUMENT, "history_width must be in [0, 2^30), num_bias in [0, 2^30] (got %d, %d)", r.history_width, r.num_bias);
         const int64_t words = ((int64_t)vocab + 31) / 32;
         if (r.mask && (r.mask_stride < words || r.mask_stride > (int64_t)1 << 32))
             return fail(KDA_ERR_INVALID_ARGUMENT, "mask_stride must be at least %lld (got %lld)", (long long)words, (long long)r.mask_stride);

@@ -503,7 +503,7 @@ kda_status kda_beam_select(int32_t batch, int32_t beams, int32_t vocab, int32_t 
  * Tokens >= vocab and lengths out of range are recorded as KDA_ERR_INVALID_ARGUMENT, the tokens skipped, the
  * lengths taken as the nearest in range; penalties that are not finite, and a repetition that is
  * not above 0, are recorded and the row's three taken as none.
- * vocab, rows, history_width, num_bias <= 2^30. */
+ * vocab, rows, num_bias <= 2^30, history_width < 2^30. */
 typedef struct kda_logits_rules {
     const int32_t* history;
     const int32_t* lens;
