@@ -437,8 +437,11 @@ kda_status kda_kvcache_attention(const kda_kvcache* cache, const void* q, int32_
  * a request or the users of one system prompt: the keys that all rows of a group have in the same pages
  * are gone through once for the whole group.  The result is kda_kvcache_attention's (sums in another
  * order), whatever the groups are: what their rows share is found in the tables, in whole units of 128
- * tokens, as kda_pages_fork leaves it.  Where the sizes say that nothing is to be gained (small tables, as
- * many groups as rows) cu_rows is not read.
+ * tokens, as kda_pages_fork leaves it.  Where the sizes that the host knows say that nothing is to be gained
+ * (tables with few places, as many groups as rows), or that it would take too much scratch, cu_rows is not
+ * read.  What counts there is the tables' width, not the rows' lengths: short rows in wide tables take the
+ * launches for shared prefixes for little (64 groups of 4 rows of 500 keys, 64 heads over 8 of 128, in tables for
+ * 131072: 172 us, with kda_kvcache_attention 74).  With malformed cu_tokens nothing is shared.
  *   cu_rows     device int32 [num_groups + 1] (cu_seqlens rules): group g is rows cu_rows[g] ..
  *               cu_rows[g + 1] - 1; nothing is shared with malformed offsets, which are
  *               recorded where they are read
@@ -495,14 +498,16 @@ kda_status kda_beam_select(int32_t batch, int32_t beams, int32_t vocab, int32_t 
  *     history      int32 [rows][history_width] or NULL: each row's tokens in order, prompt first;
  *                  negative ones are skipped
  *     lens         int32 [rows], tokens of each row's history, or NULL: history_width
- *     prompt_lens  int32 [rows], how many of those are the prompt's, or NULL: none
- *     repetition, presence, frequency  fp32 [rows] or NULL (1, 0, 0)
+ *     prompt_lens  int32 [rows], how many of those are the prompt's (less than 0 counts as none, more than
+ *                  there are as all of them), or NULL: none
+ *     repetition, presence, frequency  fp32 [rows] or NULL (1, 0, 0); a history without any of the three is
+ *                  not read
  *     bias_tokens, bias  int32 and fp32 [rows][num_bias] or NULL; negative tokens are skipped
  *     mask         int32 [rows], mask_stride words each (at least vocab / 32, rounded up), or NULL:
  *                  token t's bit is bit t % 32 of word t / 32
- * Tokens >= vocab and lengths out of range are recorded as KDA_ERR_INVALID_ARGUMENT, the tokens skipped, the
- * lengths taken as the nearest in range; penalties that are not finite, and a repetition that is
- * not above 0, are recorded and the row's three taken as none.
+ * Tokens >= vocab, and lens out of [0, history_width], are recorded as KDA_ERR_INVALID_ARGUMENT, the tokens
+ * skipped, the lengths taken as the nearest in range; penalties that are not finite, and a repetition that
+ * is not above 0, are recorded and the row's three taken as none.
  * vocab, rows, num_bias <= 2^30, history_width < 2^30. */
 typedef struct kda_logits_rules {
     const int32_t* history;

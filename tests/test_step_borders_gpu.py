@@ -268,3 +268,16 @@ def test_rows_of_negative_length(n, inter):
         keep = np.concatenate([np.arange(r * n, r * n + n) for r in there])
         check_quantised(y[1][keep], codes[0], dev[0].view(torch.uint8).cpu().numpy(), scales[0], dev[2].cpu().numpy(), tab[there],
                         [lens[r] for r in there], [n] * 2, 16)
+
+
+def test_histories_without_penalties_are_not_read():
+    x = torch.randn(3, 100, device="cuda")
+    history = torch.full((3, 7), 10 ** 6, dtype=torch.int32, device="cuda")
+    bias_tokens, bias = ints([[5], [6], [7]]), torch.full((3, 1), 2.0, device="cuda")
+    want = x.clone()
+    want[[0, 1, 2], [5, 6, 7]] += 2
+    K.kda_get_device_status()
+    assert torch.equal(K.kda_logits_penalize(x, history=history, lens=ints([8, -1, 7]), bias_tokens=bias_tokens, bias=bias), want)
+    assert K.kda_get_device_status() == 0
+    K.kda_logits_penalize(x, history=history, presence=torch.zeros(3, device="cuda"))
+    assert K.kda_get_device_status() == 1
