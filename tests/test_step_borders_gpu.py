@@ -219,6 +219,57 @@ def private(rows, pages):
     return np.arange(rows * pages).reshape(rows, pages)
 
 
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+def test_what_rows_share_is_found(page):
+    # groups of four rows: what they have in common ends where a table differs, where a row's first new token is, in units of 128
+    n = 1024 // page
+    tables = private(24, n)
+    lens = np.full(24, 1000)
+    for g, common in enumerate([128, 1024, 640, 640, 0, 512]):
+        tables[4 * g: 4 * g + 4, : common // page] = tables[4 * g, : common // page]
+    lens[4:8] = [513, 1000, 600, 514]           # 512 keys before the least row's token
+    lens[8:12] = [512, 1000, 600, 514]          # 511 keys: 384
+    tables[14, 300 // page] = tables[23, n - 1]  # a page of its own among the common ones
+    lens[20:24] = [1, 1000, 1000, 1000]
+    shared = [128, 512, 384, 256, 0, 0]
+    got = found_in_scratch([4] * 6, lens, tables, page, 8, 1)
+    assert records(range(0, 24, 4), [4] * 6, shared, range(0, 24, 4)) in got
+    assert np.repeat(shared, 4).astype("<i4").tobytes() in got
+
+
+@pytest.mark.parametrize("length,shared", [(127, 0), (128, 0), (129, 128), (130, 128), (256, 128), (257, 256)])
+def test_units_of_128_tokens(length, shared):
+    tables = np.tile(private(1, 32), (3, 1))
+    lens = np.array([400, length, 300])
+    got = found_in_scratch([3], lens, tables, 16, 4, 1)
+    assert records([0], [3], [shared], [0]) in got
+    assert np.full(3, shared, "<i4").tobytes() in got
+
+
+def test_rows_that_share():
+    # with up to eight query rows a key/value head three rows share, of more two do
+    tables = np.repeat(private(3, 32), [2, 3, 1], 0)
+    lens = np.full(6, 500)
+    got = found_in_scratch([2, 3, 1], lens, tables, 16, 8, 1)
+    assert records([0, 2, 5], [2, 3, 1], [0, 384, 0], [0, 2, 0]) in got
+    assert np.array([0, 0, 384, 384, 384, 0], "<i4").tobytes() in got
+    got = found_in_scratch([2, 3, 1], lens, tables, 16, 16, 1)
+    assert records([0, 2, 5], [2, 3, 1], [384, 384, 0], [0, 2, 0]) in got
+
+
+def test_rows_without_tokens():
+    tables = np.tile(private(1, 32), (5, 1))
+    tables[1] = -1  # an ended beam
+    lens = np.array([500, 0, 400, 300, 500])
+    got = found_in_scratch([5], lens, tables, 16, 16, 1, counts=6, cu=ints([0, 2, 2, 4, 5, 6]))
+    assert records([0], [6], [256], [0]) in got
+    assert np.full(5, 256, "<i4").tobytes() in got
+    # a first row without tokens; two groups
+    order = [1, 0, 2, 3, 4]
+    got = found_in_scratch([3, 2], lens[order], tables[order], 16, 16, 1, counts=6, cu=ints([0, 0, 2, 4, 5, 6]))
+    assert records([0, 4], [4, 2], [384, 256], [1, 3]) in got
+
+
 @pytest.mark.parametrize("cu_rows", [[0, 3, 5], [1, 3, 6], [0, 7, 6], [0, -1, 6]])
 def test_malformed_groups_share_nothing(cu_rows):
     tables, lens = np.repeat(private(2, 32), 3, 0), np.full(6, 500)
@@ -281,3 +332,22 @@ def test_histories_without_penalties_are_not_read():
     assert K.kda_get_device_status() == 0
     K.kda_logits_penalize(x, history=history, presence=torch.zeros(3, device="cuda"))
     assert K.kda_get_device_status() == 1
+
+
+def test_calls_repeat_themselves():
+    # the same bits in every call: no order of sums is left to chance
+    rng = np.random.default_rng(9)
+    groups = [[(0, 3000), (2900, 2950), (2900, 2999)], [(0, 700), (640, 690), (640, 720)]]
+    cache = make_cache(rng, groups, 16, 2, 128)
+    lens = ints(cache[5])
+    dev = gpu_cache(*cache[:5])
+    for n, hq in ((1, 8), (1, 32), (40, 16)):
+        q = torch.randn(6 * n, hq, 128, device="cuda").bfloat16()
+        call = lambda: K.kda_kvcache_attention_shared(q, *dev, lens, ints([0, 3, 6]), cu_tokens=cu_of([n] * 6))  # noqa: E731
+        want = call()
+        assert all(torch.equal(call(), want) for _ in range(50))
+    made = logits.make(rng, 20, 50257, width=3000, biases=600, mask=0.9)
+    made["bias_tokens"] %= 50
+    x = torch.randn(20, 50257, device="cuda")
+    want = logits.call(x, made)
+    assert all(torch.equal(logits.call(x, made), want) for _ in range(20))
