@@ -334,6 +334,45 @@ def test_histories_without_penalties_are_not_read():
     assert K.kda_get_device_status() == 1
 
 
+def check_logits(got, x, rules, dtype, adds=0):
+    """As in tests/test_logits_gpu.py, with NaN as wrong as any other value."""
+    want, size, touched = logits.reference(x.double().numpy().reshape(-1, x.shape[-1]), rules)
+    assert got.shape == x.shape
+    wrong_logits(got.cpu().reshape(want.shape), x.reshape(want.shape), want, size, touched, dtype, adds)
+
+
+def wrong_logits(got, x, want, size, touched, dtype, adds):
+    g, masked = got.double().numpy(), np.isneginf(want)
+    assert np.isneginf(g[masked]).all()
+    same = torch.as_tensor(~touched & ~masked)
+    assert torch.equal(got[same], x[same])
+    ok = touched & ~masked
+    allowed = torch.finfo(DT[dtype]).eps / 2 * np.abs(want) + (4 + adds) * 2.0 ** -23 * size + (2.0 ** -24 if dtype == "fp16" else 0)
+    with np.errstate(invalid="ignore"):
+        assert (np.abs(g - want) <= allowed)[ok].all()
+
+
+@pytest.mark.parametrize("vocab", [1, 33, 500, 32001, 70000])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("place", [False, True])
+@pytest.mark.parametrize("rules", [dict(width=100, biases=33, mask=0.6), dict(width=5000, lens=False), dict(biases=700), dict(width=6000, biases=10, mask=0.9)])
+def test_penalised_logits_are_numbers(vocab, dtype, place, rules):
+    rng = np.random.default_rng(vocab)
+    made = logits.make(rng, 6, vocab, **rules)
+    x = torch.as_tensor(rng.standard_normal((2, 3, vocab)) * 5).to(DT[dtype])
+    y = x.cuda()
+    check_logits(logits.call(y, made, out=y if place else None), x, made, dtype, adds=rules.get("biases", 0))
+
+
+def test_large_vocabularies_are_numbers():
+    rng = np.random.default_rng(4)
+    rows, vocab = 300, 600_001
+    made = logits.make(rng, rows, vocab, width=50, biases=3, mask=0.9)
+    x = torch.randn(rows, vocab, device="cuda").to(torch.bfloat16)
+    got, some = logits.call(x, made), [0, 1, 150, 298, 299]
+    check_logits(got[some], x[some].cpu(), {k: v[some] for k, v in made.items()}, "bf16", adds=3)
+
+
 def test_calls_repeat_themselves():
     # the same bits in every call: no order of sums is left to chance
     rng = np.random.default_rng(9)
