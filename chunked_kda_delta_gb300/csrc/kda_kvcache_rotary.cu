@@ -7,7 +7,8 @@
 // place also where the two terms cancel); an infinite product makes the result infinite, or NaN where two
 // cancel.  Rotated keys go to the cache's quantisation as they are,
 // without a rounding to 16 bits between; queries are rounded once.  Quantisation as in
-// kda_kvcache_append.cu; a table of cosines 1 and sines 0 gives its codes bit for bit.
+// kda_kvcache_append.cu; for finite values a table of cosines 1 and sines 0 gives its codes, but for the sign of
+// zeros (a' is +0 for a = -0 and b < 0).
 //
 // A thread has an item: the 16 channels of eight pairs, with their eight cosines and sines.
 // HBM-bound: 2 bytes read and 2 written for a value of q, 2 and 1 for k and v.  The table's rows

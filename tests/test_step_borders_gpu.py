@@ -321,6 +321,28 @@ def test_rows_of_negative_length(n, inter):
                         [lens[r] for r in there], [n] * 2, 16)
 
 
+@pytest.mark.parametrize("n", [1, 45])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("inter", [False, True])
+def test_angles_of_zero_give_the_appends_values(n, dtype, inter):
+    # with zeros of both signs beside partners of both signs: equal but for the sign of zero
+    rng = np.random.default_rng(n)
+    lens, counts = [0, 7, 30], [n] * 3
+    codes, scales, tab, x = rotary.make(rng, lens, counts, 3, 2, 128, 32, dtype)
+    x[torch.as_tensor(rng.random(x.shape) < 0.3)] = 0.0
+    x[torch.as_tensor(rng.random(x.shape) < 0.3)] = -0.0
+    one = torch.cat([torch.ones(128, 32), torch.zeros(128, 32)], 1).cuda()
+    a, b = rotary.device(codes, scales, tab), rotary.device(codes, scales, tab)
+    q, k, v = x.cuda().split([3, 2, 2], 1)
+    cu = cu_of(counts) if n > 1 else None
+    out = K.kda_kvcache_append_rotary(q, k, v, one, *a, ints(lens), cu_tokens=cu, interleaved=inter)
+    K.kda_kvcache_append(k, v, *b, ints(lens), cu_tokens=cu)
+    assert (out == q).all()
+    for s, t in zip(a[:4], b[:4]):
+        assert (s.float() == t.float()).all()
+    assert torch.equal(a[1].view(torch.uint8), b[1].view(torch.uint8))  # values are not turned
+
+
 def test_histories_without_penalties_are_not_read():
     x = torch.randn(3, 100, device="cuda")
     history = torch.full((3, 7), 10 ** 6, dtype=torch.int32, device="cuda")
