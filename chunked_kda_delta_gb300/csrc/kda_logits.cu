@@ -580,8 +580,8 @@ cudaError_t launch_type(LogitsParams& p, cudaStream_t stream) {
         p.direct = !hashed || len <= (int64_t)1 << log;
         p.entries = p.direct ? (int32_t)len : 1 << log;
     }
-    // Through the ring where a segment has more than a chunk (16 rows of 50257 fp32 with 32768 tokens each, 12 KB
-    // a segment: 16.6 us through it, 15.3 through registers) and rows of out have the boundaries of the logits'.
+    // Through the ring where a segment has more than a chunk (16 rows of 50257 fp32 with 32768 tokens each, 16 KB
+    // a segment, so just not: 16.6 us through it, 15.3 through registers) and rows of out have the boundaries of the logits'.
     const bool ring = !place && len * (int64_t)sizeof(T) > kChunkBytes && (((uintptr_t)p.out ^ (uintptr_t)p.logits) & 15) == 0 && (p.rows == 1 || ((p.out_stride ^ p.stride) * sizeof(T) & 15) == 0);
     const auto kernel = ring ? (touches ? penalize_kernel<T, true, true> : penalize_kernel<T, true, false>)
                              : (touches ? penalize_kernel<T, false, true> : penalize_kernel<T, false, false>);
