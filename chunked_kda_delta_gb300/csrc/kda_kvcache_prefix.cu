@@ -29,7 +29,7 @@
 // for 1024 cycles (codes in, out, operands in, K and V by the matrix instructions); it takes 1250.  For wider ones the
 // softmax's instructions with 1536 cycles of shared memory behind them; 2600.  8 groups of 8 rows and
 // 8 key/value heads with 8 query heads each, 16384 keys, take 84 us (29% of the tensor pipes, 45% of the issue slots), one
-// of 64 rows, 32768 keys, 88 (38%, 50%); 10 to 15 us of it are an item's beginning, a chain of loads (table, codes, scales, q, 2 to 3 us each while all CTAs
+// of 64 rows, 32768 keys, 86 (40%, 52%); 10 to 15 us of it are an item's beginning, a chain of loads (table, codes, scales, q, 2 to 3 us each while all CTAs
 // begin), and its part's way out.
 //
 // Work split: the CTAs take equal contiguous shares of all tiles of all items, an item of 256 rows counted

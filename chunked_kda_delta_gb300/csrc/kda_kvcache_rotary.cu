@@ -14,7 +14,7 @@
 // HBM-bound: 2 bytes read and 2 written for a value of q, 2 and 1 for k and v.  The table's rows
 // (4 rot bytes a token, twice a head's values) come from L2; a thread turns several heads of q
 // with the angles it holds, so that they are not read for each: four, two of them loaded at a time, so that
-// four blocks fit an SM (5 prompts of up to 8191 tokens, 32 heads over 8 of 128, bf16: 140.4 us, 5.0 TB/s, 54% of the
+// four blocks fit an SM (5 prompts of up to 8191 tokens, 32 heads over 8 of 128, bf16: 140.4 us, 5.0 TB/s, 60% of the
 // issue slots; eight heads, four at a time 146, two heads 142; three blocks 151, five 172).  One token a row
 // (256 rows, 64 heads over 8 of 128) takes 7.5 us, a chain of length -> table -> page -> scale -> store; one
 // row 4.8.
